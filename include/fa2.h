@@ -343,6 +343,91 @@ FA2_API int fa2_bwd_sched(const void* Q, const void* K, const void* V, const voi
                   void* workspace, size_t workspace_bytes, int schedule, struct CUstream_st* stream);
 
 /*
+ * fa2_qk_norm_rope_fwd — RMS norm of every query and key head and the
+ * position rotation, in one pass: what a program runs between its projection
+ * and fa2_fwd. The pages have no counterpart to this entry point.
+ *
+ * For every row x (one head of one token, D elements) of q and of k:
+ *   y = x / sqrt(mean(x^2) + eps) * gain
+ *   the first `rot` elements of y are then rotated in pairs by the angles of
+ *   the token's position: (a, b) -> (a cos - b sin, b cos + a sin), the
+ *   pairs being (y[i], y[i + rot/2]), or (y[2i], y[2i+1]) when interleaved
+ * computed in 32 bits and rounded once, to nearest-even.
+ *
+ * q, k      : device pointers, [B, Hq, N, D] and [B, Hkv, N, D] views of
+ *             `dtype` with the strides below; either may be NULL with its
+ *             head count 0.
+ * q_gain, k_gain: device pointers, D elements (fp32 when gain_f32 is nonzero,
+ *             else `dtype`), or NULL for a gain of one.
+ * cos, sin  : device pointers, contiguous [table_rows, rot/2] fp32 tables,
+ *             16-byte aligned; unused (may be NULL) when rot is 0.
+ * positions : device pointer, the row of the tables for each token, [B, N]
+ *             int32 (or int64 when positions_64 is nonzero) with the strides
+ *             below; NULL: the token's index n (table_rows >= N then). A
+ *             position outside [0, table_rows) reads nothing: the rotated
+ *             elements of its rows come out as NaN.
+ * q_out, k_out: device pointers, views of q's and k's shape; fully
+ *             overwritten. Each may be exactly its own input (same address
+ *             and strides); apart from that an output overlaps no input and
+ *             no other output. Views that interleave (heads of one packed
+ *             buffer) do not overlap.
+ * strides   : HOST pointer to 14 element strides: batch, head and token of q,
+ *             k, q_out, k_out in turn, then batch and token of positions;
+ *             NULL: every view contiguous, positions [B, N]. A head's D
+ *             elements are always contiguous; strides of dimensions longer
+ *             than 1 are multiples of 8 and not negative, at most 2^40.
+ * B, Hq, Hkv, N: sizes >= 0; nothing happens when there are no rows.
+ * D         : 32, 64, 96, 128, 256, 512 or 1024.
+ * rot       : rotated elements, a multiple of 16, 0 <= rot <= D.
+ * eps       : finite, >= 0.
+ *
+ * Asynchronous and allocation-free as fa2_fwd; tensor pointers are 16-byte
+ * aligned. Errors as fa2_fwd (FA2_ERR_UNSUPPORTED also for a rot that is not
+ * a multiple of 16).
+ */
+FA2_API int fa2_qk_norm_rope_fwd(const void* q, const void* k, const void* q_gain, const void* k_gain,
+                                 const float* cos, const float* sin, const void* positions, void* q_out, void* k_out,
+                                 const long long* strides, int B, int Hq, int Hkv, int N, int D, int rot,
+                                 int table_rows, float eps, int interleaved, int gain_f32, int positions_64,
+                                 int dtype, struct CUstream_st* stream);
+
+/*
+ * fa2_qk_norm_rope_bwd_workspace_bytes — bytes of device workspace
+ * fa2_qk_norm_rope_bwd needs for head dimension D: the blocks' partial sums
+ * of the gain gradients (1280 rows of D floats), whatever the other sizes.
+ * Returns FA2_OK, FA2_ERR_INVALID_ARG (bytes NULL) or FA2_ERR_UNSUPPORTED.
+ */
+FA2_API int fa2_qk_norm_rope_bwd_workspace_bytes(int D, size_t* bytes);
+
+/*
+ * fa2_qk_norm_rope_bwd — the gradient of fa2_qk_norm_rope_fwd: dq, dk and the
+ * gains' gradients for upstream gradients dq_out, dk_out of its outputs. The
+ * norms are computed again from q and k, so the forward saves nothing.
+ *
+ * dq_out, dk_out, q, k, dq, dk: device pointers, views as above. dq (dk) is
+ *             fully overwritten and may be exactly dq_out or q (dk_out or k);
+ *             apart from that an output overlaps nothing.
+ * dq_gain, dk_gain: device pointers, D elements of the gains' type, fully
+ *             overwritten with the sums over all rows (fp32 sums in a fixed
+ *             order, rounded once): present exactly where q_gain (k_gain) is.
+ *             A row with a position outside the tables makes them NaN.
+ * strides   : HOST pointer to 20 element strides: dq_out, dk_out, q, k, dq,
+ *             dk (batch, head, token each), then positions; NULL as above.
+ * workspace : device memory of at least
+ *             fa2_qk_norm_rope_bwd_workspace_bytes(D) bytes, 16-byte aligned,
+ *             overlapping nothing; scratch, not shared by calls that run at
+ *             the same time. Unused (may be NULL) without gains.
+ * The other arguments and the errors are fa2_qk_norm_rope_fwd's. Without any
+ * row the gains' gradients are zeros.
+ */
+FA2_API int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                 const void* q_gain, const void* k_gain, const float* cos, const float* sin,
+                                 const void* positions, void* dq, void* dk, void* dq_gain, void* dk_gain,
+                                 const long long* strides, int B, int Hq, int Hkv, int N, int D, int rot,
+                                 int table_rows, float eps, int interleaved, int gain_f32, int positions_64,
+                                 int dtype, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
  * fa2_device_status — read the device-side watchdog word of the current
  * device, synchronising `stream` first. *status receives 0 when no kernel of
  * this library has timed out waiting on one of its internal barriers since
