@@ -61,6 +61,12 @@ SIGNATURES = {
     "fa2_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "fa2_qk_norm_rope_bwd": (ctypes.c_int, [_VP] * 14 + [ctypes.c_int] * 7 + [ctypes.c_float] + [ctypes.c_int] * 4 +
                              [_VP, ctypes.c_size_t, _VP]),
+    "fa2_cross_fwd": (ctypes.c_int, [_VP] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _VP,
+                                                                      ctypes.c_size_t, _VP]),
+    "fa2_cross_fwd_workspace_bytes": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "fa2_cross_bwd": (ctypes.c_int, [_VP] * 10 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _VP,
+                                                                       ctypes.c_size_t, _VP]),
+    "fa2_cross_bwd_workspace_bytes": (ctypes.c_int, [ctypes.c_int] * 6 + [ctypes.POINTER(ctypes.c_size_t)]),
     "fa2_device_status": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_int), ctypes.c_int]),
     "fa2_set_watchdog_ns": (ctypes.c_int, [ctypes.c_ulonglong]),
     "fa2_test_withhold_next_load": (ctypes.c_int, [ctypes.c_int]),

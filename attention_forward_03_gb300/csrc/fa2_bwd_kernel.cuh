@@ -147,7 +147,9 @@ struct BwdLayout {
   // p_free, dq_full, dq_free, acc_full, acc_free, drain, dqs_ready[2], dqs_free[2], drain2, part_done
   static constexpr int kNumBars = 2 + 2 * kStages + 15;
   static constexpr int kMisc = kBars + kNumBars * 8;
+  static constexpr int kCrossStart = kMisc + 16;        // cross attention: CrossStart
   static constexpr int kSmemBytes = kMisc + 16 + 1024;  // + slack for 1 KB alignment
+  static constexpr int kCrossSmemBytes = kSmemBytes + sizeof(CrossStart);
   static constexpr uint32_t kColDV = 0;
   static constexpr uint32_t kColDK = kDp;
   static constexpr uint32_t kColS = 2 * kDp;
@@ -181,7 +183,8 @@ struct BwdLayout {
   static_assert(kGradATmem || kDqRows, "P^T has tensor-memory columns at every step height");
   static_assert(kColPT + kSR / 2 <= kTmemCols, "TMEM budget");
   static_assert(!kGradATmem || kColDST + kSR / 2 <= kTmemCols, "TMEM budget");
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kCrossSmemBytes <= 232448, "shared memory budget");
+  static_assert(kCrossStart % alignof(CrossStart) == 0, "alignment");
   static_assert(kRing % 1024 == 0 && kDS % 1024 == 0, "swizzled tiles need 1 KB alignment");
 };
 
@@ -286,12 +289,19 @@ __device__ __forceinline__ bool bwd_next_segment(BwdCursor& c, BwdSegment& s, co
   return true;
 }
 
-template <int D, bool kBf16, bool kCausal>
+// kCross: cross attention (fa2_cross.h). The differences: the walk (a batch
+// entry has as many K/V tiles as its keys fill), keys and queries of
+// different lengths, and rows of K behind the keys zeroed before dQ reads
+// them (their dS is zero, but what lies there can be a NaN).
+template <int D, bool kBf16, bool kCausal, bool kCross = false>
 __global__ void __launch_bounds__(bwd_threads(D), 1)
     fa2_bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
-                   const __grid_constant__ CUtensorMap tmDQ, const BwdParams p) {
+                   const __grid_constant__ CUtensorMap tmDQ,
+                   const std::conditional_t<kCross, CrossBwdParams, BwdParams> p) {
+  static_assert(!(kCross && kCausal), "cross attention has no causal mask");
   using L = BwdLayout<D>;
+  using Seg = std::conditional_t<kCross, CrossBwdSegment, BwdSegment>;
   constexpr bool kTwoIssuers = true;
   constexpr bool kATmem = L::kGradATmem;  // dS^T in TMEM for dK (P^T is there for dV at every D)
   constexpr bool kDqWarp = bwd_threads(D) > 352;  // staged dQ^T added by warp kBwdDqWarp
@@ -332,6 +342,23 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+
+  // The walk over this CTA's segments.
+  [[maybe_unused]] CrossStart* const start = reinterpret_cast<CrossStart*>(smem + L::kCrossStart);
+  if constexpr (kCross) {
+    if (warp == 0) {
+      const CrossStart st = cross_bwd_start(p);
+      if (lane == 0) *start = st;
+    }
+  }
+  auto first_segment_cursor = [&]() {
+    if constexpr (kCross) return cross_bwd_first_cursor(p, *start);
+    else return bwd_first_cursor(p);
+  };
+  auto advance = [&](auto& c, Seg& s) -> bool {
+    if constexpr (kCross) return cross_bwd_next_segment(c, s, p);
+    else return bwd_next_segment<kCausal, L::kR>(c, s, p);
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(bar_kv_full, 1);
@@ -387,9 +414,9 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       int slot = 0;
       uint32_t ph = 0, units = 0, loads = 0;
       bool ok = true;
-      BwdCursor cur = bwd_first_cursor(p);
-      BwdSegment sg;
-      while (ok && bwd_next_segment<kCausal, L::kR>(cur, sg, p)) {
+      auto cur = first_segment_cursor();
+      Seg sg;
+      while (ok && advance(cur, sg)) {
         const int bh = sg.bh, kv = sg.kv;
         if (units > 0 && !wait_bounded(bar_kv_empty, (units - 1) & 1u, wd, kSiteBwdKvEmpty, true, kNapNs)) {
           ok = false;
@@ -496,11 +523,17 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       // 64-row M panels 16 KB apart; at D = 64 the second panel is the V
       // tile and its rows are discarded), B = dS^T MN-major (N = SR query
       // columns, panels of 64 16 KB apart), 8 steps of 16 keys.
-      auto issue_dq = [&]() {
+      // Cross attention: only the steps with keys.
+      auto issue_dq = [&]([[maybe_unused]] const Seg& sgm) {
+        [[maybe_unused]] int key_steps = kBwdKeys / 16;
+        if constexpr (kCross) key_steps = cross_key_steps(sgm.n_keys - sgm.kv * kBwdKeys);
         const uint32_t kt_lo = desc_lo_sw128(sK, kPanelBytes);
         const uint32_t ds_mn = desc_lo_sw128(sDS, kPanelBytes);
 #pragma unroll
         for (int kk = 0; kk < kBwdKeys / 16; ++kk) {
+          if constexpr (kCross) {
+            if (kk >= key_steps) break;
+          }
           const uint32_t off = static_cast<uint32_t>((kk * 16 * 128) >> 4);
           if constexpr (L::kDqRows)  // dQ = dS K: A = dS^T's rows read MN-major (M = queries), B = K MN-major
             mma_ss_w(tmem + L::kColDQ, ds_mn + off, kHi, kt_lo + off, kHi, idesc_dqr, kk > 0 ? 1u : 0u);
@@ -519,13 +552,17 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         uint32_t g = 0;
         uint32_t units = 0;
         bool ok = true;
-        BwdCursor cur = bwd_first_cursor(p);
-        BwdSegment sg;
-        while (ok && bwd_next_segment<kCausal, L::kR>(cur, sg, p)) {
+        auto cur = first_segment_cursor();
+        Seg sg;
+        while (ok && advance(cur, sg)) {
           const int n_steps = sg.i_end - sg.i_begin;
           if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
             ok = false;
             break;
+          }
+          if constexpr (kCross) {
+            if (scores && sg.n_keys < p.Nk && sg.n_keys - sg.kv * kBwdKeys < kBwdKeys)
+              cross_zero_rows(sK, L::kPanels, sg.n_keys - sg.kv * kBwdKeys);
           }
           for (int t = 0; t < n_steps; ++t, ++g) {
             if (!wait_bounded(bar_stage_full(slot), ph, wd, kSiteBwdStageFull, true, 0u)) {
@@ -559,7 +596,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
                 break;
               }
               tc_fence_after_sync();
-              issue_dq();
+              issue_dq(sg);
               mma_commit(bar_p_free);
               mma_commit(bar_dq_full);
             }
@@ -594,9 +631,9 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           }
           return s;
         };
-        BwdCursor wcur = bwd_first_cursor(p);
-        BwdSegment sg;
-        while (ok && bwd_next_segment<kCausal, L::kR>(wcur, sg, p)) {
+        auto wcur = first_segment_cursor();
+        Seg sg;
+        while (ok && advance(wcur, sg)) {
           const int n_steps = sg.i_end - sg.i_begin;
           if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
             ok = false;
@@ -636,7 +673,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
               break;
             }
             tc_fence_after_sync();
-            issue_dq();
+            issue_dq(sg);
             mma_commit(bar_p_free);
             mma_commit(bar_dq_full);
             cur = nxt;
@@ -780,12 +817,21 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       return true;
     };
 
-    BwdCursor cur = bwd_first_cursor(p);
-    BwdSegment sg;
-    while (ok && bwd_next_segment<kCausal, L::kR>(cur, sg, p)) {
+    auto cur = first_segment_cursor();
+    Seg sg;
+    while (ok && advance(cur, sg)) {
       const int bh = sg.bh, kv = sg.kv;
       const int key = kv * kBwdKeys + rr;
-      const bool key_ok = key < p.N;
+      bool key_ok, key_row;  // a key; a row of dK and dV
+      int key_rows;          // rows of K, V, dK, dV per head
+      if constexpr (kCross) {
+        key_ok = key < sg.n_keys;
+        key_row = key < p.Nk;
+        key_rows = p.Nk;
+      } else {
+        key_ok = key_row = key < p.N;
+        key_rows = p.N;
+      }
       for (int i = sg.i_begin; i < sg.i_end; ++i, ++g) {
         bool got = wait_bounded(bar_s_full, g & 1u, wd, kSiteBwdSFull);
         got = got && wait_bounded(bar_stage_full(slot), ph, wd, kSiteBwdStageFull);
@@ -835,6 +881,12 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
             pk[j / 2 + 1] = pack2(pr[2], pr[3], kBf16);
             dk[j / 2] = pack2(ds[0], ds[1], kBf16);
             dk[j / 2 + 1] = pack2(ds[2], ds[3], kBf16);
+          }
+          if constexpr (kCross) {  // dP of a row behind the keys is anything
+            if (!key_ok) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) dk[j] = 0u;
+            }
           }
           // the previous step's P^T / dS^T must have been read by the tensor core
           if (h == 0 && g > 0) {
@@ -888,7 +940,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       constexpr int kMy = L::kChunksWg;
       const int c0 = wg * kMy;
       const int n_my = min(kMy, L::kChunks - c0);  // warp-uniform
-      const size_t out_row = (static_cast<size_t>(bh) * p.N + (key_ok ? key : 0)) * (D * 2);
+      const size_t out_row = (static_cast<size_t>(bh) * key_rows + (key_row ? key : 0)) * (D * 2);
       // Writes 32 columns (chunk c) of this key row of dV and dK (dK scaled).
       auto store_chunk = [&](int c, const float (&a)[32], const float (&b)[32]) {
         uint4* dvp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dv) + out_row + c * 64);
@@ -896,6 +948,12 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         const float sc = p.scale;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          if constexpr (kCross) {  // a row behind the keys: zero whatever dO and Q hold
+            if (!key_ok) {
+              dvp[q] = dkp[q] = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+          }
           const float* x = a + 8 * q;
           const float* y = b + 8 * q;
           dvp[q] = make_uint4(pack2(x[0], x[1], kBf16), pack2(x[2], x[3], kBf16), pack2(x[4], x[5], kBf16),
@@ -904,7 +962,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
                               pack2(y[4] * sc, y[5] * sc, kBf16), pack2(y[6] * sc, y[7] * sc, kBf16));
         }
       };
-      if (p.stream_k && sg.i_begin > bwd_first_step<kCausal, L::kR>(kv)) {
+      if (p.stream_k && sg.i_begin > (kCross ? 0 : bwd_first_step<kCausal, L::kR>(kv))) {
         // Not the unit's first steps: hand this CTA's partial dV, dK to the
         // unit's owner through its workspace slot ([2][D][128], column-major
         // so that a warp's stores are contiguous), 32 columns at a time.
@@ -943,7 +1001,11 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         // rest of its steps, in CTA order (a fixed order: dV and dK do not
         // depend on timing), 32 columns at a time, then write dV and dK.
         int last_c = blockIdx.x;
-        while (last_c + 1 < static_cast<int>(gridDim.x) && bwd_share_begin(p, last_c + 1) < sg.unit_end) ++last_c;
+        if constexpr (kCross) {
+          while (last_c + 1 < start->shares && cross_share_begin(*start, last_c + 1) < sg.unit_end) ++last_c;
+        } else {
+          while (last_c + 1 < static_cast<int>(gridDim.x) && bwd_share_begin(p, last_c + 1) < sg.unit_end) ++last_c;
+        }
         bool fine = true;
         for (int cb = blockIdx.x + 1; cb <= last_c && fine; ++cb)
           fine = wait_flag(p.ws_flags + cb, p.epoch, wd, kSiteBwdPartFlag);
@@ -973,7 +1035,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
               fb[i] += __ldcg(pkk + i * 128);
             }
           }
-          if (key_ok) store_chunk(c, fa, fb);
+          if (key_row) store_chunk(c, fa, fb);
         }
         tc_fence_before_sync();
         mbar_arrive(bar_acc_free);
@@ -992,7 +1054,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       }
       tc_fence_before_sync();
       mbar_arrive(bar_acc_free);
-      if (key_ok) {
+      if (key_row) {
 #pragma unroll
         for (int c = 0; c < kMy; ++c) {
           if (c < n_my)
@@ -1018,9 +1080,9 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       const uint32_t rows = sDQS + static_cast<uint32_t>(w * L::kCW * D * 4);
       uint32_t k = 0;  // steps whose rows were added
       bool ok = true;
-      BwdCursor cur = bwd_first_cursor(p);
-      BwdSegment sg;
-      while (ok && bwd_next_segment<kCausal, L::kR>(cur, sg, p)) {
+      auto cur = first_segment_cursor();
+      Seg sg;
+      while (ok && advance(cur, sg)) {
         for (int i = sg.i_begin; i < sg.i_end; ++i, ++k) {
           ok = wait_bounded(bar_dqs_ready(w), k & 1u, wd, kSiteBwdDqsReady, true, 0u);
           if (!ok) break;
@@ -1049,11 +1111,11 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
   }
 }
 
-template <int D, bool kBf16, bool kCausal>
-cudaError_t launch_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,
-                       const CUtensorMap& dq_acc, const BwdParams& p, int grid, cudaStream_t stream) {
-  auto kern = fa2_bwd_kernel<D, kBf16, kCausal>;
-  const int smem = BwdLayout<D>::kSmemBytes;
+template <int D, bool kBf16, bool kCausal, bool kCross, typename P>
+cudaError_t launch_bwd_kernel(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,
+                              const CUtensorMap& dq_acc, const P& p, int grid, cudaStream_t stream) {
+  auto kern = fa2_bwd_kernel<D, kBf16, kCausal, kCross>;
+  const int smem = kCross ? BwdLayout<D>::kCrossSmemBytes : BwdLayout<D>::kSmemBytes;
   // Once per device: the shared-memory opt-in.
   static PerDeviceOnce prepared;
   const cudaError_t e = once_per_device(
@@ -1072,6 +1134,18 @@ cudaError_t launch_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtenso
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, k, v, q, dout, dq_acc, p);
+}
+
+template <int D, bool kBf16, bool kCausal>
+cudaError_t launch_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,
+                       const CUtensorMap& dq_acc, const BwdParams& p, int grid, cudaStream_t stream) {
+  return launch_bwd_kernel<D, kBf16, kCausal, false>(k, v, q, dout, dq_acc, p, grid, stream);
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_cross_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,
+                             const CUtensorMap& dq_acc, const CrossBwdParams& p, int grid, cudaStream_t stream) {
+  return launch_bwd_kernel<D, kBf16, false, true>(k, v, q, dout, dq_acc, p, grid, stream);
 }
 
 }  // namespace fa2

@@ -1,0 +1,225 @@
+// The work-unit walks of cross attention on the forward and backward kernels
+// (fa2_kernel.cuh, fa2_bwd_kernel.cuh): as next_segment in fa2_fwd_common.cuh
+// and bwd_next_segment, with the number of K/V tiles depending on the batch
+// entry's key count, which only the device knows.
+//
+// In the forward a batch entry without keys counts as one tile of masked keys: its rows then
+// run the ordinary path and come out as O = 0, LSE = +inf.
+#pragma once
+#include "fa2_cross.h"
+#include "fa2_fwd_common.cuh"
+
+namespace fa2 {
+
+struct CrossSegment : Segment {
+  int n_keys;  // keys of the unit's batch entry
+};
+
+// Where this CTA's stream-K share begins, found once per CTA.
+struct CrossStart {
+  long long total;    // K/V-tile steps of the whole call
+  long long b_start;  // first step of batch entry b
+  int b;              // batch entry that holds the share's first step
+  int shares;         // CTAs with a share: min(grid, total)
+};
+
+struct CrossCursor {
+  int round;
+  int b;
+  long long step, end, b_start;
+};
+
+__device__ __forceinline__ int cross_tiles(int n_keys) { return max(1, (n_keys + kKeys - 1) / kKeys); }
+
+__device__ __forceinline__ long long cross_batch_steps(const CrossParams& p, int b) {
+  return static_cast<long long>(p.heads) * p.n_qt * cross_tiles(cross_keys(p, b));
+}
+
+__device__ __forceinline__ long long cross_share_begin(const CrossStart& st, int c) {
+  return c >= st.shares ? st.total : st.total * c / st.shares;
+}
+
+// By one whole warp: the total, then the batch entry of this CTA's first step
+// (32 entries at a time: a shuffle scan of their steps). `steps(b)` are the
+// steps of batch entry b, the same for all entries when `uniform`.
+template <typename F>
+__device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, F&& steps) {
+  CrossStart st;
+  const int lane = threadIdx.x & 31;
+  if (uniform) {
+    const long long per = steps(0);
+    st.total = per * B;
+    st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), st.total));
+    st.b = static_cast<int>(min(cross_share_begin(st, blockIdx.x) / per, static_cast<long long>(B - 1)));
+    st.b_start = per * st.b;
+    return st;
+  }
+  long long sum = 0;
+  for (int b = lane; b < B; b += 32) sum += steps(b);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  st.total = sum;
+  st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), st.total));
+  st.b = 0;
+  st.b_start = 0;
+  const long long want = cross_share_begin(st, blockIdx.x);
+  long long before = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    const long long mine = b < B ? steps(b) : 0;
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, b < B && before + upto > want);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      st.b = b0 + l;
+      st.b_start = before + __shfl_sync(0xffffffffu, upto - mine, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return st;
+}
+
+// The forward's start; the round schedule needs none.
+__device__ __forceinline__ CrossStart cross_fwd_start(const CrossParams& p) {
+  if (!p.stream_k) return CrossStart{0, 0, 0, 0};
+  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_batch_steps(p, b); });
+}
+
+__device__ __forceinline__ CrossCursor cross_first_cursor(const CrossParams& p, const CrossStart& st) {
+  CrossCursor c;
+  c.round = 0;
+  c.b = st.b;
+  c.b_start = st.b_start;
+  c.step = p.stream_k ? cross_share_begin(st, blockIdx.x) : 0;
+  c.end = p.stream_k ? cross_share_begin(st, blockIdx.x + 1) : 0;
+  return c;
+}
+
+// Next segment of this CTA. Every role walks the same sequence.
+__device__ __forceinline__ bool cross_next_segment(CrossCursor& c, CrossSegment& s, const CrossParams& p) {
+  if (!p.stream_k) {
+    const int u = c.round++ * gridDim.x + blockIdx.x;
+    if (u >= p.num_units || u < 0) return false;
+    s.bh = u / p.n_qt;
+    s.q0 = (u - s.bh * p.n_qt) * kSubTiles * kRows;
+    s.n_keys = cross_keys(p, s.bh / p.heads);
+    s.nkv = cross_tiles(s.n_keys);
+    s.kv_begin = 0;
+    s.kv_end = s.nkv;
+    s.unit_end = 0;
+    return true;
+  }
+  if (c.step >= c.end) return false;
+  for (;;) {
+    s.n_keys = cross_keys(p, c.b);
+    s.nkv = cross_tiles(s.n_keys);
+    const long long steps = static_cast<long long>(p.heads) * p.n_qt * s.nkv;
+    if (c.step < c.b_start + steps) break;
+    c.b_start += steps;
+    ++c.b;
+  }
+  const long long r = c.step - c.b_start;
+  const long long unit = r / s.nkv;
+  const int head = static_cast<int>(unit / p.n_qt);
+  s.bh = c.b * p.heads + head;
+  s.q0 = static_cast<int>(unit - static_cast<long long>(head) * p.n_qt) * kSubTiles * kRows;
+  s.kv_begin = static_cast<int>(r - unit * s.nkv);
+  s.kv_end = static_cast<int>(min(static_cast<long long>(s.nkv), s.kv_begin + (c.end - c.step)));
+  s.unit_end = c.step - s.kv_begin + s.nkv;
+  c.step += s.kv_end - s.kv_begin;
+  return true;
+}
+
+// The backward's walk: units are (key head, K/V tile), each with the nq query
+// steps of the head's rows. Tiles wholly behind the keys are no units (the
+// prologue writes their dK and dV, zeros).
+struct CrossBwdSegment {
+  int bh, kv;
+  int i_begin, i_end;
+  int n_keys;
+  long long unit_end;  // stream-K: global step one past the unit's last step
+};
+
+__device__ __forceinline__ int cross_bwd_tiles(int n_keys) { return (n_keys + kKeys - 1) / kKeys; }
+
+__device__ __forceinline__ long long cross_bwd_batch_steps(const CrossBwdParams& p, int b) {
+  return static_cast<long long>(p.heads) * cross_bwd_tiles(cross_keys(p, b)) * p.nq;
+}
+
+__device__ __forceinline__ CrossStart cross_bwd_start(const CrossBwdParams& p) {
+  if (!p.stream_k) return CrossStart{0, 0, 0, 0};
+  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_bwd_batch_steps(p, b); });
+}
+
+__device__ __forceinline__ CrossCursor cross_bwd_first_cursor(const CrossBwdParams& p, const CrossStart& st) {
+  CrossCursor c;
+  c.round = 0;
+  c.b = st.b;
+  c.b_start = st.b_start;
+  c.step = p.stream_k ? cross_share_begin(st, blockIdx.x) : 0;
+  c.end = p.stream_k ? cross_share_begin(st, blockIdx.x + 1) : 0;
+  return c;
+}
+
+__device__ __forceinline__ bool cross_bwd_next_segment(CrossCursor& c, CrossBwdSegment& s, const CrossBwdParams& p) {
+  if (!p.stream_k) {
+    for (;;) {
+      const int u = c.round++ * gridDim.x + blockIdx.x;
+      if (u >= p.num_units || u < 0) return false;
+      s.bh = u / p.nkv;
+      s.kv = u - s.bh * p.nkv;
+      s.n_keys = cross_keys(p, s.bh / p.heads);
+      if (s.kv < cross_bwd_tiles(s.n_keys)) break;
+    }
+    s.i_begin = 0;
+    s.i_end = p.nq;
+    s.unit_end = 0;
+    return true;
+  }
+  if (c.step >= c.end) return false;
+  int tiles;
+  for (;;) {
+    s.n_keys = cross_keys(p, c.b);
+    tiles = cross_bwd_tiles(s.n_keys);
+    const long long steps = static_cast<long long>(p.heads) * tiles * p.nq;
+    if (c.step < c.b_start + steps) break;
+    c.b_start += steps;
+    ++c.b;
+  }
+  const long long r = c.step - c.b_start;
+  const long long unit = r / p.nq;
+  const int head = static_cast<int>(unit / tiles);
+  s.bh = c.b * p.heads + head;
+  s.kv = static_cast<int>(unit - static_cast<long long>(head) * tiles);
+  s.i_begin = static_cast<int>(r - unit * p.nq);
+  s.i_end = static_cast<int>(min(static_cast<long long>(p.nq), s.i_begin + (c.end - c.step)));
+  s.unit_end = c.step - s.i_begin + p.nq;
+  c.step += s.i_end - s.i_begin;
+  return true;
+}
+
+// A K or V tile's rows [valid, 16-row boundary) in shared memory, zeroed by
+// one thread: what lies behind a batch entry's keys can be anything, and a
+// product of a zero weight with a NaN is a NaN. The products that contract
+// over keys stop at that boundary (cross_key_steps), so at most 16 rows of
+// each 64-column panel are written. Full 128-byte rows: the swizzle moves
+// bytes only within a row.
+__device__ __forceinline__ int cross_key_steps(int valid) { return min(max((valid + 15) / 16, 1), kKeys / 16); }
+
+__device__ __forceinline__ void cross_zero_rows(uint32_t tile, int panels, int valid) {
+  const int end = cross_key_steps(valid) * 16;
+  for (int r = max(valid, 0); r < end; ++r)
+    for (int pn = 0; pn < panels; ++pn)
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch)
+        st_shared_v4(tile + static_cast<uint32_t>(pn * kPanelBytes + r * 128 + ch * 16), 0u, 0u, 0u, 0u);
+  fence_proxy_async_shared();
+}
+
+}  // namespace fa2

@@ -1,0 +1,49 @@
+// Host-visible pieces of cross attention (queries and keys of different
+// lengths, per-batch key counts, grouped heads): the parameter blocks and the
+// launcher templates, instantiated in fa2_cross_d{32,64,96,128}.cu.
+//
+// Grouped heads need no kernel of their own: without a causal mask every
+// query row is independent, so the Hq / Hkv query heads that share a key
+// head, adjacent in [B, Hq, Nq, D], are the rows of one [B * Hkv, G * Nq, D]
+// tensor. The kernels see B * Hkv heads of N = G * Nq query rows.
+#pragma once
+#include "fa2_launch.h"
+
+namespace fa2 {
+
+struct CrossParams : Params {  // N: query rows per key head; BH: B * Hkv
+  int Nk;                      // rows of K and V per head
+  int B;
+  int heads;                   // Hkv
+  const int* key_lengths;      // [B] keys of each batch entry (clamped to [0, Nk]), or NULL: Nk
+};
+
+struct CrossBwdParams : BwdParams {  // N: query rows per key head; nkv: K/V tiles of Nk keys
+  int Nk;
+  int B;
+  int heads;
+  const int* key_lengths;
+};
+
+// Keys of batch entry b.
+template <typename P>
+__device__ __forceinline__ int cross_keys(const P& p, int b) {
+  return p.key_lengths ? min(max(__ldg(p.key_lengths + b), 0), p.Nk) : p.Nk;
+}
+
+// The forward on the tensor-core kernel of fa2_kernel.cuh.
+template <int D, bool kBf16>
+cudaError_t launch_cross_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+                             const CrossParams& p, int grid, cudaStream_t stream);
+
+// The backward on the tensor-core kernel of fa2_bwd_kernel.cuh.
+template <int D, bool kBf16>
+cudaError_t launch_cross_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,
+                             const CUtensorMap& dq_acc, const CrossBwdParams& p, int grid, cudaStream_t stream);
+
+// The backward's first kernel (fa2_bwd_api.cu), for B * H heads of N rows:
+// Delta and -LSE * log2(e) of every row, and the dQ accumulator zeroed.
+cudaError_t bwd_row_stats(int D, bool bf16, const void* O, const void* dO, const float* LSE, float* dq_acc,
+                          float* neg_lse2, float* delta, int bh, int N, int Npad, int sms, cudaStream_t stream);
+
+}  // namespace fa2

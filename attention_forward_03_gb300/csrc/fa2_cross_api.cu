@@ -1,0 +1,150 @@
+// C ABI of cross attention: argument checks, tensor maps, the choice of the
+// schedule and the launch. Declarations and the contract: include/fa2.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fa2.h"
+#include "fa2_cross.h"
+
+namespace fa2 {
+namespace {
+
+constexpr bool cross_head_dim_ok(int d) { return d == 32 || d == 64 || d == 96 || d == 128; }
+
+// LSE of rows that have no key at all.
+__global__ void fa2_cross_fill_lse(float* lse, long long n) {
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride)
+    lse[i] = CUDART_INF_F;
+}
+
+using CrossFn = cudaError_t (*)(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                const CrossParams&, int, cudaStream_t);
+
+CrossFn pick_cross(int d, bool bf) {
+  switch (d) {
+    case 32: return bf ? launch_cross_fwd<32, true> : launch_cross_fwd<32, false>;
+    case 64: return bf ? launch_cross_fwd<64, true> : launch_cross_fwd<64, false>;
+    case 96: return bf ? launch_cross_fwd<96, true> : launch_cross_fwd<96, false>;
+    default: return bf ? launch_cross_fwd<128, true> : launch_cross_fwd<128, false>;
+  }
+}
+
+// Whether equal shares of all K/V-tile steps (and a merge of the units they
+// cut) beat whole units in rounds. The cost of each in steps of the busiest
+// SM, as in fwd_auto_schedule; with key counts on the device the units differ
+// by an amount the host cannot know, and the shares follow it.
+bool cross_balanced(long long units, long long nkv, bool lengths, int sms) {
+  constexpr double kSplitCostSteps = 4.0;
+  if (lengths) return true;
+  const double rounds = static_cast<double>((units + sms - 1) / sms) * static_cast<double>(nkv);
+  const double balanced = static_cast<double>(units) * static_cast<double>(nkv) / sms + kSplitCostSteps;
+  return balanced < 0.95 * rounds;
+}
+
+}  // namespace
+}  // namespace fa2
+
+using namespace fa2;
+
+extern "C" int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes) {
+  if (!bytes) return FA2_ERR_INVALID_ARG;
+  if (!cross_head_dim_ok(D)) return FA2_ERR_UNSUPPORTED;
+  int sms = 0;
+  int* status = nullptr;
+  const int rc = current_device_facts(&sms, &status);
+  if (rc != FA2_OK) return rc;
+  *bytes = stream_k_workspace_bytes(sms, D);
+  return FA2_OK;
+}
+
+extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* key_lengths,
+                             int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, int dtype, void* workspace,
+                             size_t workspace_bytes, struct CUstream_st* stream) {
+  if (B < 0 || Hq < 0 || Hkv < 0 || Nq < 0 || Nk < 0) return FA2_ERR_INVALID_ARG;
+  if (!cross_head_dim_ok(D)) return FA2_ERR_UNSUPPORTED;
+  if (dtype != FA2_F16 && dtype != FA2_BF16) return FA2_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA2_ERR_INVALID_ARG;
+  if (B == 0 || Hq == 0 || Nq == 0) return FA2_OK;
+  if (Hkv == 0 || Hq % Hkv != 0) return FA2_ERR_INVALID_ARG;
+  if (!Q || !O || !LSE || (Nk > 0 && (!K || !V))) return FA2_ERR_INVALID_ARG;
+  const int64_t bh = static_cast<int64_t>(B) * Hkv;
+  const int64_t rows = static_cast<int64_t>(Hq / Hkv) * Nq;  // query rows per key head
+  const int64_t n_qt = (rows + kSubTiles * kRows - 1) / (kSubTiles * kRows);
+  // 2^30: a row index plus a unit's 256 rows stays inside 32 bits
+  if (rows > (1 << 30) || Nk > (1 << 30) || bh > INT32_MAX || bh * n_qt > INT32_MAX) return FA2_ERR_INVALID_ARG;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(K) |
+                        reinterpret_cast<uintptr_t>(V) | reinterpret_cast<uintptr_t>(O) |
+                        reinterpret_cast<uintptr_t>(LSE) | reinterpret_cast<uintptr_t>(workspace);
+  if ((mis & 15u) || (reinterpret_cast<uintptr_t>(key_lengths) & 3u)) return FA2_ERR_ALIGN;
+  const size_t qb = static_cast<size_t>(bh) * rows * D * 2, kb = static_cast<size_t>(bh) * Nk * D * 2;
+  const size_t lb = static_cast<size_t>(bh) * rows * 4, nb = key_lengths ? static_cast<size_t>(B) * 4 : 0;
+  const void* ins[4] = {Q, K, V, key_lengths};
+  const size_t in_bytes[4] = {qb, kb, kb, nb};
+  const void* outs[3] = {O, LSE, workspace};
+  const size_t out_bytes[3] = {qb, lb, workspace ? workspace_bytes : 0};
+  for (int a = 0; a < 3; ++a) {
+    if (!out_bytes[a]) continue;
+    for (int b = 0; b < 4; ++b)
+      if (in_bytes[b] && ranges_overlap(outs[a], out_bytes[a], ins[b], in_bytes[b])) return FA2_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 3; ++b)
+      if (out_bytes[b] && ranges_overlap(outs[a], out_bytes[a], outs[b], out_bytes[b])) return FA2_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  int* status = nullptr;
+  const int rc = current_device_facts(&sms, &status);
+  if (rc != FA2_OK) return rc;
+  if (workspace && workspace_bytes < stream_k_workspace_bytes(sms, D)) return FA2_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+  if (Nk == 0) {
+    cudaError_t e = cudaMemsetAsync(O, 0, qb, s);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    const long long n = bh * rows;
+    fa2_cross_fill_lse<<<static_cast<int>(std::min<long long>((n + 255) / 256, 8ll * sms)), 256, 0, s>>>(LSE, n);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
+  }
+
+  CUtensorMap mq, mk, mv, mo;
+  if (!encode_tile_map(&mq, Q, (int)bh, (int)rows, D, dtype, 128u) || !encode_tile_map(&mk, K, (int)bh, Nk, D, dtype, 128u) ||
+      !encode_tile_map(&mv, V, (int)bh, Nk, D, dtype, 128u) || !encode_tile_map(&mo, O, (int)bh, (int)rows, D, dtype, 128u))
+    return record_cuda_error(cudaErrorInvalidValue);
+  CrossParams p = {};
+  p.o = O;
+  p.lse = LSE;
+  p.status = status;
+  p.watchdog_ns = watchdog_limit_ns();
+  p.N = (int)rows;
+  p.BH = (int)bh;
+  p.n_qt = (int)n_qt;
+  p.num_units = (int)(bh * n_qt);
+  p.nkv_full = (Nk + kKeys - 1) / kKeys;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.test_withhold = take_test_withhold();
+  p.Nk = Nk;
+  p.B = B;
+  p.heads = Hkv;
+  p.key_lengths = key_lengths;
+  int grid;
+  if (workspace && cross_balanced(p.num_units, p.nkv_full, key_lengths != nullptr, sms)) {
+    p.stream_k = 1;
+    grid = static_cast<int>(std::min<long long>(sms, static_cast<long long>(p.num_units) * p.nkv_full));
+    const size_t slots = static_cast<size_t>(sms) * kSubTiles;
+    char* ws = static_cast<char*>(workspace);
+    p.ws_o = reinterpret_cast<float*>(ws);
+    p.ws_stats = p.ws_o + slots * D * 128;
+    p.ws_flags = reinterpret_cast<unsigned long long*>(
+        ws + (slots * (static_cast<size_t>(D) * 128 + 3 * 128) * sizeof(float) + 255) / 256 * 256);
+    p.epoch = next_launch_epoch();
+  } else {
+    grid = std::min(p.num_units, sms);
+  }
+  const cudaError_t e = pick_cross(D, dtype == FA2_BF16)(mq, mk, mv, mo, p, grid, s);
+  return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
+}

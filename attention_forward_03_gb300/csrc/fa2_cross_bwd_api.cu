@@ -1,0 +1,235 @@
+// C ABI of the cross-attention backward: argument checks, the workspace
+// layout, tensor maps, the launches, and the last of its three kernels.
+// Declarations and the contract: include/fa2.h.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fa2.h"
+#include "fa2_cross.h"
+
+namespace fa2 {
+namespace {
+
+constexpr int kEndThreads = 256;
+
+size_t round_up_256(size_t x) { return (x + 255) / 256 * 256; }
+
+// dQ accumulator | -LSE*log2(e) | Delta | partial dV, dK of cut units | flags
+struct CrossBwdWorkspace {
+  size_t dq_bytes, stat_bytes, part_bytes, flag_bytes, total;
+};
+
+CrossBwdWorkspace cross_bwd_layout(int64_t bh, int64_t rows, int D) {
+  const int64_t sr = bwd_step_rows(D), npad = (rows + sr - 1) / sr * sr;
+  CrossBwdWorkspace w;
+  w.dq_bytes = round_up_256(static_cast<size_t>(bh) * rows * D * sizeof(float));
+  w.stat_bytes = round_up_256(static_cast<size_t>(bh) * npad * sizeof(float));
+  w.part_bytes = round_up_256(static_cast<size_t>(kBwdMaxCtas) * 2 * D * 128 * sizeof(float));
+  w.flag_bytes = round_up_256(static_cast<size_t>(kBwdMaxCtas) * sizeof(unsigned long long));
+  w.total = w.dq_bytes + 2 * w.stat_bytes + w.part_bytes + w.flag_bytes;
+  return w;
+}
+
+__device__ __forceinline__ uint32_t pack_two(float lo, float hi, bool bf16) {
+  if (bf16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per
+// thread; zeros for the dK and dV rows of tiles wholly behind their keys; and
+// the flags of the partial results taken back, so that a replay of a captured
+// call, which carries the same tag, does not find them set.
+template <bool kBf16>
+__global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4* __restrict__ acc, uint4* __restrict__ dq,
+                                                                    float scale, long long n8, uint4* __restrict__ dk,
+                                                                    uint4* __restrict__ dv, CrossBwdParams p, int per_row) {
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  for (long long i = first; i < n8; i += stride) {
+    const float4 a = acc[2 * i], b = acc[2 * i + 1];
+    dq[i] = make_uint4(pack_two(a.x * scale, a.y * scale, kBf16), pack_two(a.z * scale, a.w * scale, kBf16),
+                       pack_two(b.x * scale, b.y * scale, kBf16), pack_two(b.z * scale, b.w * scale, kBf16));
+  }
+  if (p.ws_flags && first < kBwdMaxCtas) p.ws_flags[first] = 0ull;
+  if (!p.key_lengths) return;
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  // one head of rows after the other, its rows over the block's threads
+  for (long long h = blockIdx.x; h < p.BH; h += gridDim.x) {
+    const int n = cross_keys(p, static_cast<int>(h / p.heads));
+    const long long from = min(static_cast<long long>((n + kKeys - 1) / kKeys) * kKeys, static_cast<long long>(p.Nk));
+    const long long base = h * p.Nk;
+    for (long long i = (base + from) * per_row + threadIdx.x; i < (base + p.Nk) * per_row; i += blockDim.x) {
+      dk[i] = z;
+      dv[i] = z;
+    }
+  }
+}
+
+using CrossBwdFn = cudaError_t (*)(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                   const CUtensorMap&, const CrossBwdParams&, int, cudaStream_t);
+
+CrossBwdFn pick_cross_bwd(int d, bool bf) {
+  switch (d) {
+    case 32: return bf ? launch_cross_bwd<32, true> : launch_cross_bwd<32, false>;
+    case 64: return bf ? launch_cross_bwd<64, true> : launch_cross_bwd<64, false>;
+    case 96: return bf ? launch_cross_bwd<96, true> : launch_cross_bwd<96, false>;
+    default: return bf ? launch_cross_bwd<128, true> : launch_cross_bwd<128, false>;
+  }
+}
+
+// Partial-result write and merge of a cut unit, in query steps.
+constexpr long long kCrossBwdSplitCostSteps = 2;
+
+}  // namespace
+}  // namespace fa2
+
+using namespace fa2;
+
+namespace {
+
+int check_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int D) {
+  if (B < 0 || Hq < 0 || Hkv < 0 || Nq < 0 || Nk < 0) return FA2_ERR_INVALID_ARG;
+  if (!bwd_head_dim_ok(D)) return FA2_ERR_UNSUPPORTED;
+  if (B > 0 && Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)) return FA2_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * std::max(Hq, Hkv) > INT32_MAX) return FA2_ERR_INVALID_ARG;
+  const int64_t rows = Hkv > 0 ? static_cast<int64_t>(Hq / Hkv) * Nq : 0;
+  if (rows > (1 << 30) || Nk > (1 << 30)) return FA2_ERR_INVALID_ARG;
+  return FA2_OK;
+}
+
+}  // namespace
+
+extern "C" int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, size_t* bytes) {
+  if (!bytes) return FA2_ERR_INVALID_ARG;
+  const int rc = check_sizes(B, Hq, Hkv, Nq, Nk, D);
+  if (rc != FA2_OK) return rc;
+  const int64_t rows = Hkv > 0 ? static_cast<int64_t>(Hq / Hkv) * Nq : 0;
+  *bytes = cross_bwd_layout(static_cast<int64_t>(B) * Hkv, rows, D).total;
+  return FA2_OK;
+}
+
+extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                             const float* LSE, void* dQ, void* dK, void* dV, const int* key_lengths, int B, int Hq,
+                             int Hkv, int Nq, int Nk, int D, float scale, int dtype, void* workspace,
+                             size_t workspace_bytes, struct CUstream_st* stream) {
+  int rc = check_sizes(B, Hq, Hkv, Nq, Nk, D);
+  if (rc != FA2_OK) return rc;
+  if (dtype != FA2_F16 && dtype != FA2_BF16) return FA2_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA2_ERR_INVALID_ARG;
+  const bool has_q = B > 0 && Hq > 0 && Nq > 0, has_k = B > 0 && Hkv > 0 && Nk > 0;
+  if (!has_q && !has_k) return FA2_OK;
+  if ((has_q && (!Q || !O || !dO || !LSE || !dQ)) || (has_k && (!K || !V || !dK || !dV))) return FA2_ERR_INVALID_ARG;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(K) |
+                        reinterpret_cast<uintptr_t>(V) | reinterpret_cast<uintptr_t>(O) |
+                        reinterpret_cast<uintptr_t>(dO) | reinterpret_cast<uintptr_t>(LSE) |
+                        reinterpret_cast<uintptr_t>(dQ) | reinterpret_cast<uintptr_t>(dK) |
+                        reinterpret_cast<uintptr_t>(dV);
+  if ((mis & 15u) || (reinterpret_cast<uintptr_t>(key_lengths) & 3u)) return FA2_ERR_ALIGN;
+  const int64_t bh = static_cast<int64_t>(B) * Hkv;
+  const int64_t rows = Hkv > 0 ? static_cast<int64_t>(Hq / Hkv) * Nq : 0;
+  const int sr = bwd_step_rows(D);
+  const int64_t npad = (rows + sr - 1) / sr * sr, nkv = (static_cast<int64_t>(Nk) + kBwdKeys - 1) / kBwdKeys;
+  if (bh * nkv > INT32_MAX) return FA2_ERR_INVALID_ARG;
+  const bool work = has_q && has_k;
+  const CrossBwdWorkspace wl = cross_bwd_layout(bh, rows, D);
+  if (work) {
+    if (!workspace || workspace_bytes < wl.total) return FA2_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FA2_ERR_ALIGN;
+  }
+  const size_t qb = static_cast<size_t>(bh) * rows * D * 2, kb = static_cast<size_t>(bh) * Nk * D * 2;
+  const size_t lb = static_cast<size_t>(bh) * rows * 4;
+  const void* ins[7] = {Q, K, V, O, dO, LSE, key_lengths};
+  const size_t in_bytes[7] = {qb, kb, kb, qb, qb, lb, key_lengths ? static_cast<size_t>(B) * 4 : 0};
+  const void* outs[4] = {dQ, dK, dV, workspace};
+  const size_t out_bytes[4] = {qb, kb, kb, work ? workspace_bytes : 0};
+  for (int a = 0; a < 4; ++a) {
+    if (!out_bytes[a]) continue;
+    for (int b = 0; b < 7; ++b)
+      if (in_bytes[b] && ranges_overlap(outs[a], out_bytes[a], ins[b], in_bytes[b])) return FA2_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 4; ++b)
+      if (out_bytes[b] && ranges_overlap(outs[a], out_bytes[a], outs[b], out_bytes[b])) return FA2_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  int* status = nullptr;
+  if ((rc = current_device_facts(&sms, &status)) != FA2_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!work) {  // no query or no key: every gradient there is is zero
+    if (has_q) e = cudaMemsetAsync(dQ, 0, qb, s);
+    if (has_k) e = cudaMemsetAsync(dK, 0, kb, s);
+    if (has_k && e == cudaSuccess) e = cudaMemsetAsync(dV, 0, kb, s);
+    return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
+  }
+
+  char* ws = static_cast<char*>(workspace);
+  float* dq_acc = reinterpret_cast<float*>(ws);
+  float* neg_lse2 = reinterpret_cast<float*>(ws + wl.dq_bytes);
+  float* delta = reinterpret_cast<float*>(ws + wl.dq_bytes + wl.stat_bytes);
+  CUtensorMap mk, mv, mq, mdo, mdq;
+  const int n = (int)rows, ibh = (int)bh;
+  if (!encode_tile_map(&mk, K, ibh, Nk, D, dtype, kBwdKeys) || !encode_tile_map(&mv, V, ibh, Nk, D, dtype, kBwdKeys) ||
+      !encode_tile_map(&mq, Q, ibh, n, D, dtype, static_cast<unsigned>(sr)) ||
+      !encode_tile_map(&mdo, dO, ibh, n, D, dtype, static_cast<unsigned>(sr)) ||
+      !(D <= 64 ? encode_f32_cols_map_sw128(&mdq, dq_acc, ibh, n, D, 128) : encode_f32_rows_map(&mdq, dq_acc, ibh, n, D, 32)))
+    return record_cuda_error(cudaErrorInvalidValue);
+  const bool bf = dtype == FA2_BF16;
+  e = bwd_row_stats(D, bf, O, dO, LSE, dq_acc, neg_lse2, delta, ibh, n, (int)npad, sms, s);
+  if (e != cudaSuccess) return record_cuda_error(e);
+
+  CrossBwdParams p = {};
+  p.dk = dK;
+  p.dv = dV;
+  p.dq_acc = dq_acc;
+  p.neg_lse2 = neg_lse2;
+  p.delta = delta;
+  p.status = status;
+  p.watchdog_ns = watchdog_limit_ns();
+  p.N = n;
+  p.Npad = (int)npad;
+  p.BH = ibh;
+  p.nkv = (int)nkv;
+  p.nq = (int)(npad / sr);
+  p.num_units = (int)(bh * nkv);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale = scale;
+  p.Nk = Nk;
+  p.B = B;
+  p.heads = Hkv;
+  p.key_lengths = key_lengths;
+  p.test_withhold = take_test_withhold();
+  // Equal shares of all query steps when that saves the busiest SM at least
+  // 5 %, and always with key counts on the device, which the shares follow.
+  const long long steps = static_cast<long long>(p.num_units) * p.nq;
+  const int round_grid = std::min(p.num_units, sms);
+  const int sk_grid = static_cast<int>(std::min<long long>(std::min(sms, kBwdMaxCtas), steps));
+  const long long rounds = (p.num_units + round_grid - 1) / round_grid * static_cast<long long>(p.nq);
+  const long long split = (steps + sk_grid - 1) / sk_grid + kCrossBwdSplitCostSteps;
+  int grid = round_grid;
+  if (key_lengths || 100 * split < 95 * rounds) {
+    p.stream_k = 1;
+    grid = sk_grid;
+    p.ws_part = reinterpret_cast<float*>(ws + wl.dq_bytes + 2 * wl.stat_bytes);
+    p.ws_flags = reinterpret_cast<unsigned long long*>(ws + wl.dq_bytes + 2 * wl.stat_bytes + wl.part_bytes);
+    p.epoch = next_launch_epoch();
+  }
+  e = pick_cross_bwd(D, bf)(mk, mv, mq, mdo, mdq, p, grid, s);
+  if (e != cudaSuccess) return record_cuda_error(e);
+
+  const long long n8 = bh * rows * (D / 8);
+  const int blocks = static_cast<int>(std::max<long long>(1, std::min<long long>((n8 + kEndThreads - 1) / kEndThreads, 8ll * sms)));
+  auto finish = bf ? fa2_cross_bwd_finish<true> : fa2_cross_bwd_finish<false>;
+  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), scale, n8,
+                                        static_cast<uint4*>(dK), static_cast<uint4*>(dV), p, D / 8);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
+}

@@ -62,6 +62,9 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "fa2_cross.cuh"
 #include "fa2_fwd_common.cuh"
 
 namespace fa2 {
@@ -87,11 +90,14 @@ struct Layout {
   // s_free[2], p_full[2], p_free[2], o_full[2], drain[2], part_done[2], o_staged[2], o_buf_free[2]
   static constexpr int kNumBars = 2 + 3 * kStages + 2 * 9;
   static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
+  static constexpr int kCrossStartOffset = kMiscOffset + 16;   // cross attention: CrossStart
   static constexpr int kSmemBytes = kMiscOffset + 16 + 1024;  // + slack for 1 KB alignment
+  static constexpr int kCrossSmemBytes = kSmemBytes + sizeof(CrossStart);
   static constexpr uint32_t kColO = 2 * kKeys;                 // O0 at 256, O1 at 256 + kDp
   static constexpr uint32_t kColP = kColO + 2 * kDp;            // kDp = 64: P0 at 384, P1 at 448
   static_assert(kColO + 2 * kDp + (kPInTmem ? 2 * kKeys / 2 : 0) <= kTmemCols, "TMEM budget");
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kCrossSmemBytes <= 232448, "shared memory budget");
+  static_assert(kCrossStartOffset % alignof(CrossStart) == 0, "alignment");
 };
 
 // End of sub-tile 0's K/V range in a segment [b, e). Under the causal mask
@@ -106,12 +112,18 @@ __device__ __forceinline__ int sub0_end(const Segment& w) {
   return skip ? w.kv_end - 1 : w.kv_end;
 }
 
-template <int D, bool kBf16, bool kCausal>
+// kCross: cross attention (fa2_cross.h). The differences: the walk (units of
+// a batch entry have as many K/V tiles as it has keys), the key limit, rows
+// of V behind the keys zeroed and their products skipped, and a second
+// sub-tile wholly past the query rows left out.
+template <int D, bool kBf16, bool kCausal, bool kCross = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fa2_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                   const Params p) {
+                   const std::conditional_t<kCross, CrossParams, Params> p) {
+  static_assert(!(kCross && kCausal), "cross attention has no causal mask");
   using L = Layout<D>;
+  using Seg = std::conditional_t<kCross, CrossSegment, Segment>;
   // MMA issuers split by instruction type (one thread for every S, one for
   // every P.V) or by sub-tile (each thread S and P.V of one sub-tile). Both
   // measured (with the issuers sleeping between polls): by type is 10-15 %
@@ -153,6 +165,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  // The walk over this CTA's segments.
+  [[maybe_unused]] CrossStart* const start = reinterpret_cast<CrossStart*>(smem + L::kCrossStartOffset);
+  if constexpr (kCross) {
+    if (warp == 0) {
+      const CrossStart st = cross_fwd_start(p);
+      if (lane == 0) *start = st;
+      __syncwarp();
+    }
+  }
+  auto first_segment_cursor = [&]() {
+    if constexpr (kCross) return cross_first_cursor(p, *start);
+    else return first_cursor(p);
+  };
+  auto advance = [&](auto& c, Seg& s) -> bool {
+    if constexpr (kCross) return cross_next_segment(c, s, p);
+    else return next_segment<kCausal>(c, s, p);
+  };
+  // Sub-tiles of the unit with any query row.
+  auto live_subtiles = [&](const Seg& s) -> int { return kCross && s.q0 + kRows >= p.N ? 1 : kSubTiles; };
+
   if (threadIdx.x == 0) {
     mbar_init(bar_q_full, 1);
     // released by the S issuer (K tile, Q) or the P.V issuer (V tile); with
@@ -180,9 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // TMEM allocation, the CTA barrier and the register hand-off, so that
     // their load latency overlaps that set-up; the producer carries on after
     // them (ring slot 0).
-    SegCursor c0 = first_cursor(p);
-    Segment w0;
-    if (next_segment<kCausal>(c0, w0, p)) {
+    auto c0 = first_segment_cursor();
+    Seg w0;
+    if (advance(c0, w0)) {
       mbar_arrive_expect_tx(bar_q_full, L::kQBytes);
       for (int t = 0; t < kSubTiles; ++t)
         for (int pn = 0; pn < L::kPanels; ++pn)
@@ -228,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next use of its K / V full barrier
         uint32_t types = 0, kbits = 0, vbits = 0;
         bool ok = true;
-        SegCursor cur = first_cursor(p);
-        Segment w;
+        auto cur = first_segment_cursor();
+        Seg w;
         auto load_tile = [&](const CUtensorMap* map, int j, uint32_t is_v) -> bool {
           if (!wait_bounded(bar_empty(slot), ring_ph ^ 1u, wd, kSiteLoadRingEmpty, true, kNapNs)) return false;
           const uint32_t full = bar_full(slot, is_v);
@@ -248,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        while (ok && next_segment<kCausal>(cur, w, p)) {
+        while (ok && advance(cur, w)) {
           if (q_round == 0) {
             // Q and K_b of the first segment were requested at kernel entry
             // (into ring slot 0): account for them as loads of this thread.
@@ -296,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the high words are constants.
         constexpr uint32_t kHi = desc_hi_sw128(1024);  // 8-row (K-major) / 8-key (MN-major) groups 1 KB apart
         // S_t = Q_t K^T : D/16 steps of K=16 along the head dimension.
-        auto issue_s = [&](int t, int slot) {
+        // Cross attention: N only as wide as the tile's keys (`steps` groups of 16).
+        auto issue_s = [&](int t, int slot, [[maybe_unused]] int steps) {
+          const uint32_t idesc = kCross ? make_idesc_f16(kBf16, 16 * steps, false) : idesc_s;
           const uint32_t q_lo = desc_lo_sw128(sQ, 16);
           const uint32_t ring_lo = desc_lo_sw128(sRing, 16);
           const uint32_t qa = q_lo + static_cast<uint32_t>((t * L::kTileBytes) >> 4);
@@ -305,12 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
-            mma_ss_w(dt, qa + off, kHi, ka + off, kHi, idesc_s, kk > 0 ? 1u : 0u);
+            mma_ss_w(dt, qa + off, kHi, ka + off, kHi, idesc, kk > 0 ? 1u : 0u);
           }
         };
         // O_t (+)= P_t V : P (K-major, shared memory; Dp = 64: tensor memory)
         // and V (MN-major, shared memory), 8 steps of 16 keys.
-        auto issue_pv = [&](int t, int slot, bool acc) {
+        // Cross attention: only the tile's first `steps` ones, those with keys.
+        auto issue_pv = [&](int t, int slot, bool acc, [[maybe_unused]] int steps) {
           const uint32_t p_lo = desc_lo_sw128(sP, 16);
           const uint32_t ring_lo_v = desc_lo_sw128(sRing, kPanelBytes);  // V: 64-column panels 16 KB apart
           const uint32_t pa = p_lo + static_cast<uint32_t>((t * kPTileBytes) >> 4);
@@ -321,6 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kKeys / 16; ++kk) {
             const uint32_t vb = va + static_cast<uint32_t>((kk * 16 * 128) >> 4);
             const uint32_t acc_kk = (acc || kk > 0) ? 1u : 0u;
+            if constexpr (kCross) {
+              if (kk >= steps) break;
+            }
             if constexpr (L::kPInTmem) {
               mma_ts_w(dt, pt + 8u * kk, vb, kHi, idesc_o, acc_kk);
             } else {
@@ -330,6 +368,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
 
+        // 16-key groups of tile j with keys, and the rows of its V tile behind
+        // the keys zeroed (nothing to do at Nk: the copy engine read zeros).
+        auto key_steps = [&]([[maybe_unused]] const Seg& s, [[maybe_unused]] int j) -> int {
+          if constexpr (kCross) return cross_key_steps(s.n_keys - j * kKeys);
+          else return kKeys / 16;
+        };
+        auto clean_v = [&]([[maybe_unused]] const Seg& s, [[maybe_unused]] int j, [[maybe_unused]] int slot) {
+          if constexpr (kCross) {
+            if (j == s.nkv - 1 && s.n_keys < p.Nk)
+              cross_zero_rows(sRing + static_cast<uint32_t>(slot * L::kTileBytes), L::kPanels, s.n_keys - j * kKeys);
+          }
+        };
         // Position of a tile in the producer's load sequence of a segment
         // [b, e): K_b, then for each j: K_{j+1} (if any), V_j. Each issuer
         // walks the ring through the global load index of its own tiles.
@@ -347,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint32_t base_idx = 0;  // global load index of the current segment's first tile
         bool ok = true;
-        SegCursor cur = first_cursor(p);
-        Segment w;
+        auto cur = first_segment_cursor();
+        Seg w;
         if constexpr (kTypeSplit) {
           if (me == 0) {
             // S issuer: S_t(j) for both sub-tiles, each as soon as K_j has landed
@@ -356,20 +406,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             // segments) into registers.
             uint32_t q_round = 0, s_free_ph[2] = {0u, 0u};
             bool s_out[2] = {false, false};  // an S issued whose TMEM the softmax has not released yet
-            while (ok && next_segment<kCausal>(cur, w, p)) {
+            while (ok && advance(cur, w)) {
               const int b = w.kv_begin, e = w.kv_end;
+              const int n_sub = live_subtiles(w);
               if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) { ok = false; break; }
               ++q_round;
               for (int j = b; j < e && ok; ++j) {
                 const int slot_k = take(base_idx + k_index(j, b), 0u);
                 if (slot_k < 0) { ok = false; break; }
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < n_sub; ++t) {
                   if (s_out[t]) {
                     if (!wait_bounded(bar_s_free0 + 8 * t, s_free_ph[t], wd, kSiteMmaSFree, true, kNapNs)) { ok = false; break; }
                     s_free_ph[t] ^= 1u;
                   }
                   tc_fence_after_sync();
-                  issue_s(t, slot_k);
+                  issue_s(t, slot_k, key_steps(w, j));
                   mma_commit(bar_s_full0 + 8 * t);
                   s_out[t] = true;
                 }
@@ -383,16 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // P.V issuer: O_t += P_t(j) V_j for both sub-tiles, each as soon as
             // V_j has landed and the softmax has published P_t(j).
             uint32_t p_full_ph[2] = {0u, 0u};
-            while (ok && next_segment<kCausal>(cur, w, p)) {
+            while (ok && advance(cur, w)) {
               const int b = w.kv_begin, e = w.kv_end;
+              const int n_sub = live_subtiles(w);
               for (int j = b; j < e && ok; ++j) {
                 const int slot_v = take(base_idx + v_index(j, b, e), 1u);
                 if (slot_v < 0) { ok = false; break; }
-                for (int t = 0; t < 2; ++t) {
+                clean_v(w, j, slot_v);
+                for (int t = 0; t < n_sub; ++t) {
                   if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; break; }
                   p_full_ph[t] ^= 1u;
                   tc_fence_after_sync();
-                  issue_pv(t, slot_v, j > b);
+                  issue_pv(t, slot_v, j > b, key_steps(w, j));
                   mma_commit(bar_p_free0 + 8 * t);
                   if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
                 }
@@ -411,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t q_round = 0, s_free_ph = 0, p_full_ph = 0;
           bool s_out = false;
           bool skip_s = false;  // the S of the tile being taken is skipped (sub-tile 0, masked tile)
-          auto next_s = [&](int slot_k) -> bool {
+          auto next_s = [&](int slot_k, int steps) -> bool {
             if (skip_s) {  // a tile sub-tile 0 skips: release the K slot, no product
               mma_commit(bar_empty(slot_k));
               return true;
@@ -421,35 +474,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               s_free_ph ^= 1u;
             }
             tc_fence_after_sync();
-            issue_s(t, slot_k);
+            issue_s(t, slot_k, steps);
             mma_commit(bar_s_full0 + 8 * t);
             mma_commit(bar_empty(slot_k));
             s_out = true;
             return true;
           };
-          while (ok && next_segment<kCausal>(cur, w, p)) {
+          while (ok && advance(cur, w)) {
             const int b = w.kv_begin, e = w.kv_end;
-            const int et = t == 0 ? sub0_end<kCausal>(w) : e;  // this sub-tile's end
+            // this sub-tile's end (a sub-tile without query rows: nothing but the slots' release)
+            const int et = t == 0 ? sub0_end<kCausal>(w) : (t < live_subtiles(w) ? e : b);
             if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) { ok = false; break; }
             ++q_round;
             int slot_k = take(base_idx + k_index(b, b), 0u);
-            skip_s = false;
-            if (slot_k < 0 || !next_s(slot_k)) { ok = false; break; }
+            skip_s = et == b;
+            if (slot_k < 0 || !next_s(slot_k, key_steps(w, b))) { ok = false; break; }
             if (e - b == 1) mma_commit(bar_q_empty);
             for (int j = b; j < e && ok; ++j) {
               if (j + 1 < e) {
                 slot_k = take(base_idx + k_index(j + 1, b), 0u);
                 skip_s = j + 1 >= et;
-                if (slot_k < 0 || !next_s(slot_k)) { ok = false; break; }
+                if (slot_k < 0 || !next_s(slot_k, key_steps(w, j + 1))) { ok = false; break; }
                 if (j + 2 == e) mma_commit(bar_q_empty);
               }
               const int slot_v = take(base_idx + v_index(j, b, e), 1u);
               if (slot_v < 0) { ok = false; break; }
               if (j < et) {
+                clean_v(w, j, slot_v);
                 if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph, wd, kSiteMmaPFull, true, kNapNs)) { ok = false; break; }
                 p_full_ph ^= 1u;
                 tc_fence_after_sync();
-                issue_pv(t, slot_v, j > b);
+                issue_pv(t, slot_v, j > b, key_steps(w, j));
                 mma_commit(bar_p_free0 + 8 * t);
                 if (j == et - 1) mma_commit(bar_o_full0 + 8 * t);
               }
@@ -491,9 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ost_state = 0;
     uint32_t p_count = 0;  // P tiles published so far (= P.V products issued or pending)
     bool ok = true;
-    SegCursor cur = first_cursor(p);
-    Segment w;
-    while (ok && next_segment<kCausal>(cur, w, p)) {
+    auto cur = first_segment_cursor();
+    Seg w;
+    while (ok && advance(cur, w)) {
+      if (t >= live_subtiles(w)) continue;
       if constexpr (!L::kPInTmem) {
         // the previous segment's O was staged in this P buffer: the store
         // engine must have read it before this segment's first P overwrites it
@@ -505,7 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int row = w.q0 + t * kRows + rr;
-      const int limit = kCausal ? min(p.N, row + 1) : p.N;  // allowed keys: [0, limit)
+      int limit;  // allowed keys: [0, limit)
+      if constexpr (kCross) limit = w.n_keys;
+      else limit = kCausal ? min(p.N, row + 1) : p.N;
       float m_raw = -CUDART_INF_F;  // running max of the raw scores seen so far
       float base = -CUDART_INF_F;   // exponent base (log2 units) that l and O are relative to
       float l = 0.f;    // sum of p (unrounded): LSE
@@ -664,12 +722,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       float a_own = 1.f, nbase = base;
       int first_c = blockIdx.x + 1, last_c = blockIdx.x;  // partial holders [first_c, last_c]
       if (p.stream_k && w.kv_end < w.nkv) {
-        while (last_c + 1 < static_cast<int>(gridDim.x) && stream_k_begin(p, last_c + 1) < w.unit_end) ++last_c;
+        if constexpr (kCross) {
+          while (last_c + 1 < start->shares && cross_share_begin(*start, last_c + 1) < w.unit_end) ++last_c;
+        } else {
+          while (last_c + 1 < static_cast<int>(gridDim.x) && stream_k_begin(p, last_c + 1) < w.unit_end) ++last_c;
+        }
         bool fine = true;
         for (int cb = first_c; cb <= last_c && fine; ++cb)
           fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSitePartialFlag);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
+        if constexpr (kCross) {
+          // Every thread of the warpgroup has seen the flags: take them back,
+          // so that a replay of a captured launch, which carries the same
+          // tag, does not find them set before its partials are written.
+          mbar_arrive(bar_part0 + 8 * t);
+          if (rr < 32) {
+            bool seen = wait_bounded(bar_part0 + 8 * t, part_phase, wd, kSitePartialFlag);
+            seen = __all_sync(0xffffffffu, seen);
+            if (!seen) break;
+            if (rr == 0)
+              for (int cb = first_c; cb <= last_c; ++cb) p.ws_flags[static_cast<size_t>(cb) * 2 + t] = 0ull;
+          }
+          part_phase ^= 1u;
+        }
         for (int cb = first_c; cb <= last_c; ++cb)
           nbase = fmaxf(nbase, __ldcg(p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128 + rr));
         a_own = ex2_approx(base - nbase);
@@ -768,11 +844,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The stream-K schedule waits across CTAs, so it is launched cooperatively
 // (the whole grid resident at once, or the launch fails).
-template <int D, bool kBf16, bool kCausal>
-cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
-                       const Params& p, int grid, cudaStream_t stream) {
-  auto kern = fa2_fwd_kernel<D, kBf16, kCausal>;
-  const int smem = Layout<D>::kSmemBytes;
+template <int D, bool kBf16, bool kCausal, bool kCross, typename P>
+cudaError_t launch_fwd_kernel(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+                              const P& p, int grid, cudaStream_t stream) {
+  auto kern = fa2_fwd_kernel<D, kBf16, kCausal, kCross>;
+  const int smem = kCross ? Layout<D>::kCrossSmemBytes : Layout<D>::kSmemBytes;
   // Once per device: the register check and the shared-memory opt-in.
   static PerDeviceOnce prepared;
   const cudaError_t e = once_per_device(prepared, [&]() -> cudaError_t {
@@ -796,6 +872,18 @@ cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, q, k, v, o, p);
+}
+
+template <int D, bool kBf16, bool kCausal>
+cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+                       const Params& p, int grid, cudaStream_t stream) {
+  return launch_fwd_kernel<D, kBf16, kCausal, false>(q, k, v, o, p, grid, stream);
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_cross_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+                             const CrossParams& p, int grid, cudaStream_t stream) {
+  return launch_fwd_kernel<D, kBf16, false, true>(q, k, v, o, p, grid, stream);
 }
 
 }  // namespace fa2

@@ -428,6 +428,84 @@ FA2_API int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const v
                                  int dtype, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
 
 /*
+ * fa2_cross_fwd — cross attention: the queries of one sequence over the keys
+ * and values of another (an encoder's states, say), of another length.
+ *
+ *   O[b,h,i,:] = softmax_j(scale <Q[b,h,i,:], K[b,g,j,:]>) V[b,g,:,:],
+ *   LSE[b,h,i] = ln sum_j exp(scale <Q[b,h,i,:], K[b,g,j,:]>)
+ *   over the keys j < key_lengths[b], with key head g = h / (Hq / Hkv).
+ * A row without any key gives O = 0 and LSE = +inf.
+ *
+ * Q, O      : device pointers, contiguous [B, Hq, Nq, D] of `dtype`.
+ * K, V      : device pointers, contiguous [B, Hkv, Nk, D] of `dtype`. What
+ *             lies behind a batch entry's keys is never used: it may hold
+ *             anything, NaN included. NULL is accepted when Nk is 0.
+ * LSE       : device pointer, contiguous [B, Hq, Nq] fp32.
+ * key_lengths: device pointer, [B] int32: how many of the Nk keys each batch
+ *             entry has (values outside [0, Nk] count as the nearer end), or
+ *             NULL: all of them.
+ * B, Hq, Hkv, Nq, Nk: sizes >= 0; Hq a multiple of Hkv. Nothing happens when
+ *             O is empty. Hq / Hkv * Nq and Nk are at most 2^30.
+ * D         : 32, 64, 96 or 128.
+ * scale, dtype, stream: as fa2_fwd.
+ * workspace : NULL, or a 16-byte aligned device buffer of at least
+ *             fa2_cross_fwd_workspace_bytes(D) bytes that overlaps no tensor;
+ *             scratch, needs no initialisation, not shared by calls that run
+ *             at the same time. With it the work of long key rows is cut into
+ *             equal shares for all SMs; without it every work unit runs on
+ *             one SM. A captured call can be replayed; the replays share the
+ *             workspace.
+ * O and LSE are fully overwritten; neither overlaps an input. Asynchronous,
+ * allocation-free; errors as fa2_fwd_ws.
+ */
+FA2_API int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* key_lengths,
+                          int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, int dtype, void* workspace,
+                          size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * fa2_cross_fwd_workspace_bytes — bytes of device workspace fa2_cross_fwd
+ * takes on the current device for head dimension D, whatever the other sizes.
+ * Returns FA2_OK, FA2_ERR_INVALID_ARG (bytes NULL), FA2_ERR_UNSUPPORTED or
+ * FA2_ERR_CUDA.
+ */
+FA2_API int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes);
+
+/*
+ * fa2_cross_bwd — the gradient of fa2_cross_fwd's O with respect to Q, K and
+ * V for an upstream gradient dO, as fa2_bwd computes it, over keys of another
+ * length:
+ *   dV = P^T dO,  dP = dO V^T,  Delta_i = <dO_i, O_i>,  dS = P * (dP - Delta)
+ *   dQ = scale * dS K,  dK = scale * dS^T Q
+ * dK and dV of a key head are sums over its Hq / Hkv query heads.
+ *
+ * Q, K, V, key_lengths, scale: the forward's. O, LSE: its outputs for them.
+ * dO, dQ    : device pointers, contiguous [B, Hq, Nq, D] of `dtype`.
+ * dK, dV    : device pointers, contiguous [B, Hkv, Nk, D] of `dtype`. Rows
+ *             behind a batch entry's keys are zeros, as is dQ of rows without
+ *             keys; K and V there are never used.
+ * workspace : device memory of at least fa2_cross_bwd_workspace_bytes(...)
+ *             bytes, 256-byte aligned; scratch, needs no initialisation, not
+ *             shared by calls that run at the same time. May be NULL where
+ *             there is no query or no key (every gradient is zero then).
+ * Every gradient is fully overwritten, rounded to nearest-even, and overlaps
+ * nothing. dQ is summed with fp32 atomic adds in no fixed order; dK and dV
+ * are summed in a fixed one. The other arguments and the errors are
+ * fa2_cross_fwd's, with FA2_ERR_INVALID_ARG for a missing workspace.
+ */
+FA2_API int fa2_cross_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                          const float* LSE, void* dQ, void* dK, void* dV, const int* key_lengths, int B, int Hq,
+                          int Hkv, int Nq, int Nk, int D, float scale, int dtype, void* workspace,
+                          size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * fa2_cross_bwd_workspace_bytes — bytes of device workspace fa2_cross_bwd
+ * needs: an fp32 dQ accumulator, two fp32 statistics per query row, and the
+ * partial dK, dV of cut units. Needs no device. Returns FA2_OK,
+ * FA2_ERR_INVALID_ARG or FA2_ERR_UNSUPPORTED.
+ */
+FA2_API int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, size_t* bytes);
+
+/*
  * fa2_device_status — read the device-side watchdog word of the current
  * device, synchronising `stream` first. *status receives 0 when no kernel of
  * this library has timed out waiting on one of its internal barriers since
