@@ -12,7 +12,7 @@ import ctypes
 import math
 
 from .binding import FA2_OK, _check, _dtype_code_of, library
-from .streams import empty_on, launch_stream
+from .streams import empty_on, on_device, scratch_for, stream_handle
 
 _fwd_bytes = {}
 
@@ -31,44 +31,41 @@ def fa2_cross_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, D
 
 
 def _check_inputs(q, k, v, key_lengths):
-    """(B, Hq, Hkv, Nq, Nk, D) of a call, after the checks the C ABI cannot make."""
-    import torch
-    if not (q.is_cuda and k.is_cuda and v.is_cuda):
-        raise ValueError("q, k, v must be CUDA tensors")
-    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape:
+    """(B, Hq, Hkv, Nq, Nk, D, device index) of a call, after the checks the C ABI cannot make."""
+    dev = q.get_device()
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k, v must be CUDA tensors on one device")
+    ks = k.shape
+    if q.dim() != 4 or len(ks) != 4 or v.shape != ks:
         raise ValueError("q must be [B, Hq, Nq, D], and k, v of one shape [B, Hkv, Nk, D]")
     B, Hq, Nq, D = q.shape
-    if k.shape[0] != B or k.shape[3] != D:
+    _, Hkv, Nk, _ = ks
+    if ks[0] != B or ks[3] != D:
         raise ValueError("q, k, v must share B and D")
-    Hkv, Nk = k.shape[1], k.shape[2]
     if Hkv == 0 or Hq % Hkv:
         raise ValueError(f"the {Hq} query heads must be a multiple of the {Hkv} key heads")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt:
         raise ValueError("q, k, v must share one dtype")
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
         raise ValueError("q, k, v must be contiguous")
-    if k.device != q.device or v.device != q.device:
-        raise ValueError("q, k, v must be on one device")
-    if key_lengths is not None and (key_lengths.shape != (B,) or key_lengths.dtype != torch.int32 or
-                                    not key_lengths.is_contiguous() or key_lengths.device != q.device):
-        raise ValueError(f"key_lengths must be a contiguous int32 [{B}] tensor on q's device")
-    return B, Hq, Hkv, Nq, Nk, D
+    if key_lengths is not None:
+        import torch
+        if key_lengths.shape != (B,) or key_lengths.dtype != torch.int32 or not key_lengths.is_contiguous() or \
+                key_lengths.get_device() != dev:
+            raise ValueError(f"key_lengths must be a contiguous int32 [{B}] tensor on q's device")
+    return B, Hq, Hkv, Nq, Nk, D, dev
 
 
-def _like(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != device:
+def _like(name, t, shape, dtype, dev):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on q's device")
     return t
 
 
-def _workspace(workspace, need, s, stream, device):
-    import torch
-    if workspace is None:
-        return empty_on(s, stream, (max(need, 1),), torch.uint8, device)
-    if workspace.device != device or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < need:
+def _check_workspace(workspace, need, dev):
+    if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
         raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on q's device")
-    return workspace
 
 
 def cross_attention_forward(q, k, v, scale: float | None = None, key_lengths=None, out=None, lse=None,
@@ -80,28 +77,36 @@ def cross_attention_forward(q, k, v, scale: float | None = None, key_lengths=Non
     (default: all Nk); what lies behind them is never used. A row without any
     key gives O = 0 and LSE = +inf.
     out, lse: caller-owned outputs. workspace: a uint8 CUDA tensor of at least
-    fa2_cross_fwd_workspace_bytes(D) bytes (allocated per call otherwise).
+    fa2_cross_fwd_workspace_bytes(D) bytes (by default one is kept for each
+    device, head dim and current stream; a captured call, and one that names
+    its stream, gets its own).
     Runs on `stream` (a torch.cuda.Stream) or the current stream.
     """
     import torch
-    B, Hq, Hkv, Nq, Nk, D = _check_inputs(q, k, v, key_lengths)
-    dtc = _dtype_code_of(q.dtype)
-    dev = q.device
-    s = launch_stream(dev, stream, (q, k, v, key_lengths, out, lse, workspace))
-    out = empty_on(s, stream, q.shape, q.dtype, dev) if out is None else _like("out", out, q.shape, q.dtype, dev)
-    lse_shape = (B, Hq, Nq)
-    lse = empty_on(s, stream, lse_shape, torch.float32, dev) if lse is None else \
-        _like("lse", lse, lse_shape, torch.float32, dev)
+    B, Hq, Hkv, Nq, Nk, D, dev = _check_inputs(q, k, v, key_lengths)
+    dt = q.dtype
+    dtc = _dtype_code_of(dt)
+    if out is not None:
+        _like("out", out, q.shape, dt, dev)
+    if lse is not None:
+        _like("lse", lse, (B, Hq, Nq), torch.float32, dev)
+    handle = stream_handle(dev, stream, (q, k, v, key_lengths, out, lse, workspace))
+    if out is None:
+        out = empty_on(stream, q.shape, dt, q.device)
+    if lse is None:
+        lse = empty_on(stream, (B, Hq, Nq), torch.float32, q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with torch.cuda.device(dev):
-        need = _fwd_bytes.get((dev.index, D))
-        if need is None:
-            need = _fwd_bytes[(dev.index, D)] = fa2_cross_fwd_workspace_bytes(D)
-        ws = _workspace(workspace, need, s, stream, dev)
-        code = library().fa2_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                       None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk,
-                                       D, scale, dtc, ws.data_ptr(), ws.numel() * ws.element_size(), s.cuda_stream)
+    need = _fwd_bytes.get((dev, D))
+    if need is None:
+        need = _fwd_bytes[(dev, D)] = on_device(dev, fa2_cross_fwd_workspace_bytes, D)
+    if workspace is None:
+        workspace = scratch_for("cross_fwd", need, q.device, dev, handle, stream)
+    else:
+        _check_workspace(workspace, need, dev)
+    code = on_device(dev, library().fa2_cross_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                     lse.data_ptr(), None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk, D,
+                     scale, dtc, workspace.data_ptr(), workspace.nbytes, handle)
     if code != FA2_OK:
         _check(code, "fa2_cross_fwd")
     return out, lse
@@ -119,24 +124,33 @@ def cross_attention_backward(q, k, v, o, lse, do, scale: float | None = None, ke
     (allocated per call otherwise).
     """
     import torch
-    B, Hq, Hkv, Nq, Nk, D = _check_inputs(q, k, v, key_lengths)
-    dtc = _dtype_code_of(q.dtype)
-    dev = q.device
-    for name, t in (("o", o), ("do", do)):
-        _like(name, t, q.shape, q.dtype, dev)
+    B, Hq, Hkv, Nq, Nk, D, dev = _check_inputs(q, k, v, key_lengths)
+    dt = q.dtype
+    dtc = _dtype_code_of(dt)
+    _like("o", o, q.shape, dt, dev)
+    _like("do", do, q.shape, dt, dev)
     _like("lse", lse, (B, Hq, Nq), torch.float32, dev)
-    s = launch_stream(dev, stream, (q, k, v, o, lse, do, key_lengths, dq, dk, dv, workspace))
-    outs = []
-    for name, t, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        outs.append(empty_on(s, stream, x.shape, x.dtype, dev) if t is None else _like(name, t, x.shape, x.dtype, dev))
+    for name, t, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+        if t is not None:
+            _like(name, t, x.shape, dt, dev)
+    handle = stream_handle(dev, stream, (q, k, v, o, lse, do, key_lengths, dq, dk, dv, workspace))
+    if dq is None:
+        dq = empty_on(stream, q.shape, dt, q.device)
+    if dk is None:
+        dk = empty_on(stream, k.shape, dt, q.device)
+    if dv is None:
+        dv = empty_on(stream, k.shape, dt, q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    ws = _workspace(workspace, fa2_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, D), s, stream, dev)
-    with torch.cuda.device(dev):
-        code = library().fa2_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                       lse.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
-                                       None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk,
-                                       D, scale, dtc, ws.data_ptr(), ws.numel() * ws.element_size(), s.cuda_stream)
+    need = fa2_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, D)
+    if workspace is None:  # as large as the queries: a call's own
+        workspace = empty_on(stream, max(need, 1), torch.uint8, q.device)
+    else:
+        _check_workspace(workspace, need, dev)
+    code = on_device(dev, library().fa2_cross_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                     do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                     None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk, D, scale, dtc,
+                     workspace.data_ptr(), workspace.nbytes, handle)
     if code != FA2_OK:
         _check(code, "fa2_cross_bwd")
-    return tuple(outs)
+    return dq, dk, dv

@@ -20,7 +20,7 @@ struct CrossStart {
   long long total;    // K/V-tile steps of the whole call
   long long b_start;  // first step of batch entry b
   int b;              // batch entry that holds the share's first step
-  int shares;         // CTAs with a share: min(grid, total)
+  int shares;         // CTAs with a share: at most the grid, and total / the least share
 };
 
 struct CrossCursor {
@@ -39,17 +39,22 @@ __device__ __forceinline__ long long cross_share_begin(const CrossStart& st, int
   return c >= st.shares ? st.total : st.total * c / st.shares;
 }
 
+__device__ __forceinline__ int cross_shares(long long total, int least) {
+  return static_cast<int>(min(static_cast<long long>(gridDim.x), total > 0 ? max(total / least, 1ll) : 0ll));
+}
+
 // By one whole warp: the total, then the batch entry of this CTA's first step
 // (32 entries at a time: a shuffle scan of their steps). `steps(b)` are the
-// steps of batch entry b, the same for all entries when `uniform`.
+// steps of batch entry b, the same for all entries when `uniform`; a share is
+// at least `least` steps.
 template <typename F>
-__device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, F&& steps) {
+__device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, int least, F&& steps) {
   CrossStart st;
   const int lane = threadIdx.x & 31;
   if (uniform) {
     const long long per = steps(0);
     st.total = per * B;
-    st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), st.total));
+    st.shares = cross_shares(st.total, least);
     st.b = static_cast<int>(min(cross_share_begin(st, blockIdx.x) / per, static_cast<long long>(B - 1)));
     st.b_start = per * st.b;
     return st;
@@ -59,7 +64,7 @@ __device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, F&& 
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   st.total = sum;
-  st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), st.total));
+  st.shares = cross_shares(st.total, least);
   st.b = 0;
   st.b_start = 0;
   const long long want = cross_share_begin(st, blockIdx.x);
@@ -88,7 +93,7 @@ __device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, F&& 
 // The forward's start; the round schedule needs none.
 __device__ __forceinline__ CrossStart cross_fwd_start(const CrossParams& p) {
   if (!p.stream_k) return CrossStart{0, 0, 0, 0};
-  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_batch_steps(p, b); });
+  return cross_find_start(p.B, !p.key_lengths, 1, [&](int b) { return cross_batch_steps(p, b); });
 }
 
 __device__ __forceinline__ CrossCursor cross_first_cursor(const CrossParams& p, const CrossStart& st) {
@@ -154,7 +159,7 @@ __device__ __forceinline__ long long cross_bwd_batch_steps(const CrossBwdParams&
 
 __device__ __forceinline__ CrossStart cross_bwd_start(const CrossBwdParams& p) {
   if (!p.stream_k) return CrossStart{0, 0, 0, 0};
-  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_bwd_batch_steps(p, b); });
+  return cross_find_start(p.B, !p.key_lengths, 1, [&](int b) { return cross_bwd_batch_steps(p, b); });
 }
 
 __device__ __forceinline__ CrossCursor cross_bwd_first_cursor(const CrossBwdParams& p, const CrossStart& st) {

@@ -36,6 +36,24 @@ template <int D, bool kBf16>
 cudaError_t launch_cross_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                              const CrossParams& p, int grid, cudaStream_t stream);
 
+// Few query rows per key head (fa2_cross_rows.cu): 16 at most, 128 keys per
+// tile, 16 of them for each of a CTA's 8 warps.
+constexpr int kFewRows = 16;
+constexpr int kFewRowsKeys = 128;
+constexpr int kFewRowsMaxCtas = 256;  // what a cut unit's holder has room to join
+struct CrossRowsParams : CrossParams {  // ws_o: [grid][16][D], ws_stats: [grid][3][16], ws_flags: [grid]
+  const void* q;
+};
+
+constexpr size_t few_rows_workspace_bytes(int grid, int d) {
+  return (static_cast<size_t>(grid) * kFewRows * (d + 3) * sizeof(float) + 255) / 256 * 256 +
+         static_cast<size_t>(grid) * 8;
+}
+
+// k, v: maps with boxes of 16 rows x 64 elements.
+cudaError_t launch_cross_rows(int D, bool bf16, const CUtensorMap& k, const CUtensorMap& v, const CrossRowsParams& p,
+                              int grid, cudaStream_t stream);
+
 // The backward on the tensor-core kernel of fa2_bwd_kernel.cuh.
 template <int D, bool kBf16>
 cudaError_t launch_cross_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,

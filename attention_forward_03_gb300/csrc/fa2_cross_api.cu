@@ -47,6 +47,11 @@ bool cross_balanced(long long units, long long nkv, bool lengths, int sms) {
   return balanced < 0.95 * rounds;
 }
 
+// The larger of the two kernels' partial results.
+size_t workspace_bytes_for(int sms, int D) {
+  return std::max(stream_k_workspace_bytes(sms, D), few_rows_workspace_bytes(sms, D));
+}
+
 }  // namespace
 }  // namespace fa2
 
@@ -59,7 +64,7 @@ extern "C" int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes) {
   int* status = nullptr;
   const int rc = current_device_facts(&sms, &status);
   if (rc != FA2_OK) return rc;
-  *bytes = stream_k_workspace_bytes(sms, D);
+  *bytes = workspace_bytes_for(sms, D);
   return FA2_OK;
 }
 
@@ -99,7 +104,7 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   int* status = nullptr;
   const int rc = current_device_facts(&sms, &status);
   if (rc != FA2_OK) return rc;
-  if (workspace && workspace_bytes < stream_k_workspace_bytes(sms, D)) return FA2_ERR_INVALID_ARG;
+  if (workspace && workspace_bytes < workspace_bytes_for(sms, D)) return FA2_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
   if (Nk == 0) {
@@ -111,32 +116,47 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
     return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
   }
 
-  CUtensorMap mq, mk, mv, mo;
-  if (!encode_tile_map(&mq, Q, (int)bh, (int)rows, D, dtype, 128u) || !encode_tile_map(&mk, K, (int)bh, Nk, D, dtype, 128u) ||
-      !encode_tile_map(&mv, V, (int)bh, Nk, D, dtype, 128u) || !encode_tile_map(&mo, O, (int)bh, (int)rows, D, dtype, 128u))
-    return record_cuda_error(cudaErrorInvalidValue);
-  CrossParams p = {};
+  CrossRowsParams p = {};
   p.o = O;
   p.lse = LSE;
   p.status = status;
   p.watchdog_ns = watchdog_limit_ns();
   p.N = (int)rows;
   p.BH = (int)bh;
-  p.n_qt = (int)n_qt;
-  p.num_units = (int)(bh * n_qt);
-  p.nkv_full = (Nk + kKeys - 1) / kKeys;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.test_withhold = take_test_withhold();
   p.Nk = Nk;
   p.B = B;
   p.heads = Hkv;
   p.key_lengths = key_lengths;
+  char* const ws = static_cast<char*>(workspace);
+  if (workspace && rows <= kFewRows) {
+    const int grid = static_cast<int>(
+        std::min<long long>(std::min(sms, kFewRowsMaxCtas), bh * ((static_cast<long long>(Nk) + kFewRowsKeys - 1) / kFewRowsKeys)));
+    CUtensorMap mk, mv;
+    if (!encode_tile_map(&mk, K, (int)bh, Nk, D, dtype, 16u) || !encode_tile_map(&mv, V, (int)bh, Nk, D, dtype, 16u))
+      return record_cuda_error(cudaErrorInvalidValue);
+    p.q = Q;
+    p.ws_o = reinterpret_cast<float*>(ws);
+    p.ws_stats = p.ws_o + static_cast<size_t>(grid) * kFewRows * D;
+    p.ws_flags = reinterpret_cast<unsigned long long*>(ws + few_rows_workspace_bytes(grid, D) - static_cast<size_t>(grid) * 8);
+    p.epoch = next_launch_epoch();
+    const cudaError_t e = launch_cross_rows(D, dtype == FA2_BF16, mk, mv, p, grid, s);
+    return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
+  }
+
+  CUtensorMap mq, mk, mv, mo;
+  if (!encode_tile_map(&mq, Q, (int)bh, (int)rows, D, dtype, 128u) || !encode_tile_map(&mk, K, (int)bh, Nk, D, dtype, 128u) ||
+      !encode_tile_map(&mv, V, (int)bh, Nk, D, dtype, 128u) || !encode_tile_map(&mo, O, (int)bh, (int)rows, D, dtype, 128u))
+    return record_cuda_error(cudaErrorInvalidValue);
+  p.n_qt = (int)n_qt;
+  p.num_units = (int)(bh * n_qt);
+  p.nkv_full = (Nk + kKeys - 1) / kKeys;
+  p.test_withhold = take_test_withhold();
   int grid;
   if (workspace && cross_balanced(p.num_units, p.nkv_full, key_lengths != nullptr, sms)) {
     p.stream_k = 1;
     grid = static_cast<int>(std::min<long long>(sms, static_cast<long long>(p.num_units) * p.nkv_full));
     const size_t slots = static_cast<size_t>(sms) * kSubTiles;
-    char* ws = static_cast<char*>(workspace);
     p.ws_o = reinterpret_cast<float*>(ws);
     p.ws_stats = p.ws_o + slots * D * 128;
     p.ws_flags = reinterpret_cast<unsigned long long*>(

@@ -14,10 +14,12 @@ import ctypes
 
 from .binding import Fa2Error  # noqa: F401  (what these calls raise)
 from .binding import _check, _dtype_code_of, library
-from .streams import empty_on, launch_stream
+from .streams import empty_on, on_device, scratch_for, stream_handle
 
 _F_ARGS = ctypes.c_longlong * 14
 _B_ARGS = ctypes.c_longlong * 20
+_NO_VIEW = (0, 0, 0)
+_bwd_bytes = {}
 
 
 def fa2_qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
@@ -27,88 +29,91 @@ def fa2_qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
     return n.value
 
 
-def _strides(t):
-    """(batch, head, token) strides of a view, for the C call."""
-    if t is None:
-        return 0, 0, 0
-    s = t.stride()
-    return s[0], s[1], s[2]
-
-
-def _check_view(name, t, like, shape):
-    if t.dim() != 4 or t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
+def _check_view(name, t, B, H, N, D, dt, dev):
+    """(batch, head, token) strides of a [B, H, N, D] view, which has the dtype and device of the call."""
+    if t.shape != (B, H, N, D):
+        raise ValueError(f"{name} must have the shape {[B, H, N, D]}")
+    if t.dtype != dt or t.get_device() != dev:
         raise ValueError(f"{name} must have the dtype and device of q and k")
-    if t.stride(3) != 1 and shape[3] > 1:
+    sb, sh, sn, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    return sb, sh, sn
 
 
 def _check_sides(q, k):
-    """The present one of q and k (for device, dtype and sizes), the head counts, and B, N, D."""
+    """(like, Hq, Hkv, B, N, D, dtype, device index, q's strides, k's strides); `like` is the present one of q and k."""
     like = q if q is not None else k
     if like is None:
         raise ValueError("at least one of q and k is needed")
-    if like.dim() != 4 or not like.is_cuda:
+    dev = like.get_device()
+    if like.dim() != 4 or dev < 0:
         raise ValueError("q and k must be CUDA tensors [B, H, N, D]")
-    B, _, N, D = like.shape
-    heads = []
-    for name, t in (("q", q), ("k", k)):
-        if t is None:
-            heads.append(0)
-            continue
-        if t.dim() != 4:
+    B, Hq, N, D = like.shape
+    dt = like.dtype
+    Hkv = 0
+    qs = ks = _NO_VIEW
+    if q is not None:
+        qs = _check_view("q", q, B, Hq, N, D, dt, dev)
+    else:
+        Hq = 0
+    if k is not None:
+        if k.dim() != 4:
             raise ValueError("q and k must be CUDA tensors [B, H, N, D]")
-        _check_view(name, t, like, (B, t.shape[1], N, D))
-        heads.append(t.shape[1])
-    return like, heads[0], heads[1], B, N, D
+        Hkv = k.shape[1]
+        ks = _check_view("k", k, B, Hkv, N, D, dt, dev)
+    return like, Hq, Hkv, B, N, D, dt, dev, qs, ks
 
 
-def _check_gains(q_gain, k_gain, like, D):
+def _check_gains(q_gain, k_gain, D, dt, dev):
     """Nonzero when the gains are float32. Both have one dtype: float32 or that of q and k."""
     import torch
     kind = None
-    for name, w in (("q_gain", q_gain), ("k_gain", k_gain)):
+    for w in (q_gain, k_gain):
         if w is None:
             continue
-        if w.shape != (D,) or not w.is_contiguous() or w.device != like.device:
-            raise ValueError(f"{name} must be a contiguous [{D}] tensor on the device of q and k")
-        if w.dtype != torch.float32 and w.dtype != like.dtype:
-            raise ValueError(f"{name} must be float32 or of the dtype of q and k")
-        if kind is not None and w.dtype != kind:
+        wt = w.dtype
+        if w.shape != (D,) or not w.is_contiguous() or w.get_device() != dev:
+            raise ValueError(f"a gain must be a contiguous [{D}] tensor on the device of q and k")
+        if wt != torch.float32 and wt != dt:
+            raise ValueError("a gain must be float32 or of the dtype of q and k")
+        if kind is not None and wt != kind:
             raise ValueError("q_gain and k_gain must share one dtype")
-        kind = w.dtype
-    return int(kind == torch.float32)
+        kind = wt
+    return 1 if kind == torch.float32 else 0
 
 
-def _check_tables(cos, sin, positions, like, B, N):
+def _check_tables(cos, sin, positions, B, N, dev):
     """(rot, table rows, positions are int64, strides of positions)."""
     import torch
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin must be given together")
-    if cos is None:
+    if cos is None or sin is None:
+        if cos is not sin:
+            raise ValueError("cos and sin must be given together")
         if positions is not None:
             raise ValueError("positions need cos and sin")
         return 0, 0, 0, 0, 0
-    for name, t in (("cos", cos), ("sin", sin)):
-        if t.dim() != 2 or t.dtype != torch.float32 or not t.is_contiguous() or t.device != like.device:
-            raise ValueError(f"{name} must be a contiguous float32 [rows, rot / 2] tensor on the device of q and k")
-    if cos.shape != sin.shape:
-        raise ValueError("cos and sin must share one shape")
-    rows, half = cos.shape
+    shape = cos.shape
+    if len(shape) != 2 or sin.shape != shape:
+        raise ValueError("cos and sin must share one shape [rows, rot / 2]")
+    f32 = torch.float32
+    if cos.dtype != f32 or sin.dtype != f32 or not cos.is_contiguous() or not sin.is_contiguous() or \
+            cos.get_device() != dev or sin.get_device() != dev:
+        raise ValueError("cos and sin must be contiguous float32 tensors on the device of q and k")
+    rows, half = shape
     if positions is None:
         if rows < N:
             raise ValueError(f"the tables have {rows} rows; without positions {N} are needed")
         return 2 * half, rows, 0, 0, 0
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != like.device:
+    pt = positions.dtype
+    if (pt != torch.int64 and pt != torch.int32) or positions.get_device() != dev:
         raise ValueError("positions must be int32 or int64 on the device of q and k")
-    if positions.shape == (N,):
-        strides = 0, positions.stride(0)
-    elif positions.shape == (B, N):
-        strides = positions.stride()
+    if positions.shape == (B, N):
+        pb, pn = positions.stride()
+    elif positions.shape == (N,):
+        pb, pn = 0, positions.stride(0)
     else:
         raise ValueError(f"positions must be [{B}, {N}] or [{N}]")
-    return 2 * half, rows, int(positions.dtype == torch.int64), strides[0], strides[1]
+    return 2 * half, rows, 1 if pt == torch.int64 else 0, pb, pn
 
 
 def _ptr(t):
@@ -133,32 +138,35 @@ def qk_norm_rope_forward(q, k, q_gain=None, k_gain=None, cos=None, sin=None, pos
     its own input. Contiguous tensors are allocated otherwise.
     Runs on `stream` (a torch.cuda.Stream) or the current stream.
     """
-    import torch
-    like, Hq, Hkv, B, N, D = _check_sides(q, k)
-    gain_f32 = _check_gains(q_gain, k_gain, like, D)
-    rot, rows, p64, pb, pn = _check_tables(cos, sin, positions, like, B, N)
-    dtc = _dtype_code_of(like.dtype)
-    dev = like.device
-    s = launch_stream(dev, stream, (q, k, q_gain, k_gain, cos, sin, positions, q_out, k_out))
-    outs = []
-    for name, x, out in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{name} was given without its input")
-        elif out is None:
-            out = empty_on(s, stream, x.shape, x.dtype, dev)
-        else:
-            _check_view(name, out, like, x.shape)
-        outs.append(out)
-    strides = _F_ARGS(*_strides(q), *_strides(k), *_strides(outs[0]), *_strides(outs[1]), pb, pn)
-    with torch.cuda.device(dev):
-        code = library().fa2_qk_norm_rope_fwd(_ptr(q), _ptr(k), _ptr(q_gain), _ptr(k_gain), _ptr(cos), _ptr(sin),
-                                              _ptr(positions), _ptr(outs[0]), _ptr(outs[1]), strides, B, Hq, Hkv, N,
-                                              D, rot, rows, eps, 1 if interleaved else 0, gain_f32, p64, dtc,
-                                              s.cuda_stream)
+    like, Hq, Hkv, B, N, D, dt, dev, qs, ks = _check_sides(q, k)
+    gain_f32 = _check_gains(q_gain, k_gain, D, dt, dev)
+    rot, rows, p64, pb, pn = _check_tables(cos, sin, positions, B, N, dev)
+    dtc = _dtype_code_of(dt)
+    handle = stream_handle(dev, stream, (q, k, q_gain, k_gain, cos, sin, positions, q_out, k_out))
+    qos = kos = _NO_VIEW
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out was given without q")
+    elif q_out is None:
+        q_out = empty_on(stream, (B, Hq, N, D), dt, like.device)
+        qos = (Hq * N * D, N * D, D)
+    else:
+        qos = _check_view("q_out", q_out, B, Hq, N, D, dt, dev)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out was given without k")
+    elif k_out is None:
+        k_out = empty_on(stream, (B, Hkv, N, D), dt, like.device)
+        kos = (Hkv * N * D, N * D, D)
+    else:
+        kos = _check_view("k_out", k_out, B, Hkv, N, D, dt, dev)
+    strides = _F_ARGS(*qs, *ks, *qos, *kos, pb, pn)
+    code = on_device(dev, library().fa2_qk_norm_rope_fwd, _ptr(q), _ptr(k), _ptr(q_gain), _ptr(k_gain), _ptr(cos),
+                     _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), strides, B, Hq, Hkv, N, D, rot, rows, eps,
+                     1 if interleaved else 0, gain_f32, p64, dtc, handle)
     if code:
         _check(code, "fa2_qk_norm_rope_fwd")
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain=None, k_gain=None, cos=None, sin=None, positions=None,
@@ -172,48 +180,58 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain=None, k_gain=None, cos=No
     dq, dk: views to write to, for instance the parts of a packed projection's
     gradient; each may be exactly its upstream gradient or its input.
     workspace: optional uint8 CUDA tensor of at least
-    fa2_qk_norm_rope_bwd_workspace_bytes(D) bytes (allocated per call otherwise).
+    fa2_qk_norm_rope_bwd_workspace_bytes(D) bytes (by default one is kept for
+    each device, head dim and current stream; a captured call, and one that
+    names its stream, gets its own).
     """
-    import torch
-    like, Hq, Hkv, B, N, D = _check_sides(q, k)
-    gain_f32 = _check_gains(q_gain, k_gain, like, D)
-    rot, rows, p64, pb, pn = _check_tables(cos, sin, positions, like, B, N)
-    dtc = _dtype_code_of(like.dtype)
-    dev = like.device
-    s = launch_stream(dev, stream, (dq_out, dk_out, q, k, q_gain, k_gain, cos, sin, positions, dq, dk, workspace))
-    outs, gains = [], []
-    for i, x, g, out, w in (("q", q, dq_out, dq, q_gain), ("k", k, dk_out, dk, k_gain)):
-        if x is None:
-            if g is not None or out is not None or w is not None:
-                raise ValueError(f"d{i}_out, d{i} and {i}_gain need {i}")
-        else:
-            if g is None:
-                raise ValueError(f"d{i}_out is needed with {i}")
-            _check_view(f"d{i}_out", g, like, x.shape)
-            if out is None:
-                out = empty_on(s, stream, x.shape, x.dtype, dev)
-            else:
-                _check_view(f"d{i}", out, like, x.shape)
-        outs.append(out)
-        gains.append(None if w is None else empty_on(s, stream, (D,), w.dtype, dev))
-    if q_gain is None and k_gain is None:
-        need = 0
+    like, Hq, Hkv, B, N, D, dt, dev, qs, ks = _check_sides(q, k)
+    gain_f32 = _check_gains(q_gain, k_gain, D, dt, dev)
+    rot, rows, p64, pb, pn = _check_tables(cos, sin, positions, B, N, dev)
+    dtc = _dtype_code_of(dt)
+    handle = stream_handle(dev, stream, (dq_out, dk_out, q, k, q_gain, k_gain, cos, sin, positions, dq, dk, workspace))
+    device = like.device
+    gqs = gks = dqs = dks = _NO_VIEW
+    dq_gain = dk_gain = None
+    if q is None:
+        if dq_out is not None or dq is not None or q_gain is not None:
+            raise ValueError("dq_out, dq and q_gain need q")
     else:
-        need = fa2_qk_norm_rope_bwd_workspace_bytes(D)
+        if dq_out is None:
+            raise ValueError("dq_out is needed with q")
+        gqs = _check_view("dq_out", dq_out, B, Hq, N, D, dt, dev)
+        if dq is None:
+            dq = empty_on(stream, (B, Hq, N, D), dt, device)
+        dqs = _check_view("dq", dq, B, Hq, N, D, dt, dev)
+        if q_gain is not None:
+            dq_gain = empty_on(stream, (D,), q_gain.dtype, device)
+    if k is None:
+        if dk_out is not None or dk is not None or k_gain is not None:
+            raise ValueError("dk_out, dk and k_gain need k")
+    else:
+        if dk_out is None:
+            raise ValueError("dk_out is needed with k")
+        gks = _check_view("dk_out", dk_out, B, Hkv, N, D, dt, dev)
+        if dk is None:
+            dk = empty_on(stream, (B, Hkv, N, D), dt, device)
+        dks = _check_view("dk", dk, B, Hkv, N, D, dt, dev)
+        if k_gain is not None:
+            dk_gain = empty_on(stream, (D,), k_gain.dtype, device)
+    ws_ptr, ws_bytes = None, 0
+    if q_gain is not None or k_gain is not None:
+        need = _bwd_bytes.get(D)
+        if need is None:
+            need = _bwd_bytes[D] = fa2_qk_norm_rope_bwd_workspace_bytes(D)
         if workspace is None:
-            workspace = empty_on(s, stream, (need,), torch.uint8, dev)
-        elif workspace.device != dev or not workspace.is_contiguous() or \
+            workspace = scratch_for("norm_rope_bwd", need, device, dev, handle, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous() or \
                 workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on q's device")
-    ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if need else (None, 0)
-    strides = _B_ARGS(*_strides(dq_out), *_strides(dk_out), *_strides(q), *_strides(k), *_strides(outs[0]),
-                      *_strides(outs[1]), pb, pn)
-    with torch.cuda.device(dev):
-        code = library().fa2_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_gain),
-                                              _ptr(k_gain), _ptr(cos), _ptr(sin), _ptr(positions), _ptr(outs[0]),
-                                              _ptr(outs[1]), _ptr(gains[0]), _ptr(gains[1]), strides, B, Hq, Hkv, N,
-                                              D, rot, rows, eps, 1 if interleaved else 0, gain_f32, p64, dtc, ws_ptr,
-                                              ws_bytes, s.cuda_stream)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    strides = _B_ARGS(*gqs, *gks, *qs, *ks, *dqs, *dks, pb, pn)
+    code = on_device(dev, library().fa2_qk_norm_rope_bwd, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_gain),
+                     _ptr(k_gain), _ptr(cos), _ptr(sin), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dq_gain),
+                     _ptr(dk_gain), strides, B, Hq, Hkv, N, D, rot, rows, eps, 1 if interleaved else 0, gain_f32, p64,
+                     dtc, ws_ptr, ws_bytes, handle)
     if code:
         _check(code, "fa2_qk_norm_rope_bwd")
-    return outs[0], outs[1], gains[0], gains[1]
+    return dq, dk, dq_gain, dk_gain

@@ -1,31 +1,73 @@
-"""The stream a call runs on, and the tensors that are made for it.
+"""The stream and device a call runs on, and the tensors that are made for it.
 
 torch's allocator hands a freed block to later work of the stream that the
 block was allocated on. A call on another stream than the current one
 therefore tells the allocator about its inputs (record_stream), and makes its
 outputs and scratch on the stream that writes them.
+
+The checks of a small call cost more than its kernel, so these helpers stay
+with the cheap queries: device indices instead of torch.device objects, the
+current stream's handle instead of a Stream object, and the device switched
+only where it is not the current one (measured on a call of 12 heads: 26 us
+before, of which the library's own share is 5 us).
 """
 from __future__ import annotations
 
 
-def launch_stream(device, stream, tensors):
-    """`stream`, or the current stream of `device`; records `tensors` (None skipped) on a stream that is not current."""
-    import torch
-    cur = torch.cuda.current_stream(device)
-    if stream is None or stream == cur:
-        return cur
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+def stream_handle(index: int, stream, tensors) -> int:
+    """The handle of `stream`, or of the current stream of device `index`; records `tensors` (None skipped) on a given one."""
+    if stream is None:
+        return current_handle(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream is on device {stream.device_index}, the tensors on {index}")
     for t in tensors:
         if t is not None and t.is_cuda:
             t.record_stream(stream)
-    return stream
+    return stream.cuda_stream
 
 
-def empty_on(s, stream, shape, dtype, device):
-    """An uninitialised tensor that belongs to the call's stream `s` (`stream`: the caller's argument)."""
+def current_handle(index: int) -> int:
+    """The handle of the current stream of device `index`, by torch's query for it alone where there is one."""
+    global current_handle
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    current_handle = raw if raw is not None else (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return current_handle(index)
+
+
+def empty_on(stream, shape, dtype, device):
+    """An uninitialised tensor that belongs to the call's stream (`stream`: the caller's argument)."""
     import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(s):
+    with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+_scratch = {}
+
+
+def scratch_for(kind, need, device, index, handle, stream):
+    """A workspace of `need` bytes for a call on stream `handle` of device `index`.
+
+    One per kind, size and current stream is kept: calls on one stream are
+    ordered, so they may share it. A call that names its stream, and one that
+    is being captured (two graphs may be replayed at once), gets its own.
+    """
+    import torch
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        return empty_on(stream, max(need, 1), torch.uint8, device)
+    key = (kind, need, index, handle)
+    ws = _scratch.get(key)
+    if ws is None:
+        ws = _scratch[key] = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return ws
+
+
+def on_device(index: int, fn, *args):
+    """fn(*args) with device `index` current (switched only where it is not)."""
+    import torch
+    if torch.cuda.current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)

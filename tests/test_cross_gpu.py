@@ -134,6 +134,12 @@ SHAPES = [  # B, Hq, Hkv, Nq, Nk, D, dtype, lengths
     (3, 6, 2, 200, 700, 128, BF16, [700, 16, 450]),
     (2, 5, 5, 513, 640, 96, BF16, None),
     (1, 16, 2, 1000, 1500, 64, BF16, [1200]),
+    (1, 1, 1, 1, 20000, 128, BF16, None),
+    (1, 16, 1, 1, 3001, 64, F16, None),
+    (2, 8, 8, 16, 1000, 96, BF16, [1000, 513]),
+    (2, 17, 1, 1, 700, 128, F16, [700, 64]),
+    (1, 8, 2, 4, 190, 128, BF16, None),
+    (300, 4, 2, 1, 256, 64, BF16, [(37 * i) % 257 for i in range(300)]),
     (70, 1, 1, 3, 90, 32, BF16, [(7 * i) % 91 for i in range(70)]),
     (40, 2, 2, 130, 260, 64, F16, [(13 * i) % 261 for i in range(40)]),
 ]
