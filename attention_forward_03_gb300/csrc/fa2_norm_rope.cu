@@ -23,6 +23,14 @@
 // cos and sin (32 bits each, as many bytes as the row itself) are read once
 // for all of them.
 //
+// Bytes in flight: rows come through shared memory by cp.async, 16 bytes at a
+// time, and every thread reads back only what it copied itself, so there is
+// no barrier and the depth costs no registers. The forward requests all rows
+// of its item at once, the backward runs four rows ahead across its items.
+// (Rows loaded into registers, four at a time: 37.7 us forward and 55.3 us
+// backward on the shapes below, at a quarter of the warps and 45 to 57 % of
+// the memory's rate.) Products run two at a time (f32x2).
+//
 // Sums, r and gain gradients are held in 32 bits. The 16-bit results are
 // rounded once, after the rotation.
 #include <cuda_bf16.h>
@@ -42,7 +50,7 @@ namespace {
 
 constexpr int kThreadsNr = 256;
 // Heads of one token per thread at most (see heads_per_item).
-constexpr int kMaxHeads = 8;
+constexpr int kMaxHeads = 8;  // a power of two
 
 // One of the two tensors (queries or keys) of a call. Strides in elements.
 struct NormRopeSide {
@@ -52,6 +60,7 @@ struct NormRopeSide {
   const void* gain;    // NULL: ones
   long long xb, xh, xn, gb, gh, gn, yb, yh, yn;
   int heads;
+  int per_item;        // heads per item, a power of two
   int slices;          // ceil(heads / heads per item)
 };
 
@@ -68,25 +77,51 @@ struct NormRopeParams {
   int D;
   int N;
   long long tokens;    // B * N
-  int heads_per_item;
+  int heads_per_item;  // the larger of the two sides'
   float eps;
   // backward
   float* partials;     // [grid][D] gain-gradient sums of each block
   int q_blocks;        // blocks [0, q_blocks) take the queries, the rest the keys
 };
 
-__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi, bool bf16) {
-  if (bf16) {
-    lo = __uint_as_float(w << 16);
-    hi = __uint_as_float(w & 0xffff0000u);
-  } else {
-    const __half2 h = *reinterpret_cast<const __half2*>(&w);
-    lo = __low2float(h);
-    hi = __high2float(h);
-  }
+// Two fp32 values in one 64-bit register pair.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void halves(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 swapped(F2 v) {
+  float a, b;
+  halves(v, a, b);
+  return pair(b, a);
+}
+__device__ __forceinline__ float sum2(F2 v) {
+  float a, b;
+  halves(v, a, b);
+  return a + b;
 }
 
-__device__ __forceinline__ uint32_t pack_2(float lo, float hi, bool bf16) {
+__device__ __forceinline__ F2 unpack2(uint32_t w, bool bf16) {
+  if (bf16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pair(f.x, f.y);
+}
+
+__device__ __forceinline__ uint32_t pack2h(F2 v, bool bf16) {
+  float lo, hi;
+  halves(v, lo, hi);
   if (bf16) {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
@@ -95,23 +130,42 @@ __device__ __forceinline__ uint32_t pack_2(float lo, float hi, bool bf16) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* f, bool bf16) {
-  unpack2(u.x, f[0], f[1], bf16);
-  unpack2(u.y, f[2], f[3], bf16);
-  unpack2(u.z, f[4], f[5], bf16);
-  unpack2(u.w, f[6], f[7], bf16);
+__device__ __forceinline__ void unpack8(const uint4& u, F2* f, bool bf16) {
+  f[0] = unpack2(u.x, bf16);
+  f[1] = unpack2(u.y, bf16);
+  f[2] = unpack2(u.z, bf16);
+  f[3] = unpack2(u.w, bf16);
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f, bool bf16) {
-  return make_uint4(pack_2(f[0], f[1], bf16), pack_2(f[2], f[3], bf16), pack_2(f[4], f[5], bf16),
-                    pack_2(f[6], f[7], bf16));
+__device__ __forceinline__ uint4 pack8(const F2* f, bool bf16) {
+  return make_uint4(pack2h(f[0], bf16), pack2h(f[1], bf16), pack2h(f[2], bf16), pack2h(f[3], bf16));
 }
 
-__device__ __forceinline__ float gain_at(const NormRopeParams& p, const void* gain, int i, bool bf16) {
-  if (!gain) return 1.f;
-  if (p.gain_f32) return static_cast<const float*>(gain)[i];
-  const uint16_t u = static_cast<const uint16_t*>(gain)[i];
-  return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// Gains of the 8 elements from i on (i a multiple of 8).
+__device__ __forceinline__ void load_gains(const NormRopeParams& p, const void* gain, int i, float* w, bool bf16) {
+  if (!gain) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
+  } else if (p.gain_f32) {
+    const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(gain) + i);
+    const float4 u = __ldg(g), v = __ldg(g + 1);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+  } else {
+    F2 f[4];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gain) + i)), f, bf16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) halves(f[e], w[2 * e], w[2 * e + 1]);
+  }
 }
 
 // The element offsets of the two 8-element chunks of chunk pair i (0 <= i <
@@ -156,30 +210,22 @@ __device__ __forceinline__ void load_angles(const NormRopeParams& p, long long p
   }
 }
 
-// Rotates the 16 elements of a chunk pair (f[0..7] at offset a, f[8..15] at
-// b) by the angles, or back (kBack).
-template <bool kInter, bool kBack>
-__device__ __forceinline__ void rotate16(float* f, const float* cs, const float* sn, int a, int b, int rot) {
+// What a pair of elements of chunk h (0: a, 1: b) is multiplied with in a
+// rotation by the angle (cs, sn): out = own * cos + partner * sin_signed,
+// where the partner is the same place of the other chunk (half-split) or the
+// pair's other element (interleaved). i: the pair of registers, 0..3.
+template <bool kInter>
+__device__ __forceinline__ void angle_factors(const float* cs, const float* sn, int h, int i, float& c0, float& c1,
+                                              float& s0, float& s1) {
   if (kInter) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if ((h ? b : a) >= rot) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float c = cs[4 * h + i], s = kBack ? -sn[4 * h + i] : sn[4 * h + i];
-        const float x = f[8 * h + 2 * i], y = f[8 * h + 2 * i + 1];
-        f[8 * h + 2 * i] = x * c - y * s;
-        f[8 * h + 2 * i + 1] = y * c + x * s;
-      }
-    }
-  } else if (a < rot) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = cs[i], s = kBack ? -sn[i] : sn[i];
-      const float x = f[i], y = f[8 + i];
-      f[i] = x * c - y * s;
-      f[8 + i] = y * c + x * s;
-    }
+    c0 = c1 = cs[4 * h + i];
+    s0 = -sn[4 * h + i];
+    s1 = sn[4 * h + i];
+  } else {
+    c0 = cs[2 * i];
+    c1 = cs[2 * i + 1];
+    s0 = h ? sn[2 * i] : -sn[2 * i];
+    s1 = h ? sn[2 * i + 1] : -sn[2 * i + 1];
   }
 }
 
@@ -189,81 +235,135 @@ __device__ __forceinline__ long long position_of(const NormRopeParams& p, long l
   return p.positions_64 ? static_cast<const long long*>(p.positions)[o] : static_cast<const int*>(p.positions)[o];
 }
 
+// Rows a thread of the forward has under way at most (its item's heads).
+template <int kPairs>
+constexpr int kFwdDepth = kMaxHeads / kPairs;
+// ... and of the backward (x and g of each).
+template <int kPairs>
+constexpr int kBwdDepth = 4 / kPairs;
+
+// The token, the first head and the number of heads of an item. Items of one
+// slice of heads are neighbouring tokens.
+struct Item {
+  int b, n, h0, heads;
+};
+__device__ __forceinline__ Item item_at(const NormRopeParams& p, const NormRopeSide& sd, unsigned item) {
+  const unsigned tokens = static_cast<unsigned>(p.tokens), slice = item / tokens, t = item - slice * tokens;
+  Item it;
+  it.b = static_cast<int>(t / static_cast<unsigned>(p.N));
+  it.n = static_cast<int>(t - static_cast<unsigned>(it.b) * p.N);
+  it.h0 = static_cast<int>(slice) * sd.per_item;
+  it.heads = min(sd.per_item, sd.heads - it.h0);
+  return it;
+}
+
 // A row's threads: kLanes of a warp (6 of 8 at D = 96), each with kPairs
 // chunk pairs. An item is one token and one slice of heads.
 template <int kLanes, int kPairs, bool kBf16, bool kInter>
 __global__ void __launch_bounds__(kThreadsNr) fa2_norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int kDepth = kFwdDepth<kPairs>;
+  extern __shared__ __align__(16) uint4 rows[];  // [depth][pairs][2][threads]
   const int lane = threadIdx.x % kLanes;
-  const long long q_items = p.tokens * p.side[0].slices;
-  const long long items = q_items + p.tokens * p.side[1].slices;
   const int per = p.D / 16;
-  long long item = (static_cast<long long>(blockIdx.x) * kThreadsNr + threadIdx.x) / kLanes;
+  const unsigned q_items = static_cast<unsigned>(p.tokens * p.side[0].slices);
+  const unsigned items = q_items + static_cast<unsigned>(p.tokens * p.side[1].slices);
+  unsigned item = blockIdx.x * (kThreadsNr / kLanes) + threadIdx.x / kLanes;
   const bool live = item < items && lane < per;
   if (item >= items) item = items - 1;  // whole warps take part in the shuffles
   const bool is_k = item >= q_items;
   if (is_k) item -= q_items;
   const NormRopeSide& sd = p.side[is_k ? 1 : 0];
-  const long long slice = item / p.tokens, t = item - slice * p.tokens;
-  const long long b = t / p.N;
-  const int n = static_cast<int>(t - b * p.N);
-  const int h0 = static_cast<int>(slice) * p.heads_per_item, h1 = min(h0 + p.heads_per_item, sd.heads);
+  const Item it = item_at(p, sd, item);
+  const uint16_t* x = sd.x + it.b * sd.xb + it.n * sd.xn + it.h0 * sd.xh;
+  uint16_t* y = sd.y + it.b * sd.yb + it.n * sd.yn + it.h0 * sd.yh;
+  const int heads = live ? it.heads : 0;
 
   int oa[kPairs], ob[kPairs];
-  float cs[kPairs][8], sn[kPairs][8], w[kPairs][16];
-  const long long pos = p.rot ? position_of(p, b, n) : 0;
-  const bool pos_ok = pos >= 0 && pos < p.table_rows;
 #pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
-    const int i = min(lane, per - 1) + kLanes * j;
-    chunk_offsets<kInter>(i, p.rot, p.D, oa[j], ob[j]);
-    load_angles<kInter>(p, pos, pos_ok, oa[j], ob[j], cs[j], sn[j]);
+  for (int j = 0; j < kPairs; ++j) chunk_offsets<kInter>(min(lane, per - 1) + kLanes * j, p.rot, p.D, oa[j], ob[j]);
+  uint4* const mine = rows + threadIdx.x;
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  // two groups of copies, so that the first half's arithmetic overlaps the second half's arrival
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[j][e] = gain_at(p, sd.gain, oa[j] + e, kBf16);
-      w[j][8 + e] = gain_at(p, sd.gain, ob[j] + e, kBf16);
+  for (int k = 0; k < kDepth; ++k) {
+    if (k < heads) {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        copy_16(to + ((k * kPairs + j) * 2) * kThreadsNr * 16, x + k * sd.xh + oa[j]);
+        copy_16(to + ((k * kPairs + j) * 2 + 1) * kThreadsNr * 16, x + k * sd.xh + ob[j]);
+      }
+    }
+    if (k == kDepth / 2 - 1 || k == kDepth - 1) copies_commit();
+  }
+
+  // out = r * (x * own + partner * other), gain and angle in one factor each
+  F2 own[kPairs][8], other[kPairs][8];
+  bool rot_a[kPairs], rot_b[kPairs];
+  {
+    const long long pos = p.rot ? position_of(p, it.b, it.n) : 0;
+    const bool pos_ok = pos >= 0 && pos < p.table_rows;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      float cs[8], sn[8], w[16];
+      load_angles<kInter>(p, pos, pos_ok, oa[j], ob[j], cs, sn);
+      load_gains(p, sd.gain, oa[j], w, kBf16);
+      load_gains(p, sd.gain, ob[j], w + 8, kBf16);
+      rot_a[j] = oa[j] < p.rot;
+      rot_b[j] = kInter ? ob[j] < p.rot : rot_a[j];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* wo = w + 8 * h + 2 * i;                              // own gains
+          const float* wp = kInter ? wo : w + 8 * (1 - h) + 2 * i;          // the partners'
+          own[j][4 * h + i] = pair(wo[0], wo[1]);
+          other[j][4 * h + i] = pair(0.f, 0.f);
+          if (h ? rot_b[j] : rot_a[j]) {
+            float c0, c1, s0, s1;
+            angle_factors<kInter>(cs, sn, h, i, c0, c1, s0, s1);
+            own[j][4 * h + i] = pair(wo[0] * c0, wo[1] * c1);
+            other[j][4 * h + i] = kInter ? pair(wp[1] * s0, wp[0] * s1) : pair(wp[0] * s0, wp[1] * s1);
+          }
+        }
     }
   }
-  const uint16_t* x = sd.x + b * sd.xb + n * sd.xn;
-  uint16_t* y = sd.y + b * sd.yb + n * sd.yn;
   const float inv_d = 1.f / static_cast<float>(p.D);
-  // every lane of the warp runs the same number of rounds (the shuffles)
-  constexpr int kUnroll = kPairs == 1 ? 4 : 2;
-  for (int hb = 0; hb < p.heads_per_item; hb += kUnroll) {
-    uint4 u[kUnroll][kPairs][2];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int h = h0 + hb + k;
-#pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        u[k][j][0] = u[k][j][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h < h1) {
-          u[k][j][0] = *reinterpret_cast<const uint4*>(x + h * sd.xh + oa[j]);
-          u[k][j][1] = *reinterpret_cast<const uint4*>(x + h * sd.xh + ob[j]);
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int h = h0 + hb + k;
-      float f[kPairs][16], ss = 0.f;
+  for (int half = 0; half < 2; ++half) {
+    if (half == 0) copies_wait<1>();
+    else copies_wait<0>();
+#pragma unroll 2
+    for (int k = half * (kDepth / 2); k < (half + 1) * (kDepth / 2); ++k) {
+      if (k >= p.heads_per_item) break;  // the same for every thread: whole warps take part in the shuffles
+      F2 f[kPairs][8], ss2 = pair(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        unpack8(u[k][j][0], f[j], kBf16);
-        unpack8(u[k][j][1], f[j] + 8, kBf16);
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        unpack8(k < heads ? mine[((k * kPairs + j) * 2) * kThreadsNr] : z, f[j], kBf16);
+        unpack8(k < heads ? mine[((k * kPairs + j) * 2 + 1) * kThreadsNr] : z, f[j] + 4, kBf16);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(f[j][e], f[j][e], ss);
+        for (int e = 0; e < 8; ++e) ss2 = fma2(f[j][e], f[j][e], ss2);
       }
+      float ss = sum2(ss2);
 #pragma unroll
       for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off, kLanes);
       const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+      const F2 r2 = pair(r, r);
+      if (k < heads) {
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
+        for (int j = 0; j < kPairs; ++j) {
+          F2 o[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[j][e] = f[j][e] * r * w[j][e];
-        rotate16<kInter, false>(f[j], cs[j], sn[j], oa[j], ob[j], p.rot);
-        if (live && h < h1) {
-          *reinterpret_cast<uint4*>(y + h * sd.yh + oa[j]) = pack8(f[j], kBf16);
-          *reinterpret_cast<uint4*>(y + h * sd.yh + ob[j]) = pack8(f[j] + 8, kBf16);
+          for (int e = 0; e < 8; ++e) {
+            f[j][e] = mul2(f[j][e], r2);
+            o[e] = mul2(f[j][e], own[j][e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < 4 ? rot_a[j] : rot_b[j])
+              o[e] = fma2(kInter ? swapped(f[j][e]) : f[j][e ^ 4], other[j][e], o[e]);
+          *reinterpret_cast<uint4*>(y + k * sd.yh + oa[j]) = pack8(o, kBf16);
+          *reinterpret_cast<uint4*>(y + k * sd.yh + ob[j]) = pack8(o + 4, kBf16);
         }
       }
     }
@@ -274,103 +374,144 @@ __global__ void __launch_bounds__(kThreadsNr) fa2_norm_rope_fwd_kernel(const __g
 // items; each block leaves its sum of the gain gradient in its row of
 // `partials`, which fa2_norm_rope_gain_kernel adds up in a fixed order.
 template <int kLanes, int kPairs, bool kBf16, bool kInter>
-__global__ void __launch_bounds__(kThreadsNr) fa2_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
+    fa2_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kRows = kThreadsNr / kLanes;  // row groups of a block
+  constexpr int kDepth = kBwdDepth<kPairs>;
+  extern __shared__ __align__(16) uint4 rows[];  // [depth][pairs][x a, x b, g a, g b][threads]
   __shared__ float sums[kThreadsNr / 32][kLanes * kPairs * 16];
   const int lane = threadIdx.x % kLanes;
   const bool is_k = static_cast<int>(blockIdx.x) >= p.q_blocks;
   const NormRopeSide& sd = p.side[is_k ? 1 : 0];
-  const long long first = is_k ? blockIdx.x - p.q_blocks : blockIdx.x;
-  const long long blocks = is_k ? gridDim.x - p.q_blocks : p.q_blocks;
-  const long long items = p.tokens * sd.slices;
+  const unsigned first = is_k ? blockIdx.x - p.q_blocks : blockIdx.x;
+  const unsigned blocks = is_k ? gridDim.x - p.q_blocks : p.q_blocks;
+  const unsigned items = static_cast<unsigned>(p.tokens * sd.slices);
   const int per = p.D / 16;
   const float inv_d = 1.f / static_cast<float>(p.D);
 
   int oa[kPairs], ob[kPairs];
-  float w[kPairs][16], dw[kPairs][16];
+  F2 w[kPairs][8], dw[kPairs][8];
+  bool rot_a[kPairs], rot_b[kPairs];
 #pragma unroll
   for (int j = 0; j < kPairs; ++j) {
     chunk_offsets<kInter>(min(lane, per - 1) + kLanes * j, p.rot, p.D, oa[j], ob[j]);
+    rot_a[j] = oa[j] < p.rot;
+    rot_b[j] = kInter ? ob[j] < p.rot : rot_a[j];
+    float g[16];
+    load_gains(p, sd.gain, oa[j], g, kBf16);
+    load_gains(p, sd.gain, ob[j], g + 8, kBf16);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      w[j][e] = gain_at(p, sd.gain, oa[j] + e, kBf16);
-      w[j][8 + e] = gain_at(p, sd.gain, ob[j] + e, kBf16);
+      w[j][e] = pair(g[2 * e], g[2 * e + 1]);
+      dw[j][e] = pair(0.f, 0.f);
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) dw[j][e] = 0.f;
   }
 
-  for (long long base = first * kRows; base < items; base += blocks * kRows) {
-    long long item = base + threadIdx.x / kLanes;
+  // The rows of this thread, one after the other: row u is head u % per_item
+  // of its item u / per_item; the same count for every thread of the block. Rows past the items, or past an item's heads, are
+  // walked without data.
+  const unsigned steps = items > first * kRows ? (items - first * kRows + blocks * kRows - 1) / (blocks * kRows) : 0;
+  const unsigned total = steps * sd.per_item;
+  uint4* const mine = rows + threadIdx.x;
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  const unsigned my_first = first * kRows + threadIdx.x / kLanes, my_stride = blocks * kRows;
+  Item ahead = {};      // the item being requested
+  int ahead_head = 0;   // its next head
+  unsigned ahead_step = 0, requested = 0;
+  auto request = [&]() {
+    if (requested < total) {
+      if (ahead_head == 0) {
+        const unsigned item = my_first + ahead_step * my_stride;
+        const bool live = item < items && lane < per;
+        ahead = item_at(p, sd, live ? item : 0u);
+        if (!live) ahead.heads = 0;
+      }
+      if (ahead_head < ahead.heads) {
+        const int h = ahead.h0 + ahead_head;
+        const uint16_t* x = sd.x + ahead.b * sd.xb + ahead.n * sd.xn + h * sd.xh;
+        const uint16_t* g = sd.g + ahead.b * sd.gb + ahead.n * sd.gn + h * sd.gh;
+        const uint32_t at = to + (requested % kDepth) * (kPairs * 4 * kThreadsNr * 16);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          copy_16(at + (j * 4) * kThreadsNr * 16, x + oa[j]);
+          copy_16(at + (j * 4 + 1) * kThreadsNr * 16, x + ob[j]);
+          copy_16(at + (j * 4 + 2) * kThreadsNr * 16, g + oa[j]);
+          copy_16(at + (j * 4 + 3) * kThreadsNr * 16, g + ob[j]);
+        }
+      }
+      ++requested;
+      if (++ahead_head == sd.per_item) {
+        ahead_head = 0;
+        ++ahead_step;
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) request();
+
+  unsigned u = 0;
+  for (unsigned step = 0; step < steps; ++step) {
+    const unsigned item = my_first + step * my_stride;
     const bool live = item < items && lane < per;
-    if (item >= items) item = items - 1;
-    const long long slice = item / p.tokens, t = item - slice * p.tokens;
-    const long long b = t / p.N;
-    const int n = static_cast<int>(t - b * p.N);
-    const int h0 = static_cast<int>(slice) * p.heads_per_item, h1 = min(h0 + p.heads_per_item, sd.heads);
-    const long long pos = p.rot ? position_of(p, b, n) : 0;
+    const Item it = item_at(p, sd, live ? item : 0u);
+    const long long pos = p.rot ? position_of(p, it.b, it.n) : 0;
     const bool pos_ok = pos >= 0 && pos < p.table_rows;
     float cs[kPairs][8], sn[kPairs][8];
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) load_angles<kInter>(p, pos, pos_ok, oa[j], ob[j], cs[j], sn[j]);
-    const uint16_t* x = sd.x + b * sd.xb + n * sd.xn;
-    const uint16_t* g = sd.g + b * sd.gb + n * sd.gn;
-    uint16_t* y = sd.y + b * sd.yb + n * sd.yn;
-    constexpr int kUnroll = kPairs == 1 ? 2 : 1;
-    for (int hb = 0; hb < p.heads_per_item; hb += kUnroll) {
-      uint4 u[kUnroll][kPairs][2], v[kUnroll][kPairs][2];
+    uint16_t* y = sd.y + it.b * sd.yb + it.n * sd.yn + it.h0 * sd.yh;
+    for (int k = 0; k < sd.per_item; ++k, ++u) {
+      const bool row = live && k < it.heads;
+      copies_wait<kDepth - 1>();
+      F2 x[kPairs][8], h[kPairs][8], ss2 = pair(0.f, 0.f), dot2 = ss2;
+      const uint4* at = mine + (u % kDepth) * (kPairs * 4 * kThreadsNr);
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int h = h0 + hb + k;
+      for (int j = 0; j < kPairs; ++j) {
+        F2 g[8];
+        unpack8(at[(j * 4) * kThreadsNr], x[j], kBf16);
+        unpack8(at[(j * 4 + 1) * kThreadsNr], x[j] + 4, kBf16);
+        unpack8(at[(j * 4 + 2) * kThreadsNr], g, kBf16);
+        unpack8(at[(j * 4 + 3) * kThreadsNr], g + 4, kBf16);
+        // h = R^T g: the rotation by the opposite angle
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          u[k][j][0] = u[k][j][1] = v[k][j][0] = v[k][j][1] = make_uint4(0u, 0u, 0u, 0u);
-          if (live && h < h1) {
-            u[k][j][0] = *reinterpret_cast<const uint4*>(x + h * sd.xh + oa[j]);
-            u[k][j][1] = *reinterpret_cast<const uint4*>(x + h * sd.xh + ob[j]);
-            v[k][j][0] = *reinterpret_cast<const uint4*>(g + h * sd.gh + oa[j]);
-            v[k][j][1] = *reinterpret_cast<const uint4*>(g + h * sd.gh + ob[j]);
+        for (int e = 0; e < 8; ++e) {
+          h[j][e] = g[e];
+          if (e < 4 ? rot_a[j] : rot_b[j]) {
+            float c0, c1, s0, s1;
+            angle_factors<kInter>(cs[j], sn[j], e >> 2, e & 3, c0, c1, s0, s1);
+            h[j][e] = fma2(kInter ? swapped(g[e]) : g[e ^ 4], pair(-s0, -s1), mul2(g[e], pair(c0, c1)));
           }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          ss2 = fma2(x[j][e], x[j][e], ss2);
+          dot2 = fma2(mul2(h[j][e], w[j][e]), x[j][e], dot2);
         }
       }
+      // this thread has read its row: the slot takes the row kDepth further on
+      request();
+      float ss = row ? sum2(ss2) : 0.f, dot = row ? sum2(dot2) : 0.f;
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int h = h0 + hb + k;
-        const bool row = live && h < h1;
-        float f[kPairs][16], hg[kPairs][16], ss = 0.f, dot = 0.f;
+      for (int off = kLanes / 2; off > 0; off >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, off, kLanes);
+        dot += __shfl_xor_sync(0xffffffffu, dot, off, kLanes);
+      }
+      const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+      const float m = -dot * r * inv_d;  // -mean(h gain n)
+      if (row) {
+        const F2 r2 = pair(r, r), m2 = pair(m, m);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          unpack8(u[k][j][0], f[j], kBf16);
-          unpack8(u[k][j][1], f[j] + 8, kBf16);
-          unpack8(v[k][j][0], hg[j], kBf16);
-          unpack8(v[k][j][1], hg[j] + 8, kBf16);
-          rotate16<kInter, true>(hg[j], cs[j], sn[j], oa[j], ob[j], p.rot);
+          F2 o[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            ss = fmaf(f[j][e], f[j][e], ss);
-            dot = fmaf(hg[j][e] * w[j][e], f[j][e], dot);
+          for (int e = 0; e < 8; ++e) {
+            const F2 n = mul2(x[j][e], r2);
+            dw[j][e] = fma2(h[j][e], n, dw[j][e]);
+            o[e] = mul2(r2, fma2(n, m2, mul2(h[j][e], w[j][e])));
           }
-        }
-        if (!row) ss = dot = 0.f;
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, off, kLanes);
-          dot += __shfl_xor_sync(0xffffffffu, dot, off, kLanes);
-        }
-        const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-        const float m = dot * r * inv_d;  // mean(h gain n)
-        if (row) {
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float nx = f[j][e] * r;
-              dw[j][e] = fmaf(hg[j][e], nx, dw[j][e]);
-              f[j][e] = r * (hg[j][e] * w[j][e] - nx * m);
-            }
-            *reinterpret_cast<uint4*>(y + h * sd.yh + oa[j]) = pack8(f[j], kBf16);
-            *reinterpret_cast<uint4*>(y + h * sd.yh + ob[j]) = pack8(f[j] + 8, kBf16);
-          }
+          *reinterpret_cast<uint4*>(y + k * sd.yh + oa[j]) = pack8(o, kBf16);
+          *reinterpret_cast<uint4*>(y + k * sd.yh + ob[j]) = pack8(o + 4, kBf16);
         }
       }
     }
@@ -383,7 +524,9 @@ __global__ void __launch_bounds__(kThreadsNr) fa2_norm_rope_bwd_kernel(const __g
   for (int j = 0; j < kPairs; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float s = dw[j][e];
+      float lo, hi;
+      halves(dw[j][e / 2], lo, hi);
+      float s = e & 1 ? hi : lo;
 #pragma unroll
       for (int off = 16; off >= kLanes; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       if (threadIdx.x % 32 < kLanes) sums[warp][(j * 16 + e) * kLanes + lane] = s;
@@ -428,27 +571,29 @@ __global__ void __launch_bounds__(kThreadsNr) fa2_norm_rope_gain_kernel(const fl
     static_cast<__half*>(out)[i] = __float2half_rn(s);
 }
 
+// A kernel and its one-time set-up on each device.
+struct Picked {
+  const void* kern;
+  PerDeviceOnce* prepared;
+};
+
+template <bool kBwd, int kLanes, int kPairs, bool kBf16, bool kInter>
+Picked picked() {
+  static PerDeviceOnce prepared;
+  if constexpr (kBwd) return {(const void*)fa2_norm_rope_bwd_kernel<kLanes, kPairs, kBf16, kInter>, &prepared};
+  else return {(const void*)fa2_norm_rope_fwd_kernel<kLanes, kPairs, kBf16, kInter>, &prepared};
+}
+
 template <bool kBwd, int kLanes, int kPairs>
-const void* pick_variant(bool bf16, bool inter) {
-  if constexpr (kBwd) {
-    if (bf16)
-      return inter ? (const void*)fa2_norm_rope_bwd_kernel<kLanes, kPairs, true, true>
-                   : (const void*)fa2_norm_rope_bwd_kernel<kLanes, kPairs, true, false>;
-    return inter ? (const void*)fa2_norm_rope_bwd_kernel<kLanes, kPairs, false, true>
-                 : (const void*)fa2_norm_rope_bwd_kernel<kLanes, kPairs, false, false>;
-  } else {
-    if (bf16)
-      return inter ? (const void*)fa2_norm_rope_fwd_kernel<kLanes, kPairs, true, true>
-                   : (const void*)fa2_norm_rope_fwd_kernel<kLanes, kPairs, true, false>;
-    return inter ? (const void*)fa2_norm_rope_fwd_kernel<kLanes, kPairs, false, true>
-                 : (const void*)fa2_norm_rope_fwd_kernel<kLanes, kPairs, false, false>;
-  }
+Picked pick_variant(bool bf16, bool inter) {
+  if (bf16) return inter ? picked<kBwd, kLanes, kPairs, true, true>() : picked<kBwd, kLanes, kPairs, true, false>();
+  return inter ? picked<kBwd, kLanes, kPairs, false, true>() : picked<kBwd, kLanes, kPairs, false, false>();
 }
 
 int lanes_for(int D) { return D <= 32 ? 2 : D <= 64 ? 4 : D <= 128 ? 8 : D <= 256 ? 16 : 32; }
 
 template <bool kBwd>
-const void* pick_kernel(int D, bool bf16, bool inter) {
+Picked pick_kernel(int D, bool bf16, bool inter) {
   switch (D) {
     case 32: return pick_variant<kBwd, 2, 1>(bf16, inter);
     case 64: return pick_variant<kBwd, 4, 1>(bf16, inter);
@@ -536,7 +681,7 @@ struct NormRopeArgs {
 // give a small call more threads: halved from kMaxHeads until the items fill
 // two blocks per SM.
 int heads_per_item(long long tokens, int hq, int hk, int D, int sms) {
-  int hp = kMaxHeads;
+  int hp = D == 1024 ? kMaxHeads / 2 : kMaxHeads;
   const long long rows = kThreadsNr / lanes_for(D);
   while (hp > 1) {
     const long long items = tokens * ((hq + hp - 1) / hp + (hk + hp - 1) / hp);
@@ -547,8 +692,9 @@ int heads_per_item(long long tokens, int hq, int hk, int D, int sms) {
 }
 
 // What forward and backward check alike.
-int check_common(NormRopeArgs& a, const void* q, const void* k, const void* cos, const void* sin, int B, int Hq,
-                 int Hkv, int N, int D, int rot, int table_rows, float eps, int dtype) {
+int check_common(NormRopeArgs& a, const void* q, const void* k, const void* q_gain, const void* k_gain, const void* cos,
+                 const void* sin, const void* positions, int B, int Hq, int Hkv, int N, int D, int rot, int table_rows,
+                 float eps, int positions_64, int dtype) {
   if (B < 0 || Hq < 0 || Hkv < 0 || N < 0 || rot < 0 || table_rows < 0) return FA2_ERR_INVALID_ARG;
   if (!fwd_head_dim_ok(D)) return FA2_ERR_UNSUPPORTED;
   if (dtype != FA2_F16 && dtype != FA2_BF16) return FA2_ERR_UNSUPPORTED;
@@ -559,7 +705,10 @@ int check_common(NormRopeArgs& a, const void* q, const void* k, const void* cos,
   if (B == 0 || N == 0 || (Hq == 0 && Hkv == 0)) return FA2_OK;
   if ((Hq > 0 && !q) || (Hkv > 0 && !k)) return FA2_ERR_INVALID_ARG;
   if (rot > 0 && (!cos || !sin)) return FA2_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 15u) return FA2_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin) | reinterpret_cast<uintptr_t>(q_gain) |
+       reinterpret_cast<uintptr_t>(k_gain)) & 15u)
+    return FA2_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(positions) & (positions_64 ? 7u : 3u)) return FA2_ERR_ALIGN;
   if (static_cast<int64_t>(B) * N > INT32_MAX) return FA2_ERR_INVALID_ARG;
   a.B = B;
   return FA2_OK;
@@ -619,7 +768,7 @@ void fill_params(NormRopeArgs& a, const float* cos, const float* sin, const void
   p = {};
   const int heads[2] = {Hq, Hkv};
   p.tokens = static_cast<long long>(a.B) * N;
-  p.heads_per_item = heads_per_item(p.tokens, Hq, Hkv, D, sms);
+  const int hp = heads_per_item(p.tokens, Hq, Hkv, D, sms);
   for (int i = 0; i < 2; ++i) {
     NormRopeSide& s = p.side[i];
     s.x = static_cast<const uint16_t*>(a.x[i].p);
@@ -630,7 +779,10 @@ void fill_params(NormRopeArgs& a, const float* cos, const float* sin, const void
     s.gb = a.g[i].b; s.gh = a.g[i].h; s.gn = a.g[i].n;
     s.yb = a.y[i].b; s.yh = a.y[i].h; s.yn = a.y[i].n;
     s.heads = heads[i];
-    s.slices = (heads[i] + p.heads_per_item - 1) / p.heads_per_item;
+    s.per_item = hp;
+    while (s.per_item / 2 >= std::max(heads[i], 1)) s.per_item /= 2;
+    s.slices = (heads[i] + s.per_item - 1) / s.per_item;
+    p.heads_per_item = std::max(p.heads_per_item, s.per_item);
   }
   p.cos = cos;
   p.sin = sin;
@@ -646,13 +798,20 @@ void fill_params(NormRopeArgs& a, const float* cos, const float* sin, const void
   p.eps = eps;
 }
 
-// Blocks of the backward at most: 8 per SM of a 160-SM device, so that the
-// workspace's size needs no device.
+// Blocks of the backward at most, so that the workspace's size needs no device.
 constexpr int kMaxGainBlocks = 1280;
 
-int launch_kernel(const void* kern, int grid, NormRopeParams& p, cudaStream_t s) {
+// Shared memory of a block: the rows its threads have under way.
+constexpr int kRowStageBytes = kMaxHeads * 2 * kThreadsNr * 16;
+static_assert(kRowStageBytes == 4 * 4 * kThreadsNr * 16, "forward and backward take the same");
+
+int launch_kernel(const void* kern, PerDeviceOnce& prepared, int grid, NormRopeParams& p, cudaStream_t s) {
+  cudaError_t e = once_per_device(prepared, [&]() {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowStageBytes);
+  });
+  if (e != cudaSuccess) return record_cuda_error(e);
   void* args[1] = {&p};
-  const cudaError_t e = cudaLaunchKernel(kern, dim3(grid), dim3(kThreadsNr), args, 0, s);
+  e = cudaLaunchKernel(kern, dim3(grid), dim3(kThreadsNr), args, kRowStageBytes, s);
   return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
 }
 
@@ -667,7 +826,8 @@ extern "C" int fa2_qk_norm_rope_fwd(const void* q, const void* k, const void* q_
                                     int rot, int table_rows, float eps, int interleaved, int gain_f32,
                                     int positions_64, int dtype, struct CUstream_st* stream) {
   NormRopeArgs a = {};
-  int rc = check_common(a, q, k, cos, sin, B, Hq, Hkv, N, D, rot, table_rows, eps, dtype);
+  int rc = check_common(a, q, k, q_gain, k_gain, cos, sin, positions, B, Hq, Hkv, N, D, rot, table_rows, eps,
+                        positions_64, dtype);
   if (rc != FA2_OK || B == 0 || N == 0 || (Hq == 0 && Hkv == 0)) return rc;
   if (rot > 0 && !positions && table_rows < N) return FA2_ERR_INVALID_ARG;
   a.x[0] = view_of(q, strides, B, Hq, N, D);
@@ -687,9 +847,9 @@ extern "C" int fa2_qk_norm_rope_fwd(const void* q, const void* k, const void* q_
   const long long items = a.p.tokens * (a.p.side[0].slices + a.p.side[1].slices);
   const long long rows = kThreadsNr / lanes_for(D);
   const long long grid = (items + rows - 1) / rows;
-  if (grid > INT32_MAX) return FA2_ERR_INVALID_ARG;
-  return launch_kernel(pick_kernel<false>(D, dtype == FA2_BF16, interleaved != 0), static_cast<int>(grid), a.p,
-                       reinterpret_cast<cudaStream_t>(stream));
+  if (items > INT32_MAX) return FA2_ERR_INVALID_ARG;  // the kernels count items in 32 bits
+  const Picked kern = pick_kernel<false>(D, dtype == FA2_BF16, interleaved != 0);
+  return launch_kernel(kern.kern, *kern.prepared, static_cast<int>(grid), a.p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fa2_qk_norm_rope_bwd_workspace_bytes(int D, size_t* bytes) {
@@ -706,7 +866,8 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
                                     int table_rows, float eps, int interleaved, int gain_f32, int positions_64,
                                     int dtype, void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
   NormRopeArgs a = {};
-  int rc = check_common(a, q, k, cos, sin, B, Hq, Hkv, N, D, rot, table_rows, eps, dtype);
+  int rc = check_common(a, q, k, q_gain, k_gain, cos, sin, positions, B, Hq, Hkv, N, D, rot, table_rows, eps,
+                        positions_64, dtype);
   if (rc != FA2_OK) return rc;
   const size_t gbytes = static_cast<size_t>(D) * (gain_f32 ? 4 : 2);
   // a gain's gradient is written exactly where there is a gain
@@ -734,6 +895,7 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   if ((rc = check_arrays(a, cos, sin, positions, rot, table_rows, gain_f32, positions_64, pb, pn, N, D)) != FA2_OK)
     return rc;
   const bool gains = q_gain || k_gain;
+  if ((reinterpret_cast<uintptr_t>(dq_gain) | reinterpret_cast<uintptr_t>(dk_gain)) & 15u) return FA2_ERR_ALIGN;
   if (gains) {
     if (!workspace) return FA2_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) & 15u) return FA2_ERR_ALIGN;
@@ -758,12 +920,14 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   if ((rc = current_device_facts(&sms, &status)) != FA2_OK) return rc;
   fill_params(a, cos, sin, positions, Hq, Hkv, N, D, rot, table_rows, eps, gain_f32, positions_64, pb, pn, sms);
   a.p.partials = static_cast<float*>(workspace);
-  // Blocks: as many as the items need, at most 4 per SM (each leaves one row
-  // of partial sums), dealt to queries and keys by their shares of the work.
+  // Blocks: as many as the items need, at most 2 per SM (what an SM holds;
+  // each leaves one row of partial sums), dealt to queries and keys by their
+  // shares of the work.
   const long long rows = kThreadsNr / lanes_for(D);
   auto need = [&](int i) { return (a.p.tokens * a.p.side[i].slices + rows - 1) / rows; };
-  const long long cap = std::min<long long>(4ll * sms, kMaxGainBlocks);
+  const long long cap = std::min<long long>(2ll * sms, kMaxGainBlocks);
   long long nq = need(0), nk = need(1);
+  if (std::max(nq, nk) * rows > INT32_MAX) return FA2_ERR_INVALID_ARG;  // the kernels count items in 32 bits
   if (nq + nk > cap) {
     const long long all = nq + nk;
     nk = nk ? std::max<long long>(1, cap * nk / all) : 0;
@@ -771,8 +935,8 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   }
   a.p.q_blocks = static_cast<int>(nq);
   const int grid = static_cast<int>(nq + nk);
-  if ((rc = launch_kernel(pick_kernel<true>(D, dtype == FA2_BF16, interleaved != 0), grid, a.p, s)) != FA2_OK)
-    return rc;
+  const Picked kern = pick_kernel<true>(D, dtype == FA2_BF16, interleaved != 0);
+  if ((rc = launch_kernel(kern.kern, *kern.prepared, grid, a.p, s)) != FA2_OK) return rc;
   if (gains) {
     fa2_norm_rope_gain_kernel<<<dim3(D / 32, 2), kThreadsNr, 0, s>>>(a.p.partials, dq_gain, dk_gain, a.p.q_blocks,
                                                                       grid, D, gain_f32, dtype == FA2_BF16);

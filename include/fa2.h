@@ -382,7 +382,7 @@ FA2_API int fa2_bwd_sched(const void* Q, const void* K, const void* V, const voi
  * eps       : finite, >= 0.
  *
  * Asynchronous and allocation-free as fa2_fwd; tensor pointers are 16-byte
- * aligned. Errors as fa2_fwd (FA2_ERR_UNSUPPORTED also for a rot that is not
+ * aligned (positions: to its element). Errors as fa2_fwd (FA2_ERR_UNSUPPORTED also for a rot that is not
  * a multiple of 16).
  */
 FA2_API int fa2_qk_norm_rope_fwd(const void* q, const void* k, const void* q_gain, const void* k_gain,

@@ -84,6 +84,7 @@ def s_with(**at):
     (dict(rot=80), -1), (dict(eps=-1e-6), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
     (dict(q=None), -1), (dict(k=None), -1), (dict(qo=None), -1), (dict(ko=None), -1), (dict(cos=None), -1),
     (dict(sin=None), -1), (dict(rows=7), -1),
+    (dict(qw=A * 3 + 8), -3), (dict(kw=A * 4 + 2), -3), (dict(pos=A * 9 + 2), -3), (dict(pos=A * 9 + 4, p64=1), -3),
     (dict(q=A + 8), -3), (dict(ko=A * 8 + 2), -3), (dict(cos=A * 5 + 4), -3), (dict(sin=A * 6 + 8), -3),
     (dict(qo=A + 64), -1),                    # q_out meets q, not exactly
     (dict(qo=A * 2), -1),                     # q_out meets k
@@ -139,6 +140,7 @@ def bwd(lib, **over):
     (dict(B=-1), -1), (dict(D=40), -2), (dict(dtype=7), -2), (dict(rot=40), -2), (dict(rot=96), -1),
     (dict(dqo=None), -1), (dict(dk=None), -1), (dict(dqw=None), -1), (dict(qw=None), -1), (dict(kw=None), -1),
     (dict(ws=None), -1), (dict(wsb=1280 * 64 * 4 - 4), -1), (dict(ws=A * 20 + 8), -3), (dict(dq=A * 7 + 2), -3),
+    (dict(dqw=A * 12 + 4), -3),
     (dict(dq=A + 128), -1), (dict(dq=A * 10 + 128), -1), (dict(dq=A * 11), -1), (dict(dk=A * 7), -1),
     (dict(ws=A * 7), -1), (dict(ws=A), -1), (dict(dqw=A * 12, dkw=A * 12 + 64), -1), (dict(dqw=A * 20 + 256), -1),
     (dict(dqw=A * 3), -1), (dict(dqw=A * 7 + 64), -1), (dict(rows=4), -1),
