@@ -529,17 +529,22 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         if constexpr (kCross) key_steps = cross_key_steps(sgm.n_keys - sgm.kv * kBwdKeys);
         const uint32_t kt_lo = desc_lo_sw128(sK, kPanelBytes);
         const uint32_t ds_mn = desc_lo_sw128(sDS, kPanelBytes);
-#pragma unroll
-        for (int kk = 0; kk < kBwdKeys / 16; ++kk) {
-          if constexpr (kCross) {
-            if (kk >= key_steps) break;
-          }
+        auto one = [&](int kk) {
           const uint32_t off = static_cast<uint32_t>((kk * 16 * 128) >> 4);
           if constexpr (L::kDqRows)  // dQ = dS K: A = dS^T's rows read MN-major (M = queries), B = K MN-major
             mma_ss_w(tmem + L::kColDQ, ds_mn + off, kHi, kt_lo + off, kHi, idesc_dqr, kk > 0 ? 1u : 0u);
           else
             mma_ss_w(tmem + L::kColDQ, kt_lo + off, kHi, ds_mn + off, kHi, idesc_dq, kk > 0 ? 1u : 0u);
+        };
+        if constexpr (kCross) {
+          if (key_steps < kBwdKeys / 16) {  // a loop, so that the full tiles' code has no test in it
+#pragma unroll 1
+            for (int kk = 0; kk < key_steps; ++kk) one(kk);
+            return;
+          }
         }
+#pragma unroll
+        for (int kk = 0; kk < kBwdKeys / 16; ++kk) one(kk);
       };
 
       if constexpr (kTwoIssuers) {

@@ -17,6 +17,7 @@ namespace fa2 {
 namespace {
 
 constexpr int kEndThreads = 256;
+constexpr int kZeroRows = 128;  // dK, dV rows a block writes zeros to at a time
 
 size_t round_up_256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -62,15 +63,18 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4
   }
   if (p.ws_flags && first < kBwdMaxCtas) p.ws_flags[first] = 0ull;
   if (!p.key_lengths) return;
+  // pieces of kZeroRows rows of a head, dealt to the blocks in turn
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  // one head of rows after the other, its rows over the block's threads
-  for (long long h = blockIdx.x; h < p.BH; h += gridDim.x) {
-    const int n = cross_keys(p, static_cast<int>(h / p.heads));
-    const long long from = min(static_cast<long long>((n + kKeys - 1) / kKeys) * kKeys, static_cast<long long>(p.Nk));
-    const long long base = h * p.Nk;
-    for (long long i = (base + from) * per_row + threadIdx.x; i < (base + p.Nk) * per_row; i += blockDim.x) {
-      dk[i] = z;
-      dv[i] = z;
+  const int pieces = (p.Nk + kZeroRows - 1) / kZeroRows;
+  const long long all = static_cast<long long>(p.BH) * pieces;
+  for (long long i = blockIdx.x; i < all; i += gridDim.x) {
+    const int h = static_cast<int>(i / pieces), piece = static_cast<int>(i - static_cast<long long>(h) * pieces);
+    const int from = (cross_keys(p, h / p.heads) + kKeys - 1) / kKeys * kKeys;
+    const int r0 = max(piece * kZeroRows, from), r1 = min((piece + 1) * kZeroRows, p.Nk);
+    const long long base = static_cast<long long>(h) * p.Nk;
+    for (long long e = (base + r0) * per_row + threadIdx.x; e < (base + r1) * per_row; e += blockDim.x) {
+      dk[e] = z;
+      dv[e] = z;
     }
   }
 }

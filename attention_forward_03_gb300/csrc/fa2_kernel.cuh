@@ -330,7 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // S_t = Q_t K^T : D/16 steps of K=16 along the head dimension.
         // Cross attention: N only as wide as the tile's keys (`steps` groups of 16).
         auto issue_s = [&](int t, int slot, [[maybe_unused]] int steps) {
-          const uint32_t idesc = kCross ? make_idesc_f16(kBf16, 16 * steps, false) : idesc_s;
+          uint32_t idesc = idesc_s;
+          if constexpr (kCross) {
+            if (steps < kKeys / 16) idesc = make_idesc_f16(kBf16, 16 * steps, false);
+          }
           const uint32_t q_lo = desc_lo_sw128(sQ, 16);
           const uint32_t ring_lo = desc_lo_sw128(sRing, 16);
           const uint32_t qa = q_lo + static_cast<uint32_t>((t * L::kTileBytes) >> 4);
@@ -352,31 +355,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t va = ring_lo_v + static_cast<uint32_t>(slot * (L::kTileBytes >> 4));
           const uint32_t dt = tmem + L::kColO + static_cast<uint32_t>(t * L::kDp);
           const uint32_t pt = tmem + L::kColP + static_cast<uint32_t>(t * (kKeys / 2));
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
+          auto one = [&](int kk) {
             const uint32_t vb = va + static_cast<uint32_t>((kk * 16 * 128) >> 4);
             const uint32_t acc_kk = (acc || kk > 0) ? 1u : 0u;
-            if constexpr (kCross) {
-              if (kk >= steps) break;
-            }
             if constexpr (L::kPInTmem) {
               mma_ts_w(dt, pt + 8u * kk, vb, kHi, idesc_o, acc_kk);
             } else {
               const uint32_t po = static_cast<uint32_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
               mma_ss_w(dt, pa + po, kHi, vb, kHi, idesc_o, acc_kk);
             }
+          };
+          if constexpr (kCross) {
+            if (steps < kKeys / 16) {  // a unit's last tile: a loop, so that the full tiles' code has no test in it
+#pragma unroll 1
+              for (int kk = 0; kk < steps; ++kk) one(kk);
+              return;
+            }
           }
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk) one(kk);
         };
 
         // 16-key groups of tile j with keys, and the rows of its V tile behind
         // the keys zeroed (nothing to do at Nk: the copy engine read zeros).
+        [[maybe_unused]] int tail_j = -1;  // the segment's tile that is not full, if it has one
+        auto enter_segment = [&]([[maybe_unused]] const Seg& s) {
+          if constexpr (kCross) tail_j = s.n_keys < s.nkv * kKeys ? s.nkv - 1 : -1;
+        };
         auto key_steps = [&]([[maybe_unused]] const Seg& s, [[maybe_unused]] int j) -> int {
-          if constexpr (kCross) return cross_key_steps(s.n_keys - j * kKeys);
-          else return kKeys / 16;
+          if constexpr (kCross) {
+            if (j == tail_j) return cross_key_steps(s.n_keys - j * kKeys);
+          }
+          return kKeys / 16;
         };
         auto clean_v = [&]([[maybe_unused]] const Seg& s, [[maybe_unused]] int j, [[maybe_unused]] int slot) {
           if constexpr (kCross) {
-            if (j == s.nkv - 1 && s.n_keys < p.Nk)
+            if (j == tail_j && s.n_keys < p.Nk)
               cross_zero_rows(sRing + static_cast<uint32_t>(slot * L::kTileBytes), L::kPanels, s.n_keys - j * kKeys);
           }
         };
@@ -409,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && advance(cur, w)) {
               const int b = w.kv_begin, e = w.kv_end;
               const int n_sub = live_subtiles(w);
+              enter_segment(w);
               if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) { ok = false; break; }
               ++q_round;
               for (int j = b; j < e && ok; ++j) {
@@ -437,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && advance(cur, w)) {
               const int b = w.kv_begin, e = w.kv_end;
               const int n_sub = live_subtiles(w);
+              enter_segment(w);
               for (int j = b; j < e && ok; ++j) {
                 const int slot_v = take(base_idx + v_index(j, b, e), 1u);
                 if (slot_v < 0) { ok = false; break; }
@@ -482,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           while (ok && advance(cur, w)) {
             const int b = w.kv_begin, e = w.kv_end;
+            enter_segment(w);
             // this sub-tile's end (a sub-tile without query rows: nothing but the slots' release)
             const int et = t == 0 ? sub0_end<kCausal>(w) : (t < live_subtiles(w) ? e : b);
             if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) { ok = false; break; }

@@ -415,34 +415,37 @@ __global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
   uint4* const mine = rows + threadIdx.x;
   const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
   const unsigned my_first = first * kRows + threadIdx.x / kLanes, my_stride = blocks * kRows;
-  Item ahead = {};      // the item being requested
+  int ahead_heads = 0;  // heads of the item being requested
   int ahead_head = 0;   // its next head
-  unsigned ahead_step = 0, requested = 0;
+  const uint16_t *ahead_x = nullptr, *ahead_g = nullptr;  // and that head's rows
+  unsigned ahead_item = my_first, requested = 0;
+  uint32_t ahead_at = to;  // ring slot
   auto request = [&]() {
     if (requested < total) {
       if (ahead_head == 0) {
-        const unsigned item = my_first + ahead_step * my_stride;
-        const bool live = item < items && lane < per;
-        ahead = item_at(p, sd, live ? item : 0u);
-        if (!live) ahead.heads = 0;
+        const bool live = ahead_item < items && lane < per;
+        const Item it = item_at(p, sd, live ? ahead_item : 0u);
+        ahead_heads = live ? it.heads : 0;
+        ahead_x = sd.x + it.b * sd.xb + it.n * sd.xn + it.h0 * sd.xh;
+        ahead_g = sd.g + it.b * sd.gb + it.n * sd.gn + it.h0 * sd.gh;
       }
-      if (ahead_head < ahead.heads) {
-        const int h = ahead.h0 + ahead_head;
-        const uint16_t* x = sd.x + ahead.b * sd.xb + ahead.n * sd.xn + h * sd.xh;
-        const uint16_t* g = sd.g + ahead.b * sd.gb + ahead.n * sd.gn + h * sd.gh;
-        const uint32_t at = to + (requested % kDepth) * (kPairs * 4 * kThreadsNr * 16);
+      if (ahead_head < ahead_heads) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          copy_16(at + (j * 4) * kThreadsNr * 16, x + oa[j]);
-          copy_16(at + (j * 4 + 1) * kThreadsNr * 16, x + ob[j]);
-          copy_16(at + (j * 4 + 2) * kThreadsNr * 16, g + oa[j]);
-          copy_16(at + (j * 4 + 3) * kThreadsNr * 16, g + ob[j]);
+          copy_16(ahead_at + (j * 4) * kThreadsNr * 16, ahead_x + oa[j]);
+          copy_16(ahead_at + (j * 4 + 1) * kThreadsNr * 16, ahead_x + ob[j]);
+          copy_16(ahead_at + (j * 4 + 2) * kThreadsNr * 16, ahead_g + oa[j]);
+          copy_16(ahead_at + (j * 4 + 3) * kThreadsNr * 16, ahead_g + ob[j]);
         }
       }
       ++requested;
+      ahead_x += sd.xh;
+      ahead_g += sd.gh;
+      ahead_at += kPairs * 4 * kThreadsNr * 16;
+      if (ahead_at == to + kDepth * (kPairs * 4 * kThreadsNr * 16)) ahead_at = to;
       if (++ahead_head == sd.per_item) {
         ahead_head = 0;
-        ++ahead_step;
+        ahead_item += my_stride;
       }
     }
     copies_commit();
@@ -450,9 +453,9 @@ __global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) request();
 
-  unsigned u = 0;
-  for (unsigned step = 0; step < steps; ++step) {
-    const unsigned item = my_first + step * my_stride;
+  unsigned slot = 0;
+  unsigned item = my_first;
+  for (unsigned step = 0; step < steps; ++step, item += my_stride) {
     const bool live = item < items && lane < per;
     const Item it = item_at(p, sd, live ? item : 0u);
     const long long pos = p.rot ? position_of(p, it.b, it.n) : 0;
@@ -461,11 +464,12 @@ __global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) load_angles<kInter>(p, pos, pos_ok, oa[j], ob[j], cs[j], sn[j]);
     uint16_t* y = sd.y + it.b * sd.yb + it.n * sd.yn + it.h0 * sd.yh;
-    for (int k = 0; k < sd.per_item; ++k, ++u) {
+    for (int k = 0; k < sd.per_item; ++k, y += sd.yh) {
       const bool row = live && k < it.heads;
       copies_wait<kDepth - 1>();
       F2 x[kPairs][8], h[kPairs][8], ss2 = pair(0.f, 0.f), dot2 = ss2;
-      const uint4* at = mine + (u % kDepth) * (kPairs * 4 * kThreadsNr);
+      const uint4* at = mine + slot * (kPairs * 4 * kThreadsNr);
+      slot = (slot + 1) % kDepth;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
         F2 g[8];
@@ -510,8 +514,8 @@ __global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
             dw[j][e] = fma2(h[j][e], n, dw[j][e]);
             o[e] = mul2(r2, fma2(n, m2, mul2(h[j][e], w[j][e])));
           }
-          *reinterpret_cast<uint4*>(y + k * sd.yh + oa[j]) = pack8(o, kBf16);
-          *reinterpret_cast<uint4*>(y + k * sd.yh + ob[j]) = pack8(o + 4, kBf16);
+          *reinterpret_cast<uint4*>(y + oa[j]) = pack8(o, kBf16);
+          *reinterpret_cast<uint4*>(y + ob[j]) = pack8(o + 4, kBf16);
         }
       }
     }
@@ -544,25 +548,31 @@ __global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
   }
 }
 
-// d gain = the sum of the blocks' partials, in block order for each of 8
-// interleaved runs, then over the runs: the same order on every launch. One
-// block per 32 elements and side.
-__global__ void __launch_bounds__(kThreadsNr) fa2_norm_rope_gain_kernel(const float* __restrict__ partials, void* dq_gain,
-                                                                        void* dk_gain, int q_blocks, int blocks, int D,
-                                                                        int gain_f32, int bf16) {
-  __shared__ float part[kThreadsNr / 32][32];
+// d gain = the sum of the blocks' partials: 32 interleaved runs of blocks, each
+// in block order, then the runs in theirs, the same order on every launch. One
+// block per 32 elements and side. Launched while the backward still runs
+// (programmatic dependent launch); it waits for it here.
+constexpr int kGainRuns = 32;
+__global__ void __launch_bounds__(32 * kGainRuns) fa2_norm_rope_gain_kernel(const float* partials, void* dq_gain,
+                                                                            void* dk_gain, int q_blocks, int blocks,
+                                                                            int D, int gain_f32, int bf16) {
+  __shared__ float part[kGainRuns][33];
   const bool is_k = blockIdx.y != 0;
   void* out = is_k ? dk_gain : dq_gain;
   if (!out) return;
   const int lane = threadIdx.x % 32, run = threadIdx.x / 32;
   const int i = blockIdx.x * 32 + lane;
+  cudaGridDependencySynchronize();
+  const int end = is_k ? blocks : q_blocks;
   float s = 0.f;
-  for (int b = (is_k ? q_blocks : 0) + run; b < (is_k ? blocks : q_blocks); b += kThreadsNr / 32)
-    s += partials[static_cast<size_t>(b) * D + i];
+#pragma unroll 10
+  for (int b = (is_k ? q_blocks : 0) + run; b < end; b += kGainRuns) s += partials[static_cast<size_t>(b) * D + i];
   part[run][lane] = s;
   __syncthreads();
   if (run != 0) return;
-  for (int k = 1; k < kThreadsNr / 32; ++k) s += part[k][lane];
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < kGainRuns; ++k) s += part[k][lane];
   if (gain_f32)
     static_cast<float*>(out)[i] = s;
   else if (bf16)
@@ -938,9 +948,18 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   const Picked kern = pick_kernel<true>(D, dtype == FA2_BF16, interleaved != 0);
   if ((rc = launch_kernel(kern.kern, *kern.prepared, grid, a.p, s)) != FA2_OK) return rc;
   if (gains) {
-    fa2_norm_rope_gain_kernel<<<dim3(D / 32, 2), kThreadsNr, 0, s>>>(a.p.partials, dq_gain, dk_gain, a.p.q_blocks,
-                                                                      grid, D, gain_f32, dtype == FA2_BF16);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / 32, 2);
+    cfg.blockDim = dim3(32 * kGainRuns);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa2_norm_rope_gain_kernel, static_cast<const float*>(a.p.partials),
+                                             dq_gain, dk_gain, a.p.q_blocks, grid, D, gain_f32,
+                                             static_cast<int>(dtype == FA2_BF16));
     if (e != cudaSuccess) return record_cuda_error(e);
   }
   return FA2_OK;
