@@ -23,7 +23,8 @@ SOURCES = ["fa2_api.cu", "fa2_noalloc.cu", "fa2_host.cu", "fa2_fwd_d32.cu", "fa2
            "fa2_fwd_d128.cu", "fa2_fwd_d256.cu",
            "fa2_fwd_d512.cu", "fa2_fwd_d1024.cu", "fa2_bwd_api.cu",
            "fa2_bwd_d32.cu", "fa2_bwd_d64.cu", "fa2_bwd_d96.cu", "fa2_bwd_d128.cu", "fa2_norm_rope.cu",
-           "fa2_cross_api.cu", "fa2_cross_rows.cu", "fa2_cross_d32.cu", "fa2_cross_d64.cu", "fa2_cross_d96.cu", "fa2_cross_d128.cu",
+           "fa2_cross_api.cu", "fa2_cross_rows.cu", "fa2_cross_short.cu",
+           "fa2_cross_d32.cu", "fa2_cross_d64.cu", "fa2_cross_d96.cu", "fa2_cross_d128.cu",
            "fa2_cross_bwd_api.cu", "fa2_cross_bwd_d32.cu", "fa2_cross_bwd_d64.cu", "fa2_cross_bwd_d96.cu",
            "fa2_cross_bwd_d128.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"

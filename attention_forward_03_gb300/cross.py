@@ -12,7 +12,7 @@ import ctypes
 import math
 
 from .binding import FA2_OK, _check, _dtype_code_of, library
-from .streams import empty_on, on_device, scratch_for, stream_handle
+from .streams import device_guard, empty_on, scratch_for, stream_handle
 
 _fwd_bytes = {}
 
@@ -97,16 +97,17 @@ def cross_attention_forward(q, k, v, scale: float | None = None, key_lengths=Non
         lse = empty_on(stream, (B, Hq, Nq), torch.float32, q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    need = _fwd_bytes.get((dev, D))
-    if need is None:
-        need = _fwd_bytes[(dev, D)] = on_device(dev, fa2_cross_fwd_workspace_bytes, D)
-    if workspace is None:
-        workspace = scratch_for("cross_fwd", need, q.device, dev, handle, stream)
-    else:
-        _check_workspace(workspace, need, dev)
-    code = on_device(dev, library().fa2_cross_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                     lse.data_ptr(), None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk, D,
-                     scale, dtc, workspace.data_ptr(), workspace.nbytes, handle)
+    with device_guard(dev):
+        need = _fwd_bytes.get((dev, D))
+        if need is None:
+            need = _fwd_bytes[(dev, D)] = fa2_cross_fwd_workspace_bytes(D)
+        if workspace is None:
+            workspace = scratch_for("cross_fwd", need, q.device, dev, handle, stream)
+        else:
+            _check_workspace(workspace, need, dev)
+        code = library().fa2_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                       None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk,
+                                       D, scale, dtc, workspace.data_ptr(), workspace.nbytes, handle)
     if code != FA2_OK:
         _check(code, "fa2_cross_fwd")
     return out, lse
@@ -147,10 +148,11 @@ def cross_attention_backward(q, k, v, o, lse, do, scale: float | None = None, ke
         workspace = empty_on(stream, max(need, 1), torch.uint8, q.device)
     else:
         _check_workspace(workspace, need, dev)
-    code = on_device(dev, library().fa2_cross_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                     do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                     None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk, D, scale, dtc,
-                     workspace.data_ptr(), workspace.nbytes, handle)
+    with device_guard(dev):
+        code = library().fa2_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                       lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                       None if key_lengths is None else key_lengths.data_ptr(), B, Hq, Hkv, Nq, Nk,
+                                       D, scale, dtc, workspace.data_ptr(), workspace.nbytes, handle)
     if code != FA2_OK:
         _check(code, "fa2_cross_bwd")
     return dq, dk, dv

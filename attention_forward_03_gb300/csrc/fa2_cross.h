@@ -54,6 +54,16 @@ constexpr size_t few_rows_workspace_bytes(int grid, int d) {
 cudaError_t launch_cross_rows(int D, bool bf16, const CUtensorMap& k, const CUtensorMap& v, const CrossRowsParams& p,
                               int grid, cudaStream_t stream);
 
+// Few keys (fa2_cross_short.cu): 128 at most, all of them in shared memory.
+constexpr int kFewKeys = 128;
+constexpr int kFewKeysRows = 64;  // query rows per unit
+struct CrossShortParams : CrossParams {  // n_qt: units per key head; num_units: BH * n_qt
+  const void* q;
+  const void* k;
+  const void* v;
+};
+cudaError_t launch_cross_short(int D, bool bf16, const CrossShortParams& p, int sms, cudaStream_t stream);
+
 // The backward on the tensor-core kernel of fa2_bwd_kernel.cuh.
 template <int D, bool kBf16>
 cudaError_t launch_cross_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,

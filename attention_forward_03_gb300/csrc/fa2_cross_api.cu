@@ -47,6 +47,17 @@ bool cross_balanced(long long units, long long nkv, bool lengths, int sms) {
   return balanced < 0.95 * rounds;
 }
 
+// Whether the few-keys kernel beats the tcgen05 one. Measured (us, few-keys
+// against tcgen05): 32 heads of 4096 rows, D = 64, 16 keys 8.7 / 20.6, 77 keys
+// 16.5 / 21.3, 128 keys 19.2 / 19.1; D = 128, 16 keys 14.6 / 26.7, 96 keys
+// 27.1 / 27.4, 128 keys 34.8 / 25.9 (its products run at the rate of
+// mma.sync); 32 heads of 17 rows, one wave whatever the keys: D = 64, 128
+// keys 3.9 / 5.6, D = 128, 128 keys 5.5 / 7.0.
+bool few_keys_pay(int D, int Nk, int64_t units, int sms) {
+  if (Nk > kFewKeys) return false;
+  return D <= 64 || Nk <= 96 || units <= 2ll * sms;
+}
+
 // The larger of the two kernels' partial results.
 size_t workspace_bytes_for(int sms, int D) {
   return std::max(stream_k_workspace_bytes(sms, D), few_rows_workspace_bytes(sms, D));
@@ -141,6 +152,19 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
     p.ws_flags = reinterpret_cast<unsigned long long*>(ws + few_rows_workspace_bytes(grid, D) - static_cast<size_t>(grid) * 8);
     p.epoch = next_launch_epoch();
     const cudaError_t e = launch_cross_rows(D, dtype == FA2_BF16, mk, mv, p, grid, s);
+    return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
+  }
+
+  const int64_t short_tiles = (rows + kFewKeysRows - 1) / kFewKeysRows;
+  if (few_keys_pay(D, Nk, bh * short_tiles, sms) && bh * short_tiles <= INT32_MAX) {
+    CrossShortParams sp = {};
+    static_cast<CrossParams&>(sp) = p;
+    sp.n_qt = (int)short_tiles;
+    sp.num_units = (int)(bh * short_tiles);
+    sp.q = Q;
+    sp.k = K;
+    sp.v = V;
+    const cudaError_t e = launch_cross_short(D, dtype == FA2_BF16, sp, sms, s);
     return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
   }
 

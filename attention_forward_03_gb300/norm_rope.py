@@ -11,13 +11,15 @@ the layout attention_forward takes, unless the caller passes views.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from .binding import Fa2Error  # noqa: F401  (what these calls raise)
 from .binding import _check, _dtype_code_of, library
-from .streams import empty_on, on_device, scratch_for, stream_handle
+from .streams import device_guard, empty_on, scratch_for, stream_handle
 
-_F_ARGS = ctypes.c_longlong * 14
-_B_ARGS = ctypes.c_longlong * 20
+# the strides a call passes, as the C side reads them (bytes are passed by address)
+_FWD_STRIDES = struct.Struct("=14q").pack
+_BWD_STRIDES = struct.Struct("=20q").pack
 _NO_VIEW = (0, 0, 0)
 _bwd_bytes = {}
 
@@ -116,10 +118,6 @@ def _check_tables(cos, sin, positions, B, N, dev):
     return 2 * half, rows, 1 if pt == torch.int64 else 0, pb, pn
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def qk_norm_rope_forward(q, k, q_gain=None, k_gain=None, cos=None, sin=None, positions=None, eps: float = 1e-6,
                          interleaved: bool = False, q_out=None, k_out=None, stream=None):
     """RMS norm of each head of q and k, times its gain, then the position rotation; returns (q', k').
@@ -160,10 +158,15 @@ def qk_norm_rope_forward(q, k, q_gain=None, k_gain=None, cos=None, sin=None, pos
         kos = (Hkv * N * D, N * D, D)
     else:
         kos = _check_view("k_out", k_out, B, Hkv, N, D, dt, dev)
-    strides = _F_ARGS(*qs, *ks, *qos, *kos, pb, pn)
-    code = on_device(dev, library().fa2_qk_norm_rope_fwd, _ptr(q), _ptr(k), _ptr(q_gain), _ptr(k_gain), _ptr(cos),
-                     _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), strides, B, Hq, Hkv, N, D, rot, rows, eps,
-                     1 if interleaved else 0, gain_f32, p64, dtc, handle)
+    strides = _FWD_STRIDES(*qs, *ks, *qos, *kos, pb, pn)
+    with device_guard(dev):
+        code = library().fa2_qk_norm_rope_fwd(
+            q.data_ptr() if q is not None else None, k.data_ptr() if k is not None else None,
+            q_gain.data_ptr() if q_gain is not None else None, k_gain.data_ptr() if k_gain is not None else None,
+            cos.data_ptr() if rot else None, sin.data_ptr() if rot else None,
+            positions.data_ptr() if positions is not None else None, q_out.data_ptr() if q is not None else None,
+            k_out.data_ptr() if k is not None else None, strides, B, Hq, Hkv, N, D, rot, rows, eps,
+            1 if interleaved else 0, gain_f32, p64, dtc, handle)
     if code:
         _check(code, "fa2_qk_norm_rope_fwd")
     return q_out, k_out
@@ -227,11 +230,18 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain=None, k_gain=None, cos=No
                 workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on q's device")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    strides = _B_ARGS(*gqs, *gks, *qs, *ks, *dqs, *dks, pb, pn)
-    code = on_device(dev, library().fa2_qk_norm_rope_bwd, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_gain),
-                     _ptr(k_gain), _ptr(cos), _ptr(sin), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dq_gain),
-                     _ptr(dk_gain), strides, B, Hq, Hkv, N, D, rot, rows, eps, 1 if interleaved else 0, gain_f32, p64,
-                     dtc, ws_ptr, ws_bytes, handle)
+    strides = _BWD_STRIDES(*gqs, *gks, *qs, *ks, *dqs, *dks, pb, pn)
+    has_q, has_k = q is not None, k is not None
+    with device_guard(dev):
+        code = library().fa2_qk_norm_rope_bwd(
+            dq_out.data_ptr() if has_q else None, dk_out.data_ptr() if has_k else None,
+            q.data_ptr() if has_q else None, k.data_ptr() if has_k else None,
+            q_gain.data_ptr() if q_gain is not None else None, k_gain.data_ptr() if k_gain is not None else None,
+            cos.data_ptr() if rot else None, sin.data_ptr() if rot else None,
+            positions.data_ptr() if positions is not None else None, dq.data_ptr() if has_q else None,
+            dk.data_ptr() if has_k else None, dq_gain.data_ptr() if q_gain is not None else None,
+            dk_gain.data_ptr() if k_gain is not None else None, strides, B, Hq, Hkv, N, D, rot, rows, eps,
+            1 if interleaved else 0, gain_f32, p64, dtc, ws_ptr, ws_bytes, handle)
     if code:
         _check(code, "fa2_qk_norm_rope_bwd")
     return dq, dk, dq_gain, dk_gain

@@ -64,10 +64,22 @@ def scratch_for(kind, need, device, index, handle, stream):
     return ws
 
 
-def on_device(index: int, fn, *args):
-    """fn(*args) with device `index` current (switched only where it is not)."""
+class _Here:
+    """A guard that has nothing to do."""
+
+    __slots__ = ()
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def device_guard(index: int):
+    """`with device_guard(i):` makes device i current (nothing happens where it already is)."""
     import torch
-    if torch.cuda.current_device() == index:
-        return fn(*args)
-    with torch.cuda.device(index):
-        return fn(*args)
+    return _here if torch.cuda.current_device() == index else torch.cuda.device(index)

@@ -130,6 +130,11 @@ SHAPES = [  # B, Hq, Hkv, Nq, Nk, D, dtype, lengths
     (1, 4, 2, 100, 1, 128, F16, None),
     (1, 2, 2, 256, 16, 64, BF16, None),
     (1, 2, 2, 257, 1000, 32, F16, [993]),
+    (1, 4, 2, 63, 128, 128, BF16, [127]),
+    (3, 2, 2, 65, 127, 96, F16, [0, 16, 127]),
+    (2, 6, 2, 700, 33, 32, BF16, [33, 17]),
+    (1, 2, 2, 3000, 77, 64, F16, None),
+    (1, 2, 1, 100, 129, 64, F16, [129]),
     (5, 4, 4, 300, 513, 64, F16, [0, 1, 512, 513, 400]),
     (3, 6, 2, 200, 700, 128, BF16, [700, 16, 450]),
     (2, 5, 5, 513, 640, 96, BF16, None),
