@@ -147,6 +147,7 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
     if (!encode_tile_map(&mk, K, (int)bh, Nk, D, dtype, 16u) || !encode_tile_map(&mv, V, (int)bh, Nk, D, dtype, 16u))
       return record_cuda_error(cudaErrorInvalidValue);
     p.q = Q;
+    p.test_withhold = take_test_withhold();
     p.ws_o = reinterpret_cast<float*>(ws);
     p.ws_stats = p.ws_o + static_cast<size_t>(grid) * kFewRows * D;
     p.ws_flags = reinterpret_cast<unsigned long long*>(ws + few_rows_workspace_bytes(grid, D) - static_cast<size_t>(grid) * 8);
@@ -172,10 +173,10 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   if (!encode_tile_map(&mq, Q, (int)bh, (int)rows, D, dtype, 128u) || !encode_tile_map(&mk, K, (int)bh, Nk, D, dtype, 128u) ||
       !encode_tile_map(&mv, V, (int)bh, Nk, D, dtype, 128u) || !encode_tile_map(&mo, O, (int)bh, (int)rows, D, dtype, 128u))
     return record_cuda_error(cudaErrorInvalidValue);
+  p.test_withhold = take_test_withhold();
   p.n_qt = (int)n_qt;
   p.num_units = (int)(bh * n_qt);
   p.nkv_full = (Nk + kKeys - 1) / kKeys;
-  p.test_withhold = take_test_withhold();
   int grid;
   if (workspace && cross_balanced(p.num_units, p.nkv_full, key_lengths != nullptr, sms)) {
     p.stream_k = 1;

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     while (requested < s1) {
       const bool any = has_keys(ahead);
       if (any) {
-        if (lane == 0) {
+        if (lane == 0 && !(p.test_withhold && requested == s0)) {  // test hook: the first tile never arrives
           const uint32_t dst = ring + static_cast<uint32_t>(into * L::kPieceBytes), bar = bars + 8 * into;
           const int key = ahead.tile * kFewRowsKeys + warp * kPiece, bh = ahead.b * p.heads + ahead.head;
           mbar_arrive_expect_tx(bar, L::kPieceBytes);

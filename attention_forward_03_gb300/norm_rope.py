@@ -219,20 +219,19 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain=None, k_gain=None, cos=No
         dks = _check_view("dk", dk, B, Hkv, N, D, dt, dev)
         if k_gain is not None:
             dk_gain = empty_on(stream, (D,), k_gain.dtype, device)
-    ws_ptr, ws_bytes = None, 0
+    need = 0
     if q_gain is not None or k_gain is not None:
         need = _bwd_bytes.get(D)
         if need is None:
             need = _bwd_bytes[D] = fa2_qk_norm_rope_bwd_workspace_bytes(D)
-        if workspace is None:
-            workspace = scratch_for("norm_rope_bwd", need, device, dev, handle, stream)
-        elif workspace.get_device() != dev or not workspace.is_contiguous() or \
-                workspace.numel() * workspace.element_size() < need:
+        if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous() or
+                                      workspace.nbytes < need):
             raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on q's device")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
     strides = _BWD_STRIDES(*gqs, *gks, *qs, *ks, *dqs, *dks, pb, pn)
     has_q, has_k = q is not None, k is not None
     with device_guard(dev):
+        if need and workspace is None:
+            workspace = scratch_for("norm_rope_bwd", need, device, dev, handle, stream)
         code = library().fa2_qk_norm_rope_bwd(
             dq_out.data_ptr() if has_q else None, dk_out.data_ptr() if has_k else None,
             q.data_ptr() if has_q else None, k.data_ptr() if has_k else None,
@@ -241,7 +240,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain=None, k_gain=None, cos=No
             positions.data_ptr() if positions is not None else None, dq.data_ptr() if has_q else None,
             dk.data_ptr() if has_k else None, dq_gain.data_ptr() if q_gain is not None else None,
             dk_gain.data_ptr() if k_gain is not None else None, strides, B, Hq, Hkv, N, D, rot, rows, eps,
-            1 if interleaved else 0, gain_f32, p64, dtc, ws_ptr, ws_bytes, handle)
+            1 if interleaved else 0, gain_f32, p64, dtc, workspace.data_ptr() if need else None,
+            workspace.nbytes if need else 0, handle)
     if code:
         _check(code, "fa2_qk_norm_rope_bwd")
     return dq, dk, dq_gain, dk_gain

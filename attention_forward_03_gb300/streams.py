@@ -50,7 +50,7 @@ _scratch = {}
 def scratch_for(kind, need, device, index, handle, stream):
     """A workspace of `need` bytes for a call on stream `handle` of device `index`.
 
-    One per kind, size and current stream is kept: calls on one stream are
+    To be called with that device current. One per kind, size and current stream is kept: calls on one stream are
     ordered, so they may share it. A call that names its stream, and one that
     is being captured (two graphs may be replayed at once), gets its own.
     """

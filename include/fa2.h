@@ -454,7 +454,8 @@ FA2_API int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const v
  *             at the same time. With it the work of long key rows is cut into
  *             equal shares for all SMs; without it every work unit runs on
  *             one SM. A captured call can be replayed; the replays share the
- *             workspace.
+ *             workspace. (After a timeout that fa2_device_status reports, the
+ *             call is captured anew.)
  * O and LSE are fully overwritten; neither overlaps an input. Asynchronous,
  * allocation-free; errors as fa2_fwd_ws.
  */
@@ -528,7 +529,8 @@ FA2_API int fa2_set_watchdog_ns(unsigned long long ns);
 /*
  * fa2_test_withhold_next_load — test hook for the watchdog. When enable is
  * nonzero, the next launch of this library (process-wide, one launch only:
- * a forward kernel, or the main kernel of fa2_bwd) withholds its first K/V
+ * a forward kernel, the main kernel of fa2_bwd or fa2_cross_bwd, or a kernel
+ * of fa2_cross_fwd that waits for tiles) withholds its first K/V
  * tile: the waits for that tile run out after the watchdog time, the kernel
  * records the wait site in the watchdog word, winds down without leaving
  * work in flight, and its outputs (O/LSE, or dQ/dK/dV) are left unspecified.

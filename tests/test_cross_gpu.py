@@ -1,22 +1,4 @@
-"""Cross attention on the GPU against its definition in 64 bits.
-
-Bounds for O, per element, with A = sum_j p_ij |v_j| (u = half a step of the
-16-bit type relative to the value): the weights are rounded once (u * A), the
-result once (u * |O|). The 32-bit part: a score is a sum of D products in
-32 bits, off by at most 16 steps of 2^-24 of s = scale * sum_d |q_d k_d| (16
-accumulation steps at D = 128), which the exponential turns into a relative
-error of its weight; ex2 and the sums add less than 32 such steps. In fp16 a
-weight below 2^-14 (of a sum that is at least 1) is off by 2^-25 instead. LSE:
-the same 32-bit part, and 4 steps of its own size for the logarithm and the
-product with ln 2.
-
-Bounds for the gradients, from O and LSE as the call got them: P and dS are
-rounded once each (u * `rounded`, the oracle's sum of the terms' sizes), the
-result once (u * |x|). The 32-bit part: weights off by 16 steps of s and 4 of
-|LSE| (relative to `rounded`), dP and Delta by 16 steps of 2^-24 of the
-products they are sums of (2^-20 * `summed`), and 64 steps for the sums. fp16:
-P or dS below 2^-14 is off by 2^-25 of the other factor instead.
-"""
+"""Cross attention on the GPU against its definition in 64 bits (the bounds: bounds.py)."""
 from __future__ import annotations
 
 import math
@@ -24,12 +6,10 @@ import math
 import pytest
 import torch
 
+from bounds import check_cross_bwd as check_bwd, check_cross_fwd as check_fwd
 from oracle import cross as ref
 
 pytestmark = pytest.mark.gpu
-
-E32 = 2.0 ** -24
-
 
 @pytest.fixture(scope="module", autouse=True)
 def lib():
@@ -57,60 +37,6 @@ def inputs(B, Hq, Hkv, Nq, Nk, D, dtype, lengths=None, seed=0, garbage=float("na
         k.masked_fill_(behind[:, None, :, None], garbage)
         v.masked_fill_(behind[:, None, :, None], garbage)
     return q, k, v, n
-
-
-def sizes_of(q, k, scale, n):
-    """max over all rows of scale * sum_d |q_d k_d|."""
-    most = 0.0
-    for b, h, g, m in ref._heads(q, k, n):
-        if m:
-            most = max(most, float((q[b, h].float().abs() @ k[b, g, :m].float().abs().T).max()) * scale)
-    return most
-
-
-def check_fwd(o, lse, q, k, v, scale, n):
-    want_o, want_l, a = ref.forward(q, k, v, scale, n)
-    u = torch.finfo(q.dtype).eps / 2
-    s32 = (16 * sizes_of(q, k, scale, n) + 32) * E32
-    tol = u * (a + want_o.abs()) * (1 + u) + s32 * a
-    if q.dtype == torch.float16:
-        vs = v.float().nan_to_num(0.0).abs().sum(2).repeat_interleave(q.shape[1] // v.shape[1], 1)
-        tol = tol + 2.0 ** -25 * (vs.cpu().double()[:, :, None] + 1)
-    o, lse = o.cpu().double(), lse.cpu().double()
-    empty = want_l.isinf()
-    assert torch.equal(lse.isinf(), empty) and bool((lse[empty] > 0).all())
-    assert bool((o[empty] == 0).all())
-    assert not o.isnan().any() and not lse.isnan().any()
-    bad = (o - want_o).abs() > tol
-    assert not bad.any(), f"O: {int(bad.sum())} of {bad.numel()}, worst {float(((o - want_o).abs() / tol.clamp(min=1e-30)).max())} tolerances"
-    dl = (lse - want_l)[~empty].abs()
-    tl = s32 + 4 * E32 * want_l[~empty].abs()
-    assert bool((dl <= tl).all()), f"LSE off by {float((dl / tl).max())} tolerances"
-
-
-def check_bwd(grads, q, k, v, o, lse, do, scale, n):
-    want = ref.backward(q, k, v, o, lse, do, scale, n)
-    u = torch.finfo(q.dtype).eps / 2
-    fin = lse[~lse.isinf()]
-    s32 = (16 * sizes_of(q, k, scale, n) + 4 * (float(fin.abs().max()) if fin.numel() else 0) + 64) * E32
-    group = q.shape[1] // k.shape[1]
-    for name, got in zip(("dq", "dk", "dv"), grads):
-        x, rounded, summed = want[name]
-        tol = u * (rounded + x.abs()) * (1 + u) + s32 * rounded + 2.0 ** -20 * summed
-        if q.dtype == torch.float16:
-            if name == "dq":
-                other = k.float().nan_to_num(0.0, 0.0, 0.0).abs().sum(2, keepdim=True).repeat_interleave(group, 1) * scale
-            else:
-                other = (q.float() * scale if name == "dk" else do.float()).abs().sum(2, keepdim=True)
-                other = other.unflatten(1, (k.shape[1], group)).sum(2)
-            tol = tol + 2.0 ** -25 * (other.cpu().double() + 1)
-        got = got.cpu().double()
-        assert not got.isnan().any(), name
-        bad = (got - x).abs() > tol
-        assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()}, worst {float(((got - x).abs() / tol.clamp(min=1e-30)).max())} tolerances"
-        if n is not None and name != "dq":  # zeros behind the keys, exactly
-            for b in range(k.shape[0]):
-                assert bool((got[b, :, min(max(int(n[b]), 0), k.shape[2]):] == 0).all()), name
 
 
 F16, BF16 = torch.float16, torch.bfloat16

@@ -1,26 +1,13 @@
-"""The head norm with position rotation on the GPU against its definition in 64 bits.
-
-Bounds, for a result y that is a sum of terms of total size m (the oracle's
-magnitude): half a step of the 16-bit type, |y| * eps16 / 2, for the one
-rounding; and 32 steps of 2^-24 * m for the arithmetic in 32 bits: the mean
-of squares (at most 32 + 5 + 1 additions, each a relative half step, halved
-by the root), rsqrtf (2 steps), and up to 5 products and sums after it,
-below 30 half steps together. The backward's mean adds as many again: 64. The
-gain gradient is one such product per row, added up in at most 8 + 5 + 8 rows,
-warps and threads of a block and 1280 / 8 + 8 blocks, below 256 + 64 half steps.
-"""
+"""The head norm with position rotation on the GPU against its definition in 64 bits (the bounds: bounds.py)."""
 from __future__ import annotations
 
 import pytest
 import torch
 
+from bounds import near
 from oracle import norm_rope as ref
 
 pytestmark = pytest.mark.gpu
-
-EPS32 = 2.0 ** -24
-TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 0.0}  # half a step of the smallest fp16 subnormals
-
 
 @pytest.fixture(scope="module", autouse=True)
 def lib():
@@ -32,16 +19,6 @@ def lib():
 def ops():
     import attention_forward_03_gb300 as fa2
     return fa2
-
-
-def near(got, want, mag, steps, dtype=None):
-    dtype = dtype or got.dtype
-    half = torch.finfo(dtype).eps / 2
-    tol = half * want.abs() + steps * EPS32 * mag * (1 + half) + TINY.get(dtype, 0.0)
-    got = got.cpu().double()
-    assert torch.equal(got.isnan(), want.isnan())
-    bad = (got - want).abs() > tol
-    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((got - want).abs() / tol).nan_to_num(0).max())} tolerances"
 
 
 def tables(rows, rot):
