@@ -524,9 +524,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       // tile and its rows are discarded), B = dS^T MN-major (N = SR query
       // columns, panels of 64 16 KB apart), 8 steps of 16 keys.
       // Cross attention: only the steps with keys.
-      auto issue_dq = [&]([[maybe_unused]] const Seg& sgm) {
-        [[maybe_unused]] int key_steps = kBwdKeys / 16;
-        if constexpr (kCross) key_steps = cross_key_steps(sgm.n_keys - sgm.kv * kBwdKeys);
+      auto issue_dq = [&]([[maybe_unused]] int key_steps) {
         const uint32_t kt_lo = desc_lo_sw128(sK, kPanelBytes);
         const uint32_t ds_mn = desc_lo_sw128(sDS, kPanelBytes);
         auto one = [&](int kk) {
@@ -561,6 +559,8 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         Seg sg;
         while (ok && advance(cur, sg)) {
           const int n_steps = sg.i_end - sg.i_begin;
+          int key_steps = kBwdKeys / 16;  // 16-key steps of the tile with keys
+          if constexpr (kCross) key_steps = cross_key_steps(sg.n_keys - sg.kv * kBwdKeys);
           if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
             ok = false;
             break;
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
                 break;
               }
               tc_fence_after_sync();
-              issue_dq(sg);
+              issue_dq(key_steps);
               mma_commit(bar_p_free);
               mma_commit(bar_dq_full);
             }
@@ -640,6 +640,8 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         Seg sg;
         while (ok && advance(wcur, sg)) {
           const int n_steps = sg.i_end - sg.i_begin;
+          int key_steps = kBwdKeys / 16;  // 16-key steps of the tile with keys
+          if constexpr (kCross) key_steps = cross_key_steps(sg.n_keys - sg.kv * kBwdKeys);
           if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
             ok = false;
             break;
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
               break;
             }
             tc_fence_after_sync();
-            issue_dq(sg);
+            issue_dq(key_steps);
             mma_commit(bar_p_free);
             mma_commit(bar_dq_full);
             cur = nxt;
