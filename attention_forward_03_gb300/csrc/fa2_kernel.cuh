@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return steps;
         };
         // End of the segment's full tiles (its last tile is the unit's and short, or e).
-        auto full_end = [&]([[maybe_unused]] const Seg& s, int e) -> int {
+        [[maybe_unused]] auto full_end = [&](const Seg& s, int e) -> int {
           if constexpr (kCross) return e == s.nkv && s.n_keys < e * kKeys ? e - 1 : e;
           else return e;
         };
@@ -447,24 +447,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && advance(cur, w)) {
               const int b = w.kv_begin, e = w.kv_end;
               const int n_sub = live_subtiles(w);
-              auto tile = [&](int j, auto tail) {
-                const int slot_v = take(base_idx + v_index(j, b, e), 1u);
-                if (slot_v < 0) { ok = false; return; }
-                int steps = kKeys / 16;
-                if constexpr (tail.value) steps = clean_v(w, j, slot_v);
-                for (int t = 0; t < n_sub; ++t) {
-                  if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
-                  p_full_ph[t] ^= 1u;
-                  tc_fence_after_sync();
-                  issue_pv(t, slot_v, j > b, tail, steps);
-                  mma_commit(bar_p_free0 + 8 * t);
-                  if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
+              if constexpr (!kCross) {
+                for (int j = b; j < e && ok; ++j) {
+                  const int slot_v = take(base_idx + v_index(j, b, e), 1u);
+                  if (slot_v < 0) { ok = false; break; }
+                  for (int t = 0; t < 2; ++t) {
+                    if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; break; }
+                    p_full_ph[t] ^= 1u;
+                    tc_fence_after_sync();
+                    issue_pv(t, slot_v, j > b, std::false_type{}, 0);
+                    mma_commit(bar_p_free0 + 8 * t);
+                    if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
+                  }
+                  if (!ok) break;
+                  mma_commit(bar_empty(slot_v));
                 }
-                mma_commit(bar_empty(slot_v));
-              };
-              const int e_full = full_end(w, e);
-              for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
-              if constexpr (kCross) {
+              } else {
+                auto tile = [&](int j, auto tail) {
+                  const int slot_v = take(base_idx + v_index(j, b, e), 1u);
+                  if (slot_v < 0) { ok = false; return; }
+                  int steps = kKeys / 16;
+                  if constexpr (tail.value) steps = clean_v(w, j, slot_v);
+                  for (int t = 0; t < n_sub; ++t) {
+                    if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
+                    p_full_ph[t] ^= 1u;
+                    tc_fence_after_sync();
+                    issue_pv(t, slot_v, j > b, tail, steps);
+                    mma_commit(bar_p_free0 + 8 * t);
+                    if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
+                  }
+                  mma_commit(bar_empty(slot_v));
+                };
+                const int e_full = full_end(w, e);
+                for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
                 if (e_full < e && ok) tile(e_full, std::true_type{});
               }
               base_idx += 2u * static_cast<uint32_t>(e - b);
@@ -505,30 +520,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             skip_s = et == b;
             if (slot_k < 0 || !next_s(slot_k)) { ok = false; break; }
             if (e - b == 1) mma_commit(bar_q_empty);
-            auto tile = [&](int j, auto tail) {
-              if (j + 1 < e) {
-                slot_k = take(base_idx + k_index(j + 1, b), 0u);
-                skip_s = j + 1 >= et;
-                if (slot_k < 0 || !next_s(slot_k)) { ok = false; return; }
-                if (j + 2 == e) mma_commit(bar_q_empty);
+            if constexpr (!kCross) {
+              for (int j = b; j < e && ok; ++j) {
+                if (j + 1 < e) {
+                  slot_k = take(base_idx + k_index(j + 1, b), 0u);
+                  skip_s = j + 1 >= et;
+                  if (slot_k < 0 || !next_s(slot_k)) { ok = false; break; }
+                  if (j + 2 == e) mma_commit(bar_q_empty);
+                }
+                const int slot_v = take(base_idx + v_index(j, b, e), 1u);
+                if (slot_v < 0) { ok = false; break; }
+                if (j < et) {
+                  if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph, wd, kSiteMmaPFull, true, kNapNs)) { ok = false; break; }
+                  p_full_ph ^= 1u;
+                  tc_fence_after_sync();
+                  issue_pv(t, slot_v, j > b, std::false_type{}, 0);
+                  mma_commit(bar_p_free0 + 8 * t);
+                  if (j == et - 1) mma_commit(bar_o_full0 + 8 * t);
+                }
+                mma_commit(bar_empty(slot_v));
               }
-              const int slot_v = take(base_idx + v_index(j, b, e), 1u);
-              if (slot_v < 0) { ok = false; return; }
-              if (j < et) {
-                int steps = kKeys / 16;
-                if constexpr (tail.value) steps = clean_v(w, j, slot_v);
-                if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph, wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
-                p_full_ph ^= 1u;
-                tc_fence_after_sync();
-                issue_pv(t, slot_v, j > b, tail, steps);
-                mma_commit(bar_p_free0 + 8 * t);
-                if (j == et - 1) mma_commit(bar_o_full0 + 8 * t);
-              }
-              mma_commit(bar_empty(slot_v));
-            };
-            const int e_full = full_end(w, e);
-            for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
-            if constexpr (kCross) {
+            } else {
+              auto tile = [&](int j, auto tail) {
+                if (j + 1 < e) {
+                  slot_k = take(base_idx + k_index(j + 1, b), 0u);
+                  skip_s = j + 1 >= et;
+                  if (slot_k < 0 || !next_s(slot_k)) { ok = false; return; }
+                  if (j + 2 == e) mma_commit(bar_q_empty);
+                }
+                const int slot_v = take(base_idx + v_index(j, b, e), 1u);
+                if (slot_v < 0) { ok = false; return; }
+                if (j < et) {
+                  int steps = kKeys / 16;
+                  if constexpr (tail.value) steps = clean_v(w, j, slot_v);
+                  if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph, wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
+                  p_full_ph ^= 1u;
+                  tc_fence_after_sync();
+                  issue_pv(t, slot_v, j > b, tail, steps);
+                  mma_commit(bar_p_free0 + 8 * t);
+                  if (j == et - 1) mma_commit(bar_o_full0 + 8 * t);
+                }
+                mma_commit(bar_empty(slot_v));
+              };
+              const int e_full = full_end(w, e);
+              for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
               if (e_full < e && ok) tile(e_full, std::true_type{});
             }
             base_idx += 2u * static_cast<uint32_t>(e - b);
