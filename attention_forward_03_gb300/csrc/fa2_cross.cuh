@@ -17,7 +17,7 @@ struct CrossSegment : Segment {
 
 // Where this CTA's stream-K share begins, found once per CTA.
 struct CrossStart {
-  long long total;    // K/V-tile steps of the whole call
+  long long total;    // steps of the whole call
   long long b_start;  // first step of batch entry b
   int b;              // batch entry that holds the share's first step
   int shares;         // CTAs with a share: at most the grid, and total / the least share
@@ -32,7 +32,7 @@ struct CrossCursor {
 __device__ __forceinline__ int cross_tiles(int n_keys) { return max(1, (n_keys + kKeys - 1) / kKeys); }
 
 __device__ __forceinline__ long long cross_batch_steps(const CrossParams& p, int b) {
-  return static_cast<long long>(p.heads) * p.n_qt * cross_tiles(cross_keys(p, b));
+  return static_cast<long long>(p.heads) * p.n_qt * (cross_tiles(cross_keys(p, b)) + p.unit_cost);
 }
 
 __device__ __forceinline__ long long cross_share_begin(const CrossStart& st, int c) {
@@ -120,25 +120,34 @@ __device__ __forceinline__ bool cross_next_segment(CrossCursor& c, CrossSegment&
     s.unit_end = 0;
     return true;
   }
-  if (c.step >= c.end) return false;
-  for (;;) {
-    s.n_keys = cross_keys(p, c.b);
-    s.nkv = cross_tiles(s.n_keys);
-    const long long steps = static_cast<long long>(p.heads) * p.n_qt * s.nkv;
-    if (c.step < c.b_start + steps) break;
-    c.b_start += steps;
-    ++c.b;
+  // The steps of a unit: p.unit_cost that stand for no tile, then its
+  // tiles. A share that ends among the first has no tile of the unit; the next
+  // share then holds all of them.
+  while (c.step < c.end) {
+    long long per_unit;
+    for (;;) {
+      s.n_keys = cross_keys(p, c.b);
+      s.nkv = cross_tiles(s.n_keys);
+      per_unit = s.nkv + p.unit_cost;
+      const long long steps = static_cast<long long>(p.heads) * p.n_qt * per_unit;
+      if (c.step < c.b_start + steps) break;
+      c.b_start += steps;
+      ++c.b;
+    }
+    const long long r = c.step - c.b_start;
+    const long long unit = r / per_unit;
+    const long long from = r - unit * per_unit, to = min(per_unit, from + (c.end - c.step));
+    s.unit_end = c.step - from + per_unit;
+    c.step += to - from;
+    s.kv_begin = static_cast<int>(max(from - p.unit_cost, 0ll));
+    s.kv_end = static_cast<int>(max(to - p.unit_cost, 0ll));
+    if (s.kv_end <= s.kv_begin) continue;
+    const int head = static_cast<int>(unit / p.n_qt);
+    s.bh = c.b * p.heads + head;
+    s.q0 = static_cast<int>(unit - static_cast<long long>(head) * p.n_qt) * kSubTiles * kRows;
+    return true;
   }
-  const long long r = c.step - c.b_start;
-  const long long unit = r / s.nkv;
-  const int head = static_cast<int>(unit / p.n_qt);
-  s.bh = c.b * p.heads + head;
-  s.q0 = static_cast<int>(unit - static_cast<long long>(head) * p.n_qt) * kSubTiles * kRows;
-  s.kv_begin = static_cast<int>(r - unit * s.nkv);
-  s.kv_end = static_cast<int>(min(static_cast<long long>(s.nkv), s.kv_begin + (c.end - c.step)));
-  s.unit_end = c.step - s.kv_begin + s.nkv;
-  c.step += s.kv_end - s.kv_begin;
-  return true;
+  return false;
 }
 
 // The backward's walk: units are (key head, K/V tile), each with the nq query

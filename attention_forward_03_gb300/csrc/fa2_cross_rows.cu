@@ -71,16 +71,26 @@ struct RowsLayout {
 
 __device__ __forceinline__ int row_tiles(int n_keys) { return max(1, (n_keys + kFewRowsKeys - 1) / kFewRowsKeys); }
 
-// A position in the sequence of tiles.
+// What a unit counts in the equal shares besides its tiles: the warps' merge
+// (us, by the cost 0, 1, 2, 3: 16 x 8 key heads of 512 .. 8192 keys, D = 64
+// 35.6, 31.0, 31.1, 31.4; 32 x 8 of 32 .. 1024 keys, D = 128 23.9, 19.4, 19.3,
+// 19.9; 64 x 8 of 0 .. 4096 keys, D = 128 91.5, 89.6, 88.4, 88.2).
+constexpr int kRowsUnitCost = 2;
+
+// A position in the sequence of tiles, and its step: a unit has kRowsUnitCost
+// steps that stand for no tile before those of its tiles.
 struct TileCursor {
   int b, head, tile, tiles, n_keys;
+  long long step;
   __device__ __forceinline__ void enter(const CrossParams& p) {
     n_keys = b < p.B ? cross_keys(p, b) : 0;
     tiles = row_tiles(n_keys);
   }
   __device__ __forceinline__ void next(const CrossParams& p) {
+    ++step;
     if (++tile < tiles) return;
     tile = 0;
+    step += kRowsUnitCost;
     if (++head < p.heads) return;
     head = 0;
     ++b;
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 
   // every warp finds the share and sets up its own ring
   const CrossStart st = cross_find_start(p.B, !p.key_lengths, kLeastTiles, [&](int b) {
-    return static_cast<long long>(p.heads) * row_tiles(cross_keys(p, b));
+    return static_cast<long long>(p.heads) * (row_tiles(cross_keys(p, b)) + kRowsUnitCost);
   });
   if (lane == 0) {
     for (int i = 0; i < L::kStages; ++i) mbar_init(bars + 8 * i, 1);
@@ -220,28 +230,29 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     }
   }
   const long long s0 = cross_share_begin(st, blockIdx.x), s1 = cross_share_begin(st, blockIdx.x + 1);
-  if (s0 >= s1) return;
-
   TileCursor cur;  // the tile being computed
   cur.b = st.b;
   cur.enter(p);
   {
     const long long r = s0 - st.b_start;
-    cur.head = static_cast<int>(r / cur.tiles);
-    cur.tile = static_cast<int>(r - static_cast<long long>(cur.head) * cur.tiles);
+    cur.head = static_cast<int>(r / (cur.tiles + kRowsUnitCost));
+    const long long at = r - static_cast<long long>(cur.head) * (cur.tiles + kRowsUnitCost);
+    cur.tile = static_cast<int>(max(at - kRowsUnitCost, 0ll));
+    cur.step = s0 - at + kRowsUnitCost + cur.tile;
   }
+  if (cur.step >= s1) return;  // no share, or one without a tile
+  const long long first_step = cur.step;
   // whether this warp's piece of a tile has a key
   auto has_keys = [&](const TileCursor& t) { return t.tile * kFewRowsKeys + warp * kPiece < t.n_keys; };
   TileCursor ahead = cur;  // the tile whose piece is requested next
-  long long requested = s0;
   int into = 0;       // its ring slot
   int under_way = 0;  // pieces requested and not yet used
   const uint64_t once = l2_policy_evict_first();
   auto request = [&]() {
-    while (requested < s1) {
+    while (ahead.step < s1) {
       const bool any = has_keys(ahead);
       if (any) {
-        if (lane == 0 && !(p.test_withhold && requested == s0)) {  // test hook: the first tile never arrives
+        if (lane == 0 && !(p.test_withhold && ahead.step == first_step)) {  // test hook: the first tile never arrives
           const uint32_t dst = ring + static_cast<uint32_t>(into * L::kPieceBytes), bar = bars + 8 * into;
           const int key = ahead.tile * kFewRowsKeys + warp * kPiece, bh = ahead.b * p.heads + ahead.head;
           mbar_arrive_expect_tx(bar, L::kPieceBytes);
@@ -255,7 +266,6 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         ++under_way;
       }
       ahead.next(p);
-      ++requested;
       if (any) return;
     }
   };
@@ -388,7 +398,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   bool ok = true;
   int slot = 0;
   uint32_t phase = 0;
-  for (long long s = s0; s < s1; ++s) {
+  while (cur.step < s1) {
     if (has_keys(cur)) {
       ok = ok && wait_bounded(bars + 8 * slot, phase, wd, kSiteRowsPiece);
       ok = __all_sync(0xffffffffu, ok);
@@ -407,9 +417,10 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const TileCursor done = cur;
     cur.next(p);
     const bool unit_end = done.tile == done.tiles - 1;
-    if (!unit_end && s + 1 < s1) continue;
+    const bool more = cur.step < s1;
+    if (!unit_end && more) continue;
     // ------------------------------------------- the end of a unit (or share)
-    if (s + 1 < s1) load_q(cur);  // under way while the warps merge
+    if (more) load_q(cur);  // under way while the warps merge
     // the warps' bases and sums (each over the 4 threads of a row)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -428,7 +439,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     // the holders of the unit's other tiles, if it is cut
     int last = blockIdx.x;
     if (from_start && !unit_end) {
-      const long long end = s + 1 + (done.tiles - 1 - done.tile);  // one past the unit's last tile
+      const long long end = done.step + done.tiles - done.tile;  // one past the unit's last tile
       while (last + 1 < st.shares && cross_share_begin(st, last + 1) < end) ++last;
     }
     ok = !__syncthreads_or(!ok);
