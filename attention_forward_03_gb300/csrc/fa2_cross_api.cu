@@ -52,8 +52,10 @@ bool cross_balanced(long long units, long long nkv, bool lengths, int sms) {
 // the short units of a padded batch came last (us, by the cost 0, 2, 3, 4: 4 x
 // 16 heads of 2048 rows over 2048, 4096, 6144 and 8192 keys, D = 128: 235, 221,
 // 221, 216; 8 x 8 heads of 1024 rows over 256, 512 .. 2048 keys: D = 128 59.9,
-// 47.2, 46.3, 46.0, D = 64 46.5, 34.2, 34.3, 34.6).
-constexpr int unit_cost(int D) { return D <= 64 ? 3 : 4; }
+// 47.2, 46.3, 46.0, D = 64 46.5, 34.2, 34.3, 34.6). Units of one length keep
+// equal tiles: there every CTA has about as many segments as any other (8
+// heads of 4096 rows x 8192 keys, D = 128: 90.6 with cost 0, 94.5 with 4).
+constexpr int unit_cost(int D, bool lengths) { return !lengths ? 0 : D <= 64 ? 3 : 4; }
 
 // Whether the few-keys kernel beats the tcgen05 one. Measured (us, few-keys
 // against tcgen05): 32 heads of 4096 rows, D = 64, 16 keys 8.7 / 20.6, 77 keys
@@ -188,7 +190,7 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   int grid;
   if (workspace && cross_balanced(p.num_units, p.nkv_full, key_lengths != nullptr, sms)) {
     p.stream_k = 1;
-    p.unit_cost = unit_cost(D);
+    p.unit_cost = unit_cost(D, key_lengths != nullptr);
     grid = static_cast<int>(std::min<long long>(sms, static_cast<long long>(p.num_units) * p.nkv_full));
     const size_t slots = static_cast<size_t>(sms) * kSubTiles;
     p.ws_o = reinterpret_cast<float*>(ws);
