@@ -3,8 +3,12 @@
 // and bwd_next_segment, with the number of K/V tiles depending on the batch
 // entry's key count, which only the device knows.
 //
-// In the forward a batch entry without keys counts as one tile of masked keys: its rows then
-// run the ordinary path and come out as O = 0, LSE = +inf.
+// In the forward a batch entry without keys counts as one tile of masked
+// keys: its rows then run the ordinary path and come out as O = 0, LSE = +inf.
+//
+// The counts are read again at every step of a walk. Should they change while
+// a kernel runs (another stream writes them), a walk still ends at the last
+// batch entry and touches nothing behind the tensors.
 #pragma once
 #include "fa2_cross.h"
 #include "fa2_fwd_common.cuh"
@@ -20,7 +24,7 @@ struct CrossStart {
   long long total;    // steps of the whole call
   long long b_start;  // first step of batch entry b
   int b;              // batch entry that holds the share's first step
-  int shares;         // CTAs with a share: at most the grid, and total / the least share
+  int shares;         // CTAs with a share: min(grid, total)
 };
 
 struct CrossCursor {
@@ -39,22 +43,17 @@ __device__ __forceinline__ long long cross_share_begin(const CrossStart& st, int
   return c >= st.shares ? st.total : st.total * c / st.shares;
 }
 
-__device__ __forceinline__ int cross_shares(long long total, int least) {
-  return static_cast<int>(min(static_cast<long long>(gridDim.x), total > 0 ? max(total / least, 1ll) : 0ll));
-}
-
 // By one whole warp: the total, then the batch entry of this CTA's first step
 // (32 entries at a time: a shuffle scan of their steps). `steps(b)` are the
-// steps of batch entry b, the same for all entries when `uniform`; a share is
-// at least `least` steps.
+// steps of batch entry b, the same for all entries when `uniform`.
 template <typename F>
-__device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, int least, F&& steps) {
+__device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, F&& steps) {
   CrossStart st;
   const int lane = threadIdx.x & 31;
   if (uniform) {
     const long long per = steps(0);
     st.total = per * B;
-    st.shares = cross_shares(st.total, least);
+    st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), st.total));
     st.b = static_cast<int>(min(cross_share_begin(st, blockIdx.x) / per, static_cast<long long>(B - 1)));
     st.b_start = per * st.b;
     return st;
@@ -64,7 +63,7 @@ __device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, int 
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   st.total = sum;
-  st.shares = cross_shares(st.total, least);
+  st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), st.total));
   st.b = 0;
   st.b_start = 0;
   const long long want = cross_share_begin(st, blockIdx.x);
@@ -93,7 +92,7 @@ __device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, int 
 // The forward's start; the round schedule needs none.
 __device__ __forceinline__ CrossStart cross_fwd_start(const CrossParams& p) {
   if (!p.stream_k) return CrossStart{0, 0, 0, 0};
-  return cross_find_start(p.B, !p.key_lengths, 1, [&](int b) { return cross_batch_steps(p, b); });
+  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_batch_steps(p, b); });
 }
 
 __device__ __forceinline__ CrossCursor cross_first_cursor(const CrossParams& p, const CrossStart& st) {
@@ -132,7 +131,7 @@ __device__ __forceinline__ bool cross_next_segment(CrossCursor& c, CrossSegment&
       const long long steps = static_cast<long long>(p.heads) * p.n_qt * per_unit;
       if (c.step < c.b_start + steps) break;
       c.b_start += steps;
-      ++c.b;
+      if (++c.b >= p.B) return false;
     }
     const long long r = c.step - c.b_start;
     const long long unit = r / per_unit;
@@ -168,7 +167,7 @@ __device__ __forceinline__ long long cross_bwd_batch_steps(const CrossBwdParams&
 
 __device__ __forceinline__ CrossStart cross_bwd_start(const CrossBwdParams& p) {
   if (!p.stream_k) return CrossStart{0, 0, 0, 0};
-  return cross_find_start(p.B, !p.key_lengths, 1, [&](int b) { return cross_bwd_batch_steps(p, b); });
+  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_bwd_batch_steps(p, b); });
 }
 
 __device__ __forceinline__ CrossCursor cross_bwd_first_cursor(const CrossBwdParams& p, const CrossStart& st) {
@@ -204,7 +203,7 @@ __device__ __forceinline__ bool cross_bwd_next_segment(CrossCursor& c, CrossBwdS
     const long long steps = static_cast<long long>(p.heads) * tiles * p.nq;
     if (c.step < c.b_start + steps) break;
     c.b_start += steps;
-    ++c.b;
+    if (++c.b >= p.B) return false;
   }
   const long long r = c.step - c.b_start;
   const long long unit = r / p.nq;

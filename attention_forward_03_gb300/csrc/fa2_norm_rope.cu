@@ -729,6 +729,9 @@ View view_of(const void* p, const long long* s, int B, int H, int N, int D) {
   return View{p, static_cast<long long>(H) * N * D, static_cast<long long>(N) * D, D, B, H, N, D};
 }
 
+// A dimension reaches at most 2^44 elements, so every offset stays far inside 63 bits.
+bool reach_ok(long long stride, int size) { return stride >= 0 && (size < 2 || stride <= (1ll << 44) / (size - 1)); }
+
 int check_views(const NormRopeArgs& a, bool backward) {
   for (int i = 0; i < 2; ++i) {
     const View* vs[3] = {&a.x[i], &a.y[i], &a.g[i]};
@@ -736,9 +739,7 @@ int check_views(const NormRopeArgs& a, bool backward) {
       const View& v = *vs[j];
       if (v.empty()) continue;
       if (!v.p) return FA2_ERR_INVALID_ARG;
-      if (v.b < 0 || v.h < 0 || v.n < 0) return FA2_ERR_INVALID_ARG;
-      // every offset stays far inside 63 bits
-      if (v.b > (1ll << 40) || v.h > (1ll << 40) || v.n > (1ll << 40)) return FA2_ERR_INVALID_ARG;
+      if (!reach_ok(v.b, v.B) || !reach_ok(v.h, v.H) || !reach_ok(v.n, v.N)) return FA2_ERR_INVALID_ARG;
       if (!aligned(v)) return FA2_ERR_ALIGN;
     }
     if (!a.y[i].empty() && !no_self_overlap(a.y[i])) return FA2_ERR_INVALID_ARG;
@@ -754,20 +755,33 @@ int check_views(const NormRopeArgs& a, bool backward) {
   return FA2_OK;
 }
 
-// The outputs against the plain arrays a call reads.
+// What a call writes besides its views (the gains' gradients and the scratch
+// of the backward): address and bytes, NULL where absent.
+struct Written {
+  const void* p;
+  size_t n;
+};
+
+// Everything written against the plain arrays a call reads: the tables, the
+// positions, the gains.
 int check_arrays(const NormRopeArgs& a, const float* cos, const float* sin, const void* positions, int rot,
-                 int table_rows, int gain_f32, int positions_64, long long pb, long long pn, int N, int D) {
+                 int table_rows, int gain_f32, int positions_64, long long pb, long long pn, int N, int D,
+                 const Written (&more)[3]) {
   const size_t table = static_cast<size_t>(table_rows) * (rot / 2) * 4, gain = static_cast<size_t>(D) * (gain_f32 ? 4 : 2);
-  if (positions && (pb < 0 || pn < 0 || pb > (1ll << 40) || pn > (1ll << 40))) return FA2_ERR_INVALID_ARG;
-  const size_t at = static_cast<size_t>((a.B - 1) * pb + (N - 1) * pn + 1) * (positions_64 ? 8 : 4);
-  for (const View& y : a.y) {
-    if (y.empty()) continue;
-    const size_t n = static_cast<size_t>(y.span()) * 2;
-    if (rot && (ranges_overlap(y.p, n, cos, table) || ranges_overlap(y.p, n, sin, table))) return FA2_ERR_INVALID_ARG;
-    if (positions && ranges_overlap(y.p, n, positions, at)) return FA2_ERR_INVALID_ARG;
+  if (positions && (!reach_ok(pb, a.B) || !reach_ok(pn, N))) return FA2_ERR_INVALID_ARG;
+  const size_t at = positions ? static_cast<size_t>((a.B - 1) * pb + (N - 1) * pn + 1) * (positions_64 ? 8 : 4) : 0;
+  auto meets_an_array = [&](const void* p, size_t n) {
+    if (!p || !n) return false;
+    if (rot && (ranges_overlap(p, n, cos, table) || ranges_overlap(p, n, sin, table))) return true;
+    if (positions && ranges_overlap(p, n, positions, at)) return true;
     for (const void* w : a.gain)
-      if (w && ranges_overlap(y.p, n, w, gain)) return FA2_ERR_INVALID_ARG;
-  }
+      if (w && ranges_overlap(p, n, w, gain)) return true;
+    return false;
+  };
+  for (const View& y : a.y)
+    if (!y.empty() && meets_an_array(y.p, static_cast<size_t>(y.span()) * 2)) return FA2_ERR_INVALID_ARG;
+  for (const Written& w : more)
+    if (meets_an_array(w.p, w.n)) return FA2_ERR_INVALID_ARG;
   return FA2_OK;
 }
 
@@ -848,7 +862,7 @@ extern "C" int fa2_qk_norm_rope_fwd(const void* q, const void* k, const void* q_
   a.gain[1] = k_gain;
   const long long pb = strides ? strides[12] : N, pn = strides ? strides[13] : 1;
   if ((rc = check_views(a, false)) != FA2_OK) return rc;
-  if ((rc = check_arrays(a, cos, sin, positions, rot, table_rows, gain_f32, positions_64, pb, pn, N, D)) != FA2_OK)
+  if ((rc = check_arrays(a, cos, sin, positions, rot, table_rows, gain_f32, positions_64, pb, pn, N, D, {})) != FA2_OK)
     return rc;
   int sms = 0;
   int* status = nullptr;
@@ -902,7 +916,8 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
   a.gain[1] = k_gain;
   const long long pb = strides ? strides[18] : N, pn = strides ? strides[19] : 1;
   if ((rc = check_views(a, true)) != FA2_OK) return rc;
-  if ((rc = check_arrays(a, cos, sin, positions, rot, table_rows, gain_f32, positions_64, pb, pn, N, D)) != FA2_OK)
+  const Written more[3] = {{dq_gain, gbytes}, {dk_gain, gbytes}, {q_gain || k_gain ? workspace : nullptr, workspace_bytes}};
+  if ((rc = check_arrays(a, cos, sin, positions, rot, table_rows, gain_f32, positions_64, pb, pn, N, D, more)) != FA2_OK)
     return rc;
   const bool gains = q_gain || k_gain;
   if ((reinterpret_cast<uintptr_t>(dq_gain) | reinterpret_cast<uintptr_t>(dk_gain)) & 15u) return FA2_ERR_ALIGN;
@@ -919,10 +934,7 @@ extern "C" int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, cons
             if (w && ranges_overlap(w, gbytes, v->p, n)) return FA2_ERR_INVALID_ARG;
         }
     for (void* w : {dq_gain, dk_gain})
-      if (w && (ranges_overlap(w, gbytes, workspace, workspace_bytes) ||
-                (q_gain && ranges_overlap(w, gbytes, q_gain, gbytes)) ||
-                (k_gain && ranges_overlap(w, gbytes, k_gain, gbytes))))
-        return FA2_ERR_INVALID_ARG;
+      if (w && ranges_overlap(w, gbytes, workspace, workspace_bytes)) return FA2_ERR_INVALID_ARG;
     if (dq_gain && dk_gain && ranges_overlap(dq_gain, gbytes, dk_gain, gbytes)) return FA2_ERR_INVALID_ARG;
   }
   int sms = 0;

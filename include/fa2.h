@@ -375,7 +375,8 @@ FA2_API int fa2_bwd_sched(const void* Q, const void* K, const void* V, const voi
  *             k, q_out, k_out in turn, then batch and token of positions;
  *             NULL: every view contiguous, positions [B, N]. A head's D
  *             elements are always contiguous; strides of dimensions longer
- *             than 1 are multiples of 8 and not negative, at most 2^40.
+ *             than 1 are multiples of 8 and not negative, and no dimension
+ *             reaches further than 2^44 elements.
  * B, Hq, Hkv, N: sizes >= 0; nothing happens when there are no rows.
  * D         : 32, 64, 96, 128, 256, 512 or 1024.
  * rot       : rotated elements, a multiple of 16, 0 <= rot <= D.
@@ -456,8 +457,8 @@ FA2_API int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const v
  *             one SM. A captured call can be replayed; the replays share the
  *             workspace. (After a timeout that fa2_device_status reports, the
  *             call is captured anew.)
- * O and LSE are fully overwritten; neither overlaps an input. Asynchronous,
- * allocation-free; errors as fa2_fwd_ws.
+ * O and LSE are fully overwritten; neither overlaps an input. Tensor pointers
+ * are 16-byte aligned. Asynchronous, allocation-free; errors as fa2_fwd_ws.
  */
 FA2_API int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* key_lengths,
                           int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, int dtype, void* workspace,

@@ -93,7 +93,7 @@ def s_with(**at):
     (dict(qo=A * 5), -1),                     # q_out meets the tables
     (dict(qo=A * 3 - 1024), -1),              # q_out reaches into q_gain
     (dict(pos=A * 7 + 16), -1),               # positions inside q_out
-    (dict(strides=s_with(_0=-8)), -1), (dict(strides=s_with(_7=1 << 41)), -1), (dict(strides=s_with(_12=-1), pos=A * 9), -1),
+    (dict(strides=s_with(_0=-8)), -1), (dict(strides=s_with(_7=1 << 45)), -1), (dict(strides=s_with(_12=-1), pos=A * 9), -1),
     (dict(strides=s_with(_1=516)), -3),       # a head stride off the 16-byte grid
     (dict(strides=s_with(_7=0)), -1), (dict(strides=s_with(_8=32)), -1),  # rows of q_out overlap one another
     (dict(B=1 << 20, N=1 << 20, rows=1 << 20), -1),
@@ -140,7 +140,9 @@ def bwd(lib, **over):
     (dict(B=-1), -1), (dict(D=40), -2), (dict(dtype=7), -2), (dict(rot=40), -2), (dict(rot=96), -1),
     (dict(dqo=None), -1), (dict(dk=None), -1), (dict(dqw=None), -1), (dict(qw=None), -1), (dict(kw=None), -1),
     (dict(ws=None), -1), (dict(wsb=1280 * 64 * 4 - 4), -1), (dict(ws=A * 20 + 8), -3), (dict(dq=A * 7 + 2), -3),
-    (dict(dqw=A * 12 + 4), -3),
+    (dict(dqw=A * 12 + 4), -3), (dict(dqw=A * 5 + 64), -1), (dict(ws=A * 6), -1), (dict(ws=A * 4), -1),
+    (dict(pos=A * 20 + 64), -1), (dict(pos=A * 13), -1),
+    (dict(B=1 << 16, N=1 << 14, rows=1 << 14, strides=[1 << 40, 64, 64] * 6 + [1, 1]), -1),
     (dict(dq=A + 128), -1), (dict(dq=A * 10 + 128), -1), (dict(dq=A * 11), -1), (dict(dk=A * 7), -1),
     (dict(ws=A * 7), -1), (dict(ws=A), -1), (dict(dqw=A * 12, dkw=A * 12 + 64), -1), (dict(dqw=A * 20 + 256), -1),
     (dict(dqw=A * 3), -1), (dict(dqw=A * 7 + 64), -1), (dict(rows=4), -1),
