@@ -14,7 +14,6 @@
 #include <cstdint>
 
 #include "fa2.h"
-#include "fa2_cross.h"
 #include "fa2_launch.h"
 
 namespace fa2 {
@@ -195,19 +194,6 @@ int grid_for(long long items, int sms) {
 }
 
 }  // namespace
-
-cudaError_t bwd_row_stats(int D, bool bf, const void* O, const void* dO, const float* LSE, float* dq_acc,
-                          float* neg_lse2, float* delta, int bh, int N, int Npad, int sms, cudaStream_t s) {
-  const long long rows = static_cast<long long>(bh) * Npad;
-  const int grid = grid_for(rows * (D / 8), sms);
-  switch (D) {
-    case 32: return launch_prologue<32>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, Npad, rows, grid, s);
-    case 64: return launch_prologue<64>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, Npad, rows, grid, s);
-    case 96: return launch_prologue<96>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, Npad, rows, grid, s);
-    default: return launch_prologue<128>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, Npad, rows, grid, s);
-  }
-}
-
 }  // namespace fa2
 
 using namespace fa2;
@@ -281,7 +267,15 @@ extern "C" int fa2_bwd_sched(const void* Q, const void* K, const void* V, const 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == FA2_BF16;
 
-  cudaError_t e = bwd_row_stats(D, bf, O, dO, LSE, dq_acc, neg_lse2, delta, (int)bh, N, npad, sms, s);
+  const long long rows = bh * npad;
+  const int pgrid = grid_for(rows * (D / 8), sms);
+  cudaError_t e;
+  switch (D) {
+    case 32: e = launch_prologue<32>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
+    case 64: e = launch_prologue<64>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
+    case 96: e = launch_prologue<96>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
+    default: e = launch_prologue<128>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
+  }
   if (e != cudaSuccess) return record_cuda_error(e);
 
   BwdParams p = {};

@@ -738,6 +738,24 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         tmem_ld32x32_wait(tmem + lane_off + L::kColDQ + 32u * wg, v);
         tc_fence_before_sync();
         mbar_arrive(bar_dq_free);
+        if constexpr (kCross) {
+          if (p.dq_out) {  // the row's only contribution: out as it is, 64 bytes
+            if (32 * wg < D && pend_q0 + rr < p.N) {
+              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dq_out) +
+                                                   (static_cast<size_t>(pend_bh) * p.N + pend_q0 + rr) * D + 32 * wg);
+              const float sc = p.scale;
+#pragma unroll
+              for (int ch = 0; ch < 4; ++ch) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  w[i] = pack2(__uint_as_float(v[8 * ch + 2 * i]) * sc, __uint_as_float(v[8 * ch + 2 * i + 1]) * sc, kBf16);
+                to[ch] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            return true;
+          }
+        }
         if (drains > 0) {
           if (leader) {
             bulk_wait_read_all();
@@ -780,6 +798,24 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       for (int h = 0; h < L::kHalves; ++h) tmem_ld32x32_wait(tDQ + 32u * h, v[h]);
       tc_fence_before_sync();
       mbar_arrive(bar_dq_free);
+      if constexpr (kCross) {
+        if (p.dq_out) {
+          // as above; this thread holds element rr of each query row, so a
+          // warp's store is 64 contiguous bytes of one row
+          const float sc = p.scale;
+          uint16_t* to = static_cast<uint16_t*>(p.dq_out) + static_cast<size_t>(pend_bh) * p.N * D + rr;
+#pragma unroll
+          for (int h = 0; h < L::kHalves; ++h) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int q = pend_q0 + L::kCW * wg + 32 * h + i;
+              if (rr < D && q < p.N)
+                to[static_cast<size_t>(q) * D] = static_cast<uint16_t>(pack2(__uint_as_float(v[h][i]) * sc, 0.f, kBf16));
+            }
+          }
+          return true;
+        }
+      }
       // the staging rows must have been read by the previous step's TMAs
       if (drains > 0) {
         if (!kDqWarp && leader) {
@@ -1082,7 +1118,9 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
     // TMA reduce-add per 32 rows into the fp32 accumulator; once the copy
     // engine has read them, the rows are given back. It polls without
     // sleeping.
-    if (lane < 2) {
+    bool adds = lane < 2;
+    if constexpr (kCross) adds = adds && !p.dq_out;
+    if (adds) {
       const int w = lane;
       const uint32_t rows = sDQS + static_cast<uint32_t>(w * L::kCW * D * 4);
       uint32_t k = 0;  // steps whose rows were added

@@ -24,6 +24,10 @@ struct CrossBwdParams : BwdParams {  // N: query rows per key head; nkv: K/V til
   int B;
   int heads;
   const int* key_lengths;
+  // One K/V tile per head (Nk <= 128): a query row's dQ is complete after its
+  // only step, and goes out scaled and rounded ([B*Hkv, N, D]; NULL otherwise,
+  // then it is added into dq_acc).
+  void* dq_out;
 };
 
 // Keys of batch entry b.
@@ -69,10 +73,5 @@ cudaError_t launch_cross_short(int D, bool bf16, const CrossShortParams& p, int 
 template <int D, bool kBf16>
 cudaError_t launch_cross_bwd(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const CUtensorMap& dout,
                              const CUtensorMap& dq_acc, const CrossBwdParams& p, int grid, cudaStream_t stream);
-
-// The backward's first kernel (fa2_bwd_api.cu), for B * H heads of N rows:
-// Delta and -LSE * log2(e) of every row, and the dQ accumulator zeroed.
-cudaError_t bwd_row_stats(int D, bool bf16, const void* O, const void* dO, const float* LSE, float* dq_acc,
-                          float* neg_lse2, float* delta, int bh, int N, int Npad, int sms, cudaStream_t stream);
 
 }  // namespace fa2

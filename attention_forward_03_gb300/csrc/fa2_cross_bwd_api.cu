@@ -1,10 +1,12 @@
 // C ABI of the cross-attention backward: argument checks, the workspace
-// layout, tensor maps, the launches, and the last of its three kernels.
+// layout, tensor maps, the launches, and the kernels before and after the
+// main one (fa2_bwd_kernel.cuh).
 // Declarations and the contract: include/fa2.h.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 
 #include <algorithm>
 #include <cmath>
@@ -17,6 +19,7 @@ namespace fa2 {
 namespace {
 
 constexpr int kEndThreads = 256;
+constexpr int kStatRows = 64;   // query rows a block takes at a time (divides a step's rows)
 constexpr int kZeroRows = 128;  // dK, dV rows a block writes zeros to at a time
 
 size_t round_up_256(size_t x) { return (x + 255) / 256 * 256; }
@@ -46,37 +49,122 @@ __device__ __forceinline__ uint32_t pack_two(float lo, float hi, bool bf16) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per
-// thread; zeros for the dK and dV rows of tiles wholly behind their keys; and
-// the flags of the partial results taken back, so that a replay of a captured
-// call, which carries the same tag, does not find them set.
-template <bool kBf16>
-__global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4* __restrict__ acc, uint4* __restrict__ dq,
-                                                                    float scale, long long n8, uint4* __restrict__ dk,
-                                                                    uint4* __restrict__ dv, CrossBwdParams p, int per_row) {
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (long long i = first; i < n8; i += stride) {
-    const float4 a = acc[2 * i], b = acc[2 * i + 1];
-    dq[i] = make_uint4(pack_two(a.x * scale, a.y * scale, kBf16), pack_two(a.z * scale, a.w * scale, kBf16),
-                       pack_two(b.x * scale, b.y * scale, kBf16), pack_two(b.z * scale, b.w * scale, kBf16));
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y, bool bf16) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 f, g;
+    if (bf16) {
+      f = make_float2(__uint_as_float(a[i] << 16), __uint_as_float(a[i] & 0xffff0000u));
+      g = make_float2(__uint_as_float(b[i] << 16), __uint_as_float(b[i] & 0xffff0000u));
+    } else {
+      f = __half22float2(*reinterpret_cast<const __half2*>(&a[i]));
+      g = __half22float2(*reinterpret_cast<const __half2*>(&b[i]));
+    }
+    s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
   }
-  if (p.ws_flags && first < kBwdMaxCtas) p.ws_flags[first] = 0ull;
+  return s;
+}
+
+// Before the main kernel. Per row of the padded [B*Hkv, Npad] grid: Delta_i =
+// <dO_i, O_i> and -LSE_i * log2(e) (rows >= N: 0 and -inf, so that P is 0
+// there), and the row of the fp32 dQ accumulator zeroed, where there is one.
+// Zeros also for what no unit writes: dK and dV of tiles wholly behind their
+// keys, and without an accumulator dQ of batch entries without keys. And the
+// flags of the partial results taken back, so that a replay of a captured
+// call, which carries the same tag, does not find them set.
+// A block takes 64 rows of a head at a time, D/8 threads of 16 bytes per row
+// in groups of a power of two, all loads of a pass before its sums.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint4* __restrict__ O,
+                                                                      const uint4* __restrict__ dO,
+                                                                      const float* __restrict__ LSE, float* neg_lse2,
+                                                                      float* delta, uint4* dk, uint4* dv,
+                                                                      const CrossBwdParams p) {
+  constexpr int kPer = D / 8;
+  constexpr int kLanes = kPer <= 4 ? 4 : (kPer <= 8 ? 8 : 16);
+  constexpr int kPasses = kStatRows * kLanes / kEndThreads;
+  static_assert(kStatRows * kLanes % kEndThreads == 0, "passes");
+  const int part = threadIdx.x % kLanes;
+  const int tiles = p.Npad / kStatRows;
+  const long long items = static_cast<long long>(p.BH) * tiles;
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int bh = static_cast<int>(it / tiles);
+    const int r0 = static_cast<int>(it - static_cast<long long>(bh) * tiles) * kStatRows + threadIdx.x / kLanes;
+    const size_t head = static_cast<size_t>(bh) * p.N;
+    uint4 x[kPasses], g[kPasses];
+#pragma unroll
+    for (int s = 0; s < kPasses; ++s) {
+      const int r = r0 + s * (kEndThreads / kLanes);
+      x[s] = g[s] = z;
+      if (r < p.N && part < kPer) {
+        x[s] = O[(head + r) * kPer + part];
+        g[s] = dO[(head + r) * kPer + part];
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kPasses; ++s) {
+      const int r = r0 + s * (kEndThreads / kLanes);
+      if (p.dq_acc && r < p.N && part < kPer) {
+        uint4* to = reinterpret_cast<uint4*>(p.dq_acc) + ((head + r) * kPer + part) * 2;
+        to[0] = z;
+        to[1] = z;
+      }
+      float d = dot8(x[s], g[s], kBf16);
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off, kLanes);
+      if (part == 0) {
+        const size_t at = static_cast<size_t>(bh) * p.Npad + r;
+        delta[at] = r < p.N ? d : 0.f;
+        neg_lse2[at] = r < p.N ? -(LSE[head + r] * 1.4426950408889634f) : -CUDART_INF_F;
+      }
+    }
+  }
+  if (p.ws_flags && blockIdx.x == 0 && threadIdx.x < kBwdMaxCtas) p.ws_flags[threadIdx.x] = 0ull;
   if (!p.key_lengths) return;
   // pieces of kZeroRows rows of a head, dealt to the blocks in turn
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
   const int pieces = (p.Nk + kZeroRows - 1) / kZeroRows;
   const long long all = static_cast<long long>(p.BH) * pieces;
   for (long long i = blockIdx.x; i < all; i += gridDim.x) {
     const int h = static_cast<int>(i / pieces), piece = static_cast<int>(i - static_cast<long long>(h) * pieces);
-    const int from = (cross_keys(p, h / p.heads) + kKeys - 1) / kKeys * kKeys;
-    const int r0 = max(piece * kZeroRows, from), r1 = min((piece + 1) * kZeroRows, p.Nk);
+    const int n_keys = cross_keys(p, h / p.heads);
+    const int from = (n_keys + kKeys - 1) / kKeys * kKeys;
+    const int a = max(piece * kZeroRows, from), b = min((piece + 1) * kZeroRows, p.Nk);
     const long long base = static_cast<long long>(h) * p.Nk;
-    for (long long e = (base + r0) * per_row + threadIdx.x; e < (base + r1) * per_row; e += blockDim.x) {
+    for (long long e = (base + a) * kPer + threadIdx.x; e < (base + b) * kPer; e += blockDim.x) {
       dk[e] = z;
       dv[e] = z;
     }
+    if (p.dq_out && n_keys == 0 && piece == 0) {
+      uint4* q = static_cast<uint4*>(p.dq_out) + static_cast<size_t>(h) * p.N * kPer;
+      for (long long e = threadIdx.x; e < static_cast<long long>(p.N) * kPer; e += blockDim.x) q[e] = z;
+    }
   }
+}
+
+// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per thread.
+template <bool kBf16>
+__global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4* __restrict__ acc, uint4* __restrict__ dq,
+                                                                    float scale, long long n8) {
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8; i += stride) {
+    const float4 a = acc[2 * i], b = acc[2 * i + 1];
+    dq[i] = make_uint4(pack_two(a.x * scale, a.y * scale, kBf16), pack_two(a.z * scale, a.w * scale, kBf16),
+                       pack_two(b.x * scale, b.y * scale, kBf16), pack_two(b.z * scale, b.w * scale, kBf16));
+  }
+}
+
+template <int D>
+cudaError_t launch_prologue(bool bf, const void* O, const void* dO, const float* LSE, float* neg_lse2, float* delta,
+                            void* dK, void* dV, const CrossBwdParams& p, int sms, cudaStream_t s) {
+  const long long items = static_cast<long long>(p.BH) * (p.Npad / kStatRows);
+  const int grid = static_cast<int>(std::min<long long>(items, 8ll * sms));
+  auto kern = bf ? fa2_cross_bwd_prologue<D, true> : fa2_cross_bwd_prologue<D, false>;
+  kern<<<grid, kEndThreads, 0, s>>>(static_cast<const uint4*>(O), static_cast<const uint4*>(dO), LSE, neg_lse2, delta,
+                                    static_cast<uint4*>(dK), static_cast<uint4*>(dV), p);
+  return cudaGetLastError();
 }
 
 using CrossBwdFn = cudaError_t (*)(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
@@ -187,9 +275,6 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
       !(D <= 64 ? encode_f32_cols_map_sw128(&mdq, dq_acc, ibh, n, D, 128) : encode_f32_rows_map(&mdq, dq_acc, ibh, n, D, 32)))
     return record_cuda_error(cudaErrorInvalidValue);
   const bool bf = dtype == FA2_BF16;
-  e = bwd_row_stats(D, bf, O, dO, LSE, dq_acc, neg_lse2, delta, ibh, n, (int)npad, sms, s);
-  if (e != cudaSuccess) return record_cuda_error(e);
-
   CrossBwdParams p = {};
   p.dk = dK;
   p.dv = dV;
@@ -226,14 +311,25 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
     p.ws_flags = reinterpret_cast<unsigned long long*>(ws + wl.dq_bytes + 2 * wl.stat_bytes + wl.part_bytes);
     p.epoch = next_launch_epoch();
   }
+  if (Nk <= kBwdKeys) {
+    p.dq_out = dQ;
+    p.dq_acc = nullptr;
+  }
+  switch (D) {
+    case 32: e = launch_prologue<32>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    case 64: e = launch_prologue<64>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    case 96: e = launch_prologue<96>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    default: e = launch_prologue<128>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+  }
+  if (e != cudaSuccess) return record_cuda_error(e);
   e = pick_cross_bwd(D, bf)(mk, mv, mq, mdo, mdq, p, grid, s);
   if (e != cudaSuccess) return record_cuda_error(e);
 
+  if (p.dq_out) return FA2_OK;
   const long long n8 = bh * rows * (D / 8);
   const int blocks = static_cast<int>(std::max<long long>(1, std::min<long long>((n8 + kEndThreads - 1) / kEndThreads, 8ll * sms)));
   auto finish = bf ? fa2_cross_bwd_finish<true> : fa2_cross_bwd_finish<false>;
-  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), scale, n8,
-                                        static_cast<uint4*>(dK), static_cast<uint4*>(dV), p, D / 8);
+  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), scale, n8);
   e = cudaGetLastError();
   return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
 }

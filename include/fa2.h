@@ -490,8 +490,9 @@ FA2_API int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes);
  *             shared by calls that run at the same time. May be NULL where
  *             there is no query or no key (every gradient is zero then).
  * Every gradient is fully overwritten, rounded to nearest-even, and overlaps
- * nothing. dQ is summed with fp32 atomic adds in no fixed order; dK and dV
- * are summed in a fixed one. The other arguments and the errors are
+ * nothing. dQ is summed with fp32 atomic adds in no fixed order (up to Nk =
+ * 128 there is one term per row and no sum); dK and dV are summed in a fixed
+ * one. The other arguments and the errors are
  * fa2_cross_fwd's, with FA2_ERR_INVALID_ARG for a missing workspace.
  */
 FA2_API int fa2_cross_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,

@@ -110,6 +110,8 @@ def test_backward(c):
     check_bwd(grads, q, k, v, o, lse, do, scale, n)
     again = ops().cross_attention_backward(q, k, v, o, lse, do, key_lengths=n)
     assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])  # dK, dV: a fixed order
+    if c[4] <= 128:
+        assert torch.equal(grads[0], again[0])  # dQ: one term per row
 
 
 def test_gradient_against_differences_of_the_forward():
@@ -151,18 +153,20 @@ def test_backward_of_nothing(shape):
         assert a.shape == b.shape and bool((a == 0).all())
 
 
-@pytest.mark.parametrize("lengths", [[0, 0], [0, 200]])
-def test_backward_with_empty_batch_entries(lengths):
-    q, k, v, n = inputs(2, 4, 2, 70, 200, 64, BF16, lengths)
+@pytest.mark.parametrize("lengths,Nk,D", [([0, 0], 200, 64), ([0, 200], 200, 64), ([0, 0], 100, 64), ([0, 100], 100, 64),
+                                          ([33, 0], 128, 128), ([0, 5], 90, 96)])
+def test_backward_with_empty_batch_entries(lengths, Nk, D):
+    q, k, v, n = inputs(2, 4, 2, 70, Nk, D, BF16, lengths)
     o, lse = ops().cross_attention_forward(q, k, v, key_lengths=n)
     do = upstream(q)
     outs = [torch.full_like(t, float("nan")) for t in (q, k, v)]
     ops().cross_attention_backward(q, k, v, o, lse, do, key_lengths=n, dq=outs[0], dk=outs[1], dv=outs[2])
-    check_bwd(outs, q, k, v, o, lse, do, 0.125, n)
-    assert bool((outs[0][0] == 0).all())
+    check_bwd(outs, q, k, v, o, lse, do, D ** -0.5, n)
+    assert all(bool((outs[0][b] == 0).all()) for b in range(2) if lengths[b] == 0)
 
 
-@pytest.mark.parametrize("c", [(2, 4, 2, 260, 700, 128, BF16, [700, 310]), (2, 2, 2, 300, 900, 64, F16, [333, 900])], ids=str)
+@pytest.mark.parametrize("c", [(2, 4, 2, 260, 700, 128, BF16, [700, 310]), (2, 2, 2, 300, 900, 64, F16, [333, 900]),
+                               (2, 2, 2, 5000, 100, 64, F16, [100, 90]), (1, 2, 2, 4000, 128, 128, BF16, [128])], ids=str)
 def test_backward_captured_and_replayed_on_new_inputs(c):
     q, k, v, n = inputs(*c, garbage=0.0)
     do = upstream(q)
@@ -175,7 +179,7 @@ def test_backward_captured_and_replayed_on_new_inputs(c):
         q2, k2, v2, _ = inputs(*c[:-1], seed=seed)
         for a, b in ((q, q2), (k, k2), (v, v2)):
             a.copy_(b)
-        n.copy_(torch.tensor([max(0, int(x) - 150 * (seed - 4)) for x in c[-1]], dtype=torch.int32))
+        n.copy_(torch.tensor([max(0, int(x) - c[4] // 5 * (seed - 4)) for x in c[-1]], dtype=torch.int32))
         for _ in range(3):
             graph.replay()
         torch.cuda.synchronize()
