@@ -35,16 +35,46 @@ CrossFn pick_cross(int d, bool bf) {
   }
 }
 
-// Whether equal shares of all K/V-tile steps (and a merge of the units they
-// cut) beat whole units in rounds. The cost of each in steps of the busiest
-// SM, as in fwd_auto_schedule; with key counts on the device the units differ
-// by an amount the host cannot know, and the shares follow it.
-bool cross_balanced(long long units, long long nkv, bool lengths, int sms) {
-  constexpr double kSplitCostSteps = 4.0;
-  if (lengths) return true;
-  const double rounds = static_cast<double>((units + sms - 1) / sms) * static_cast<double>(nkv);
-  const double balanced = static_cast<double>(units) * static_cast<double>(nkv) / sms + kSplitCostSteps;
-  return balanced < 0.95 * rounds;
+// How many CTAs share the K/V-tile steps equally, with a merge of the units
+// that they cut, or 0 for whole units in rounds. The cost of each in steps of
+// the busiest SM.
+//
+// At least one unit per SM: as in fwd_auto_schedule; with key counts on the
+// device the units differ by an amount the host cannot know, and the shares
+// follow it.
+//
+// Fewer units than SMs: the first holder of a unit joins the other holders'
+// results one after another, so more CTAs are not always faster. A join takes
+// about 0.6 steps, 1.25 with the wider O above D = 64, cutting units at all
+// five to six (the flags, the way through memory). Tried are
+// whole parts per unit, whose cuts meet the units' ends, and all SMs, where a
+// unit has up to one holder more. Measured (us, by the parts per unit; 1: not
+// cut, * the choice): 8 heads of 128 rows, D = 64: 500 keys 1* 9.1, 2 10.7;
+// 1508 keys 1 17.2, 2 17.4, 4* 14.3, 12 19.5; 4068 keys 1 36.7, 4 19.8, 6
+// 18.4, 8* 20.0, 19 23.4; 16,356 keys 1 131, 8 32.2, 12 30.6, 16* 28.4, 19 29.8.
+// D = 128: 500 keys 1* 10.8, 2 12.3; 1508 keys 1* 18.6, 3 19.7, 4 16.9, 12
+// 28.2; 4068 keys 1 37.9, 4* 22.8, 8 25.3, 19 34.5. 64 heads of 256 rows,
+// 1508 keys: D = 64 1* 21.0, 2 22.5; D = 128 1* 24.9, 2 28.5.
+int cross_share_ctas(int D, long long units, long long nkv, bool lengths, int sms) {
+  if (units >= sms) {
+    constexpr double kSplitCostSteps = 4.0;
+    const double rounds = static_cast<double>((units + sms - 1) / sms) * static_cast<double>(nkv);
+    const double balanced = static_cast<double>(units) * static_cast<double>(nkv) / sms + kSplitCostSteps;
+    return lengths || balanced < 0.95 * rounds ? sms : 0;
+  }
+  const double cut = D <= 64 ? 5.8 : 5.0, join = D <= 64 ? 0.6 : 1.25;
+  double best = 0.95 * static_cast<double>(nkv);
+  int ctas = 0;
+  const auto consider = [&](long long n, long long joins) {
+    const double cost = static_cast<double>((units * nkv + n - 1) / n) + cut + join * static_cast<double>(joins);
+    if (cost < best) {
+      best = cost;
+      ctas = static_cast<int>(n);
+    }
+  };
+  for (long long parts = 2; parts <= nkv && parts * units <= sms; ++parts) consider(parts * units, parts - 1);
+  if (units * nkv > sms) consider(sms, (sms + units - 1) / units);
+  return ctas;
 }
 
 // What a unit counts in the equal shares besides its tiles: the tensor cores
@@ -187,11 +217,10 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   p.n_qt = (int)n_qt;
   p.num_units = (int)(bh * n_qt);
   p.nkv_full = (Nk + kKeys - 1) / kKeys;
-  int grid;
-  if (workspace && cross_balanced(p.num_units, p.nkv_full, key_lengths != nullptr, sms)) {
+  int grid = workspace ? cross_share_ctas(D, p.num_units, p.nkv_full, key_lengths != nullptr, sms) : 0;
+  if (grid > 0) {
     p.stream_k = 1;
     p.unit_cost = unit_cost(D, key_lengths != nullptr);
-    grid = static_cast<int>(std::min<long long>(sms, static_cast<long long>(p.num_units) * p.nkv_full));
     const size_t slots = static_cast<size_t>(sms) * kSubTiles;
     p.ws_o = reinterpret_cast<float*>(ws);
     p.ws_stats = p.ws_o + slots * D * 128;

@@ -784,11 +784,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (last_c + 1 < static_cast<int>(gridDim.x) && stream_k_begin(p, last_c + 1) < w.unit_end) ++last_c;
         }
         bool fine = true;
-        for (int cb = first_c; cb <= last_c && fine; ++cb)
-          fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSitePartialFlag);
+        if constexpr (kCross) {
+          // one flag per lane: a cut unit can have dozens of holders
+          for (int cb = first_c + (rr & 31); cb <= last_c && fine; cb += 32)
+            fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSitePartialFlag);
+        } else {
+          for (int cb = first_c; cb <= last_c && fine; ++cb)
+            fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSitePartialFlag);
+        }
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
         if constexpr (kCross) {
+          __syncwarp();  // what one lane acquired is visible to all
           // Every thread of the warpgroup has seen the flags: take them back,
           // so that a replay of a captured launch, which carries the same
           // tag, does not find them set before its partials are written.
@@ -797,8 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool seen = wait_bounded(bar_part0 + 8 * t, part_phase, wd, kSitePartialFlag);
             seen = __all_sync(0xffffffffu, seen);
             if (!seen) break;
-            if (rr == 0)
-              for (int cb = first_c; cb <= last_c; ++cb) p.ws_flags[static_cast<size_t>(cb) * 2 + t] = 0ull;
+            for (int cb = first_c + rr; cb <= last_c; cb += 32) p.ws_flags[static_cast<size_t>(cb) * 2 + t] = 0ull;
           }
           part_phase ^= 1u;
         }

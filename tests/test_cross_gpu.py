@@ -272,6 +272,31 @@ def test_captured_and_replayed_on_new_inputs(c):
         check_fwd(o, lse, q, k, v, c[5] ** -0.5, n)
 
 
+CUT = [  # fewer heads than SMs, keys long enough to cut each head's unit between several
+    (1, 32, 8, 8, 1700, 64, BF16, None),
+    (1, 8, 8, 150, 4500, 32, F16, None),
+    (2, 8, 4, 150, 4500, 128, BF16, [4500, 0]),
+    (4, 2, 2, 300, 2300, 96, F16, [1, 2300, 129, 1024]),
+    (1, 1, 1, 40, 30000, 64, F16, [29999]),
+    (1, 1, 1, 257, 30000, 128, BF16, None),
+]
+
+
+@pytest.mark.parametrize("c", CUT, ids=str)
+def test_units_cut_between_many_sms(c):
+    q, k, v, n = inputs(*c)
+    o, lse = ops().cross_attention_forward(q, k, v, key_lengths=n)
+    check_fwd(o, lse, q, k, v, c[5] ** -0.5, n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go, glse = ops().cross_attention_forward(q, k, v, key_lengths=n)
+    for _ in range(5):  # over the workspace and the flags that the replay before left
+        go.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(go, o) and torch.equal(glse, lse)
+
+
 def test_two_streams_at_once():
     cs = [(2, 8, 2, 1, 6000, 128, BF16, [6000, 2000]), (1, 4, 4, 400, 6000, 64, F16, [5001])]
     sets = [inputs(*c) for c in cs]

@@ -47,3 +47,23 @@ def test_a_withheld_tile_times_out(fa2, Nq, D):
             check_cross_fwd(*got, q, k, v, D ** -0.5, n)
         else:
             check_cross_bwd(got, q, k, v, o, lse, q, D ** -0.5, n)
+
+
+def test_a_withheld_tile_of_a_cut_unit_times_out(fa2):
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(1, 2, n, 64, generator=g).bfloat16().cuda() for n in (300, 6000, 6000))
+    fa2.cross_attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    try:
+        fa2.fa2_set_watchdog_ns(20_000_000)  # 20 ms
+        assert fa2.library().fa2_test_withhold_next_load(1) == fa2.FA2_OK
+        fa2.cross_attention_forward(q, k, v)
+        torch.cuda.synchronize()  # the holders of the units' first tiles give up waiting for the others, too
+        assert fa2.fa2_device_status(clear=True) > 0
+    finally:
+        fa2.library().fa2_test_withhold_next_load(0)
+        fa2.fa2_set_watchdog_ns(0)
+    o, lse = fa2.cross_attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    assert fa2.fa2_device_status(clear=True) == 0
+    check_cross_fwd(o, lse, q, k, v, 0.125, None)
