@@ -1050,8 +1050,15 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           while (last_c + 1 < static_cast<int>(gridDim.x) && bwd_share_begin(p, last_c + 1) < sg.unit_end) ++last_c;
         }
         bool fine = true;
-        for (int cb = blockIdx.x + 1; cb <= last_c && fine; ++cb)
-          fine = wait_flag(p.ws_flags + cb, p.epoch, wd, kSiteBwdPartFlag);
+        if constexpr (kCross) {
+          // one flag per lane: a cut unit can have dozens of holders
+          for (int cb = blockIdx.x + 1 + lane; cb <= last_c && fine; cb += 32)
+            fine = wait_flag(p.ws_flags + cb, p.epoch, wd, kSiteBwdPartFlag);
+          __syncwarp();  // what one lane acquired is visible to all
+        } else {
+          for (int cb = blockIdx.x + 1; cb <= last_c && fine; ++cb)
+            fine = wait_flag(p.ws_flags + cb, p.epoch, wd, kSiteBwdPartFlag);
+        }
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) {
           ok = false;

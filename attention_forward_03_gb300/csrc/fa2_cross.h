@@ -36,6 +36,27 @@ __device__ __forceinline__ int cross_keys(const P& p, int b) {
   return p.key_lengths ? min(max(__ldg(p.key_lengths + b), 0), p.Nk) : p.Nk;
 }
 
+// Fewer units than SMs: how many CTAs share their steps equally, or 0 for
+// whole units, by the cost in steps of the busiest SM. The first holder of a
+// unit joins the other holders' results one after another, so more CTAs are
+// not always faster: a join takes `join` steps, cutting units at all `cut`.
+// Tried are whole parts per unit, whose cuts meet the units' ends, and all
+// SMs, where a unit has up to one holder more.
+inline int cross_cut_ctas(long long units, long long unit_steps, int sms, double cut, double join) {
+  double best = 0.95 * static_cast<double>(unit_steps);
+  int ctas = 0;
+  const auto consider = [&](long long n, long long joins) {
+    const double cost = static_cast<double>((units * unit_steps + n - 1) / n) + cut + join * static_cast<double>(joins);
+    if (cost < best) {
+      best = cost;
+      ctas = static_cast<int>(n);
+    }
+  };
+  for (long long parts = 2; parts <= unit_steps && parts * units <= sms; ++parts) consider(parts * units, parts - 1);
+  if (units * unit_steps > sms) consider(sms, (sms + units - 1) / units);
+  return ctas;
+}
+
 // The forward on the tensor-core kernel of fa2_kernel.cuh.
 template <int D, bool kBf16>
 cudaError_t launch_cross_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,

@@ -43,12 +43,9 @@ CrossFn pick_cross(int d, bool bf) {
 // device the units differ by an amount the host cannot know, and the shares
 // follow it.
 //
-// Fewer units than SMs: the first holder of a unit joins the other holders'
-// results one after another, so more CTAs are not always faster. A join takes
-// about 0.6 steps, 1.25 with the wider O above D = 64, cutting units at all
-// five to six (the flags, the way through memory). Tried are
-// whole parts per unit, whose cuts meet the units' ends, and all SMs, where a
-// unit has up to one holder more. Measured (us, by the parts per unit; 1: not
+// Fewer units than SMs: cross_cut_ctas, a join at about 0.6 steps, 1.25 with
+// the wider O above D = 64, cutting at all five to six (the flags, the way
+// through memory). Measured (us, by the parts per unit; 1: not
 // cut, * the choice): 8 heads of 128 rows, D = 64: 500 keys 1* 9.1, 2 10.7;
 // 1508 keys 1 17.2, 2 17.4, 4* 14.3, 12 19.5; 4068 keys 1 36.7, 4 19.8, 6
 // 18.4, 8* 20.0, 19 23.4; 16,356 keys 1 131, 8 32.2, 12 30.6, 16* 28.4, 19 29.8.
@@ -62,19 +59,7 @@ int cross_share_ctas(int D, long long units, long long nkv, bool lengths, int sm
     const double balanced = static_cast<double>(units) * static_cast<double>(nkv) / sms + kSplitCostSteps;
     return lengths || balanced < 0.95 * rounds ? sms : 0;
   }
-  const double cut = D <= 64 ? 5.8 : 5.0, join = D <= 64 ? 0.6 : 1.25;
-  double best = 0.95 * static_cast<double>(nkv);
-  int ctas = 0;
-  const auto consider = [&](long long n, long long joins) {
-    const double cost = static_cast<double>((units * nkv + n - 1) / n) + cut + join * static_cast<double>(joins);
-    if (cost < best) {
-      best = cost;
-      ctas = static_cast<int>(n);
-    }
-  };
-  for (long long parts = 2; parts <= nkv && parts * units <= sms; ++parts) consider(parts * units, parts - 1);
-  if (units * nkv > sms) consider(sms, (sms + units - 1) / units);
-  return ctas;
+  return D <= 64 ? cross_cut_ctas(units, nkv, sms, 5.8, 0.6) : cross_cut_ctas(units, nkv, sms, 5.0, 1.25);
 }
 
 // What a unit counts in the equal shares besides its tiles: the tensor cores

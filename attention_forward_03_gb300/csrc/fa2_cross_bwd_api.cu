@@ -179,8 +179,27 @@ CrossBwdFn pick_cross_bwd(int d, bool bf) {
   }
 }
 
-// Partial-result write and merge of a cut unit, in query steps.
-constexpr long long kCrossBwdSplitCostSteps = 2;
+// How many CTAs share all query steps equally, with a merge of the units that
+// they cut, or 0 for whole units in rounds.
+//
+// At least one unit per SM: when that saves the busiest SM at least 5 %, with
+// 2 steps for a cut unit's partial results, and always with key counts on the
+// device, which the shares follow.
+//
+// Fewer: cross_cut_ctas. Measured (us, by the parts per unit; 1: not cut, *
+// the choice): 8 heads over 77 keys, D = 64: 256 rows 1* 10.7, 2 12.7; 1024
+// rows 1 21.3, 4* 16.3, 12 18.7; 4096 rows 1 62.5, 8* 24.5, 19 26.9; 16,384
+// rows 1 231, 8 51.7, 16* 41.8, 19 42.8. D = 128: 256 rows 1* 14.8, 4 18.9;
+// 1024 rows 1 29.8, 4* 22.7, 12 33.3; 4096 rows 1 93.3, 6 38.1, 8* 37.6, 19
+// 43.4; 16,384 rows 1 348, 12 74.7, 19 70.1.
+int cross_bwd_share_ctas(int D, long long units, long long nq, bool lengths, int sms) {
+  if (units >= sms) {
+    constexpr long long kSplitCostSteps = 2;
+    const long long rounds = (units + sms - 1) / sms * nq;
+    return lengths || 100 * ((units * nq + sms - 1) / sms + kSplitCostSteps) < 95 * rounds ? sms : 0;
+  }
+  return D <= 64 ? cross_cut_ctas(units, nq, sms, 1.5, 0.6) : cross_cut_ctas(units, nq, sms, 2.3, 1.0);
+}
 
 }  // namespace
 }  // namespace fa2
@@ -296,17 +315,11 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
   p.heads = Hkv;
   p.key_lengths = key_lengths;
   p.test_withhold = take_test_withhold();
-  // Equal shares of all query steps when that saves the busiest SM at least
-  // 5 %, and always with key counts on the device, which the shares follow.
-  const long long steps = static_cast<long long>(p.num_units) * p.nq;
-  const int round_grid = std::min(p.num_units, sms);
-  const int sk_grid = static_cast<int>(std::min<long long>(std::min(sms, kBwdMaxCtas), steps));
-  const long long rounds = (p.num_units + round_grid - 1) / round_grid * static_cast<long long>(p.nq);
-  const long long split = (steps + sk_grid - 1) / sk_grid + kCrossBwdSplitCostSteps;
-  int grid = round_grid;
-  if (key_lengths || 100 * split < 95 * rounds) {
+  const int shares = cross_bwd_share_ctas(D, p.num_units, p.nq, key_lengths != nullptr, std::min(sms, kBwdMaxCtas));
+  int grid = std::min(p.num_units, sms);
+  if (shares > 0) {
     p.stream_k = 1;
-    grid = sk_grid;
+    grid = shares;
     p.ws_part = reinterpret_cast<float*>(ws + wl.dq_bytes + 2 * wl.stat_bytes);
     p.ws_flags = reinterpret_cast<unsigned long long*>(ws + wl.dq_bytes + 2 * wl.stat_bytes + wl.part_bytes);
     p.epoch = next_launch_epoch();
