@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
     }
   }
   auto first_segment_cursor = [&]() {
-    if constexpr (kCross) return cross_bwd_first_cursor(p, *start);
+    if constexpr (kCross) return cross_first_cursor(p, *start);
     else return bwd_first_cursor(p);
   };
   auto advance = [&](auto& c, Seg& s) -> bool {

@@ -25,12 +25,20 @@ struct CrossStart {
   long long b_start;  // first step of batch entry b
   int b;              // batch entry that holds the share's first step
   int shares;         // CTAs with a share: min(grid, total)
+  int head, tile;     // the unit with the first step: key head, query tile (forward) or K/V tile (backward)
+  int from;           // steps of that unit before it
 };
 
+// Where a walk stands. It steps from unit to unit without a division and reads
+// a batch entry's key count once: every role of a CTA repeats it for every
+// unit, and of the few microseconds that a unit of 3 tiles takes, fetching the
+// instructions of 64-bit divisions was a part (FIGURES).
 struct CrossCursor {
   int round;
-  int b;
-  long long step, end, b_start;
+  int b, head, tile;
+  int from;    // steps of the unit already walked (by this CTA or those before it)
+  int n_keys;  // of batch entry b
+  long long step, end;
 };
 
 __device__ __forceinline__ int cross_tiles(int n_keys) { return max(1, (n_keys + kKeys - 1) / kKeys); }
@@ -91,18 +99,41 @@ __device__ __forceinline__ CrossStart cross_find_start(int B, bool uniform, F&& 
 
 // The forward's start; the round schedule needs none.
 __device__ __forceinline__ CrossStart cross_fwd_start(const CrossParams& p) {
-  if (!p.stream_k) return CrossStart{0, 0, 0, 0};
-  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_batch_steps(p, b); });
+  if (!p.stream_k) return CrossStart{};
+  CrossStart st = cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_batch_steps(p, b); });
+  const int per_unit = cross_tiles(cross_keys(p, st.b)) + p.unit_cost;
+  const long long r = cross_share_begin(st, blockIdx.x) - st.b_start;
+  const long long unit = r / per_unit;
+  st.from = static_cast<int>(r % per_unit);
+  st.head = static_cast<int>(min(unit / p.n_qt, p.heads - 1ll));  // (should the counts have changed meanwhile)
+  st.tile = static_cast<int>(unit % p.n_qt);
+  return st;
 }
 
-__device__ __forceinline__ CrossCursor cross_first_cursor(const CrossParams& p, const CrossStart& st) {
+template <typename P>
+__device__ __forceinline__ CrossCursor cross_first_cursor(const P& p, const CrossStart& st) {
   CrossCursor c;
   c.round = 0;
   c.b = st.b;
-  c.b_start = st.b_start;
+  c.head = st.head;
+  c.tile = st.tile;
+  c.from = st.from;
+  c.n_keys = cross_keys(p, st.b);
   c.step = p.stream_k ? cross_share_begin(st, blockIdx.x) : 0;
   c.end = p.stream_k ? cross_share_begin(st, blockIdx.x + 1) : 0;
   return c;
+}
+
+// To the next unit; a key head has `tiles` of them. Past the last one the walk ends.
+template <typename P>
+__device__ __forceinline__ void cross_next_unit(CrossCursor& c, int tiles, const P& p) {
+  c.from = 0;
+  if (++c.tile < tiles) return;
+  c.tile = 0;
+  if (++c.head < p.heads) return;
+  c.head = 0;
+  if (++c.b < p.B) c.n_keys = cross_keys(p, c.b);
+  else c.step = c.end;
 }
 
 // Next segment of this CTA. Every role walks the same sequence.
@@ -112,7 +143,7 @@ __device__ __forceinline__ bool cross_next_segment(CrossCursor& c, CrossSegment&
     if (u >= p.num_units || u < 0) return false;
     s.bh = u / p.n_qt;
     s.q0 = (u - s.bh * p.n_qt) * kSubTiles * kRows;
-    s.n_keys = cross_keys(p, s.bh / p.heads);
+    s.n_keys = p.key_lengths ? cross_keys(p, s.bh / p.heads) : p.Nk;
     s.nkv = cross_tiles(s.n_keys);
     s.kv_begin = 0;
     s.kv_end = s.nkv;
@@ -123,28 +154,18 @@ __device__ __forceinline__ bool cross_next_segment(CrossCursor& c, CrossSegment&
   // tiles. A share that ends among the first has no tile of the unit; the next
   // share then holds all of them.
   while (c.step < c.end) {
-    long long per_unit;
-    for (;;) {
-      s.n_keys = cross_keys(p, c.b);
-      s.nkv = cross_tiles(s.n_keys);
-      per_unit = s.nkv + p.unit_cost;
-      const long long steps = static_cast<long long>(p.heads) * p.n_qt * per_unit;
-      if (c.step < c.b_start + steps) break;
-      c.b_start += steps;
-      if (++c.b >= p.B) return false;
-    }
-    const long long r = c.step - c.b_start;
-    const long long unit = r / per_unit;
-    const long long from = r - unit * per_unit, to = min(per_unit, from + (c.end - c.step));
+    s.n_keys = c.n_keys;
+    s.nkv = cross_tiles(c.n_keys);
+    s.bh = c.b * p.heads + c.head;
+    s.q0 = c.tile * kSubTiles * kRows;
+    const int per_unit = s.nkv + p.unit_cost, from = min(c.from, per_unit);
+    const int to = static_cast<int>(min(static_cast<long long>(per_unit), from + (c.end - c.step)));
     s.unit_end = c.step - from + per_unit;
+    s.kv_begin = max(from - p.unit_cost, 0);
+    s.kv_end = max(to - p.unit_cost, 0);
     c.step += to - from;
-    s.kv_begin = static_cast<int>(max(from - p.unit_cost, 0ll));
-    s.kv_end = static_cast<int>(max(to - p.unit_cost, 0ll));
-    if (s.kv_end <= s.kv_begin) continue;
-    const int head = static_cast<int>(unit / p.n_qt);
-    s.bh = c.b * p.heads + head;
-    s.q0 = static_cast<int>(unit - static_cast<long long>(head) * p.n_qt) * kSubTiles * kRows;
-    return true;
+    cross_next_unit(c, p.n_qt, p);  // a unit that the share's end cuts is its last
+    if (s.kv_end > s.kv_begin) return true;
   }
   return false;
 }
@@ -166,18 +187,15 @@ __device__ __forceinline__ long long cross_bwd_batch_steps(const CrossBwdParams&
 }
 
 __device__ __forceinline__ CrossStart cross_bwd_start(const CrossBwdParams& p) {
-  if (!p.stream_k) return CrossStart{0, 0, 0, 0};
-  return cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_bwd_batch_steps(p, b); });
-}
-
-__device__ __forceinline__ CrossCursor cross_bwd_first_cursor(const CrossBwdParams& p, const CrossStart& st) {
-  CrossCursor c;
-  c.round = 0;
-  c.b = st.b;
-  c.b_start = st.b_start;
-  c.step = p.stream_k ? cross_share_begin(st, blockIdx.x) : 0;
-  c.end = p.stream_k ? cross_share_begin(st, blockIdx.x + 1) : 0;
-  return c;
+  if (!p.stream_k) return CrossStart{};
+  CrossStart st = cross_find_start(p.B, !p.key_lengths, [&](int b) { return cross_bwd_batch_steps(p, b); });
+  const int tiles = max(cross_bwd_tiles(cross_keys(p, st.b)), 1);  // 0: no batch entry has keys
+  const long long r = cross_share_begin(st, blockIdx.x) - st.b_start;
+  const long long unit = r / p.nq;
+  st.from = static_cast<int>(r % p.nq);
+  st.head = static_cast<int>(min(unit / tiles, p.heads - 1ll));
+  st.tile = static_cast<int>(unit % tiles);
+  return st;
 }
 
 __device__ __forceinline__ bool cross_bwd_next_segment(CrossCursor& c, CrossBwdSegment& s, const CrossBwdParams& p) {
@@ -195,26 +213,20 @@ __device__ __forceinline__ bool cross_bwd_next_segment(CrossCursor& c, CrossBwdS
     s.unit_end = 0;
     return true;
   }
-  if (c.step >= c.end) return false;
-  int tiles;
-  for (;;) {
-    s.n_keys = cross_keys(p, c.b);
-    tiles = cross_bwd_tiles(s.n_keys);
-    const long long steps = static_cast<long long>(p.heads) * tiles * p.nq;
-    if (c.step < c.b_start + steps) break;
-    c.b_start += steps;
-    if (++c.b >= p.B) return false;
+  while (c.step < c.end) {
+    const int tiles = cross_bwd_tiles(c.n_keys);
+    s.n_keys = c.n_keys;
+    s.bh = c.b * p.heads + c.head;
+    s.kv = c.tile;
+    s.i_begin = c.from;
+    s.i_end = static_cast<int>(min(static_cast<long long>(p.nq), c.from + (c.end - c.step)));
+    s.unit_end = c.step - c.from + p.nq;
+    const bool any = c.tile < tiles;  // not in a batch entry without keys
+    if (any) c.step += s.i_end - s.i_begin;
+    cross_next_unit(c, tiles, p);
+    if (any) return true;
   }
-  const long long r = c.step - c.b_start;
-  const long long unit = r / p.nq;
-  const int head = static_cast<int>(unit / tiles);
-  s.bh = c.b * p.heads + head;
-  s.kv = static_cast<int>(unit - static_cast<long long>(head) * tiles);
-  s.i_begin = static_cast<int>(r - unit * p.nq);
-  s.i_end = static_cast<int>(min(static_cast<long long>(p.nq), s.i_begin + (c.end - c.step)));
-  s.unit_end = c.step - s.i_begin + p.nq;
-  c.step += s.i_end - s.i_begin;
-  return true;
+  return false;
 }
 
 // A K or V tile's rows [valid, 16-row boundary) in shared memory, zeroed by

@@ -17,6 +17,7 @@ struct CrossParams : Params {  // N: query rows per key head; BH: B * Hkv
   int heads;                   // Hkv
   const int* key_lengths;      // [B] keys of each batch entry (clamped to [0, Nk]), or NULL: Nk
   int unit_cost;               // what a unit counts in the equal shares besides its tiles
+  int key_split;               // a unit's sub-tiles are its keys' (D <= 64, N <= 128)
 };
 
 struct CrossBwdParams : BwdParams {  // N: query rows per key head; nkv: K/V tiles of Nk keys

@@ -202,6 +202,7 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   p.n_qt = (int)n_qt;
   p.num_units = (int)(bh * n_qt);
   p.nkv_full = (Nk + kKeys - 1) / kKeys;
+  p.key_split = D <= 64 && rows <= kRows && p.nkv_full >= 1;
   int grid = workspace ? cross_share_ctas(D, p.num_units, p.nkv_full, key_lengths != nullptr, sms) : 0;
   if (grid > 0) {
     p.stream_k = 1;

@@ -92,7 +92,9 @@ struct Layout {
   static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
   static constexpr int kCrossStartOffset = kMiscOffset + 16;   // cross attention: CrossStart
   static constexpr int kSmemBytes = kMiscOffset + 16 + 1024;  // + slack for 1 KB alignment
-  static constexpr int kCrossSmemBytes = kSmemBytes + sizeof(CrossStart);
+  // key split: sub-tile 1's base, l and l_o per row, [3][128] floats
+  static constexpr int kSplitOffset = kCrossStartOffset + (static_cast<int>(sizeof(CrossStart)) + 15) / 16 * 16;
+  static constexpr int kCrossSmemBytes = kSplitOffset + (kPanels == 1 ? 3 * kRows * 4 : 0) + 1024;
   static constexpr uint32_t kColO = 2 * kKeys;                 // O0 at 256, O1 at 256 + kDp
   static constexpr uint32_t kColP = kColO + 2 * kDp;            // kDp = 64: P0 at 384, P1 at 448
   static_assert(kColO + 2 * kDp + (kPInTmem ? 2 * kKeys / 2 : 0) <= kTmemCols, "TMEM budget");
@@ -116,19 +118,34 @@ __device__ __forceinline__ int sub0_end(const Segment& w) {
 // a batch entry have as many K/V tiles as it has keys), the key limit, rows
 // of V behind the keys zeroed and their products skipped, and a second
 // sub-tile wholly past the query rows left out.
-template <int D, bool kBf16, bool kCausal, bool kCross = false>
+//
+// kKeySplit: cross attention of at most 128 query rows per key head. Both
+// sub-tiles have the same rows, and take the segment's K/V tiles in turn
+// (sub-tile t every second from kv_begin + t), so that the two softmax
+// warpgroups and the tensor core still overlap; one sub-tile alone runs its
+// chain of products and softmax without any (about 1 us per tile). At the
+// segment's end sub-tile 0 adds sub-tile 1's O to its own, straight from
+// tensor memory (the same lanes), with both brought to the larger exponent
+// base; base, l and l_o pass through shared memory. SPLIT_FIGURES
+template <int D, bool kBf16, bool kCausal, bool kCross = false, bool kKeySplit = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fa2_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                    const std::conditional_t<kCross, CrossParams, Params> p) {
   static_assert(!(kCross && kCausal), "cross attention has no causal mask");
+  static_assert(kCross || !kKeySplit, "only cross attention has units of one sub-tile alone");
+  static_assert(!kKeySplit || D <= 64, "O waits in the P buffer above");
   using L = Layout<D>;
+  constexpr int kQTiles = kKeySplit ? 1 : kSubTiles;  // query tiles of a unit
   using Seg = std::conditional_t<kCross, CrossSegment, Segment>;
   // MMA issuers split by instruction type (one thread for every S, one for
   // every P.V) or by sub-tile (each thread S and P.V of one sub-tile). Both
   // measured (with the issuers sleeping between polls): by type is 10-15 %
-  // faster at head dim 128, by sub-tile 2-6 % faster at head dim 64.
-  constexpr bool kTypeSplit = L::kPanels == 2;
+  // faster at head dim 128, by sub-tile 2-6 % faster at head dim 64. With the
+  // keys split each tile is one sub-tile's, and the other's issuer would only
+  // give its slots back: by type, 89 against 112 us (8 heads of 128 rows x
+  // 16384 keys on 8 SMs).
+  constexpr bool kTypeSplit = L::kPanels == 2 || kKeySplit;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -182,8 +199,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kCross) return cross_next_segment(c, s, p);
     else return next_segment<kCausal>(c, s, p);
   };
-  // Sub-tiles of the unit with any query row.
-  auto live_subtiles = [&](const Seg& s) -> int { return kCross && s.q0 + kRows >= p.N ? 1 : kSubTiles; };
+  // Sub-tiles with work: of the unit with any query row, or of the segment with any K/V tile.
+  auto live_subtiles = [&](const Seg& s) -> int {
+    if constexpr (kKeySplit) return min(s.kv_end - s.kv_begin, kSubTiles);
+    else return kCross && s.q0 + kRows >= p.N ? 1 : kSubTiles;
+  };
+  // Whether tile j of a segment from b on is sub-tile t's, and is its first or last there.
+  auto own_tile = [](int t, int j, int b) -> bool { return !kKeySplit || ((j - b) & 1) == t; };
+  auto first_tile = [](int j, int b) -> bool { return kKeySplit ? j - b < kSubTiles : j == b; };
+  auto last_tile = [](int j, int e) -> bool { return kKeySplit ? j + kSubTiles >= e : j == e - 1; };
 
   if (threadIdx.x == 0) {
     mbar_init(bar_q_full, 1);
@@ -215,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto c0 = first_segment_cursor();
     Seg w0;
     if (advance(c0, w0)) {
-      mbar_arrive_expect_tx(bar_q_full, L::kQBytes);
-      for (int t = 0; t < kSubTiles; ++t)
+      mbar_arrive_expect_tx(bar_q_full, kQTiles * L::kTileBytes);
+      for (int t = 0; t < kQTiles; ++t)
         for (int pn = 0; pn < L::kPanels; ++pn)
           tma_load_3d_hint(sQ + t * L::kTileBytes + pn * kPanelBytes, &tmQ, bar_q_full, pn * 64, w0.q0 + t * kRows,
                            w0.bh, l2_policy_evict_first());
@@ -293,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(bar_q_full, L::kQBytes);
-            for (int t = 0; t < kSubTiles; ++t)
+            mbar_arrive_expect_tx(bar_q_full, kQTiles * L::kTileBytes);
+            for (int t = 0; t < kQTiles; ++t)
               for (int pn = 0; pn < L::kPanels; ++pn)
                 tma_load_3d_hint(sQ + t * L::kTileBytes + pn * kPanelBytes, &tmQ, bar_q_full, pn * 64,
                                  w.q0 + t * kRows, w.bh, stream_once);
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_s = [&](int t, int slot) {
           const uint32_t q_lo = desc_lo_sw128(sQ, 16);
           const uint32_t ring_lo = desc_lo_sw128(sRing, 16);
-          const uint32_t qa = q_lo + static_cast<uint32_t>((t * L::kTileBytes) >> 4);
+          const uint32_t qa = q_lo + static_cast<uint32_t>(((kKeySplit ? 0 : t) * L::kTileBytes) >> 4);
           const uint32_t ka = ring_lo + static_cast<uint32_t>(slot * (L::kTileBytes >> 4));
           const uint32_t dt = tmem + static_cast<uint32_t>(t * kKeys);
 #pragma unroll
@@ -425,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot_k = take(base_idx + k_index(j, b), 0u);
                 if (slot_k < 0) { ok = false; break; }
                 for (int t = 0; t < n_sub; ++t) {
+                  if (!own_tile(t, j, b)) continue;
                   if (s_out[t]) {
                     if (!wait_bounded(bar_s_free0 + 8 * t, s_free_ph[t], wd, kSiteMmaSFree, true, kNapNs)) { ok = false; break; }
                     s_free_ph[t] ^= 1u;
@@ -469,12 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   int steps = kKeys / 16;
                   if constexpr (tail.value) steps = clean_v(w, j, slot_v);
                   for (int t = 0; t < n_sub; ++t) {
+                    if (!own_tile(t, j, b)) continue;
                     if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
                     p_full_ph[t] ^= 1u;
                     tc_fence_after_sync();
-                    issue_pv(t, slot_v, j > b, tail, steps);
+                    issue_pv(t, slot_v, !first_tile(j, b), tail, steps);
                     mma_commit(bar_p_free0 + 8 * t);
-                    if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
+                    if (last_tile(j, e)) mma_commit(bar_o_full0 + 8 * t);
                   }
                   mma_commit(bar_empty(slot_v));
                 };
@@ -600,12 +626,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of the next o_staged phase, bit 1 that of o_buf_free, bit 2 set while
     // the buffer holds an O whose store may still be reading it
     uint32_t ost_state = 0;
+    [[maybe_unused]] float* const split = reinterpret_cast<float*>(smem + L::kSplitOffset);
+    // kKeySplit: parity of sub-tile 1's statistics (sub-tile 0's warps) or of
+    // its O being read out (sub-tile 1's), and whether that is awaited
+    uint32_t split_phase = 0;
+    bool o_lent = false;
     uint32_t p_count = 0;  // P tiles published so far (= P.V products issued or pending)
     bool ok = true;
     auto cur = first_segment_cursor();
     Seg w;
     while (ok && advance(cur, w)) {
       if (t >= live_subtiles(w)) continue;
+      if constexpr (kKeySplit) {
+        // sub-tile 0 must have read the O of the segment before
+        if (o_lent) {
+          bool fb = wait_bounded(bar_ostage0 + 8, split_phase, wd, kSiteOBufFree);
+          fb = __all_sync(0xffffffffu, fb);
+          if (!fb) break;
+          tc_fence_after_sync();
+          split_phase ^= 1u;
+          o_lent = false;
+        }
+      }
       if constexpr (!L::kPInTmem) {
         // the previous segment's O was staged in this P buffer: the store
         // engine must have read it before this segment's first P overwrites it
@@ -616,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ost_state = (ost_state ^ 2u) & ~4u;
         }
       }
-      const int row = w.q0 + t * kRows + rr;
+      const int row = w.q0 + (kKeySplit ? 0 : t) * kRows + rr;
       int limit;  // allowed keys: [0, limit)
       if constexpr (kCross) limit = w.n_keys;
       else limit = kCausal ? min(p.N, row + 1) : p.N;
@@ -628,7 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // its own MMA issuer (D <= 64; with the issuers split by type the two
       // sub-tiles must stay in step)
       const int e_t = (t == 0 && L::kPInTmem) ? sub0_end<kCausal>(w) : w.kv_end;
-      for (int j = w.kv_begin; j < e_t; ++j) {
+      const int b_t = w.kv_begin + (kKeySplit ? t : 0);
+      for (int j = b_t; j < e_t; j += kKeySplit ? kSubTiles : 1) {
         bool got = wait_bounded(bar_s, s_phase, wd, kSiteSoftmaxSFull);
         got = __all_sync(0xffffffffu, got);
         if (!got) { ok = false; break; }
@@ -706,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // O holds P.V up to tile j-1 (complete, see above): rescale it now
         // that the scores are no longer held in registers.
-        if (j > w.kv_begin && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (j > b_t && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             uint32_t o[32];
@@ -745,6 +788,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!got) break;
       o_phase ^= 1u;
       tc_fence_after_sync();
+      // kKeySplit: what O of either sub-tile counts, both relative to the larger base
+      [[maybe_unused]] float f0 = 1.f, f1 = 0.f;
+      if constexpr (kKeySplit) {
+        if (t == 1) {
+          split[rr] = base;
+          split[kRows + rr] = l;
+          split[2 * kRows + rr] = l_o;
+          tc_fence_before_sync();
+          mbar_arrive(bar_part0 + 8);
+          o_lent = true;
+          continue;
+        }
+        if (live_subtiles(w) == kSubTiles) {
+          bool there = wait_bounded(bar_part0 + 8, split_phase, wd, kSitePartialWrite);
+          there = __all_sync(0xffffffffu, there);
+          if (!there) break;
+          split_phase ^= 1u;
+          tc_fence_after_sync();
+          const float base1 = split[rr], both = fmaxf(base, base1);
+          f0 = base == -CUDART_INF_F ? 0.f : ex2_approx(base - both);
+          f1 = base1 == -CUDART_INF_F ? 0.f : ex2_approx(base1 - both);
+          l = fmaf(f0, l, f1 * split[kRows + rr]);
+          l_o = fmaf(f0, l_o, f1 * split[2 * kRows + rr]);
+          base = both;
+        }
+      }
+      // 32 columns of O
+      auto load_o = [&](int cc, uint32_t (&o)[32]) {
+        tmem_ld32x32_wait(tO + cc, o);
+        if constexpr (kKeySplit) {
+          if (live_subtiles(w) == kSubTiles) {
+            uint32_t o1[32];
+            tmem_ld32x32_wait(tO + L::kDp + cc, o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(f0, __uint_as_float(o[i]), f1 * __uint_as_float(o1[i])));
+          }
+        }
+      };
+      // sub-tile 1's O has been read
+      auto give_back = [&]() {
+        if constexpr (kKeySplit) {
+          if (live_subtiles(w) == kSubTiles) {
+            tc_fence_before_sync();
+            mbar_arrive(bar_ostage0 + 8);
+          }
+        }
+      };
       if (w.kv_begin > 0) {
         // Not the unit's first tiles: hand the unnormalised partial (O, base,
         // l, l_o) to the owner through this CTA's workspace slot.
@@ -754,10 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int cc = 0; cc < D; cc += 32) {
           uint32_t o[32];
-          tmem_ld32x32_wait(tO + cc, o);
+          load_o(cc, o);
 #pragma unroll
           for (int i = 0; i < 32; ++i) __stcg(po + (cc + i) * 128 + rr, __uint_as_float(o[i]));
         }
+        give_back();
         __stcg(ps + rr, base);
         __stcg(ps + 128 + rr, l);
         __stcg(ps + 256 + rr, l_o);
@@ -828,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
         uint32_t o[32];
-        tmem_ld32x32_wait(tO + cc, o);
+        load_o(cc, o);
         float of[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]) * a_own;
@@ -862,6 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      give_back();
       if constexpr (!L::kPInTmem) {
         // One thread stores the staged tile with TMA once every row is in
         // (rows past N are clipped by the map; a sub-tile wholly past N has
@@ -906,10 +999,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The stream-K schedule waits across CTAs, so it is launched cooperatively
 // (the whole grid resident at once, or the launch fails).
-template <int D, bool kBf16, bool kCausal, bool kCross, typename P>
+template <int D, bool kBf16, bool kCausal, bool kCross, bool kKeySplit, typename P>
 cudaError_t launch_fwd_kernel(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                               const P& p, int grid, cudaStream_t stream) {
-  auto kern = fa2_fwd_kernel<D, kBf16, kCausal, kCross>;
+  auto kern = fa2_fwd_kernel<D, kBf16, kCausal, kCross, kKeySplit>;
   const int smem = kCross ? Layout<D>::kCrossSmemBytes : Layout<D>::kSmemBytes;
   // Once per device: the register check and the shared-memory opt-in.
   static PerDeviceOnce prepared;
@@ -939,13 +1032,16 @@ cudaError_t launch_fwd_kernel(const CUtensorMap& q, const CUtensorMap& k, const 
 template <int D, bool kBf16, bool kCausal>
 cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                        const Params& p, int grid, cudaStream_t stream) {
-  return launch_fwd_kernel<D, kBf16, kCausal, false>(q, k, v, o, p, grid, stream);
+  return launch_fwd_kernel<D, kBf16, kCausal, false, false>(q, k, v, o, p, grid, stream);
 }
 
 template <int D, bool kBf16>
 cudaError_t launch_cross_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
                              const CrossParams& p, int grid, cudaStream_t stream) {
-  return launch_fwd_kernel<D, kBf16, false, true>(q, k, v, o, p, grid, stream);
+  if constexpr (D <= 64) {
+    if (p.key_split) return launch_fwd_kernel<D, kBf16, false, true, true>(q, k, v, o, p, grid, stream);
+  }
+  return launch_fwd_kernel<D, kBf16, false, true, false>(q, k, v, o, p, grid, stream);
 }
 
 }  // namespace fa2
