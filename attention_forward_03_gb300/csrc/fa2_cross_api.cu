@@ -35,31 +35,47 @@ CrossFn pick_cross(int d, bool bf) {
   }
 }
 
+// Whether a unit's two sub-tiles take its key tiles in turn (fa2_kernel.cuh):
+// with at most 128 rows per key head there is no second sub-tile of rows, and
+// from 5 key tiles on the overlap is worth the joining of the two (us, with /
+// without, 1024 such heads, D = 64: 300 keys 46.4 / 42.5, 512 keys 43.1 /
+// 43.9, 768 keys 54.0 / 59.0, 4096 keys 177 / 238; 8 heads, in the best number
+// of parts, 4068 keys 16.3 / 18.3). Above D = 64 the tensor cores have more to
+// do and the gain is below a tenth (1 head per SM, 16384 keys, D = 128: 114 /
+// 131; 256 heads of 4096 keys 91.5 / 94.7), the loss at 257 keys as large.
+bool split_keys(int D, long long rows, long long nkv) { return D <= 64 && rows <= kRows && nkv > 4; }
+
 // How many CTAs share the K/V-tile steps equally, with a merge of the units
-// that they cut, or 0 for whole units in rounds. The cost of each in steps of
-// the busiest SM.
+// that they cut, or 0 for whole units in rounds.
 //
-// At least one unit per SM: as in fwd_auto_schedule; with key counts on the
-// device the units differ by an amount the host cannot know, and the shares
-// follow it.
+// At least one unit per SM: equal shares when that saves the busiest SM 5 %
+// with what the cuts cost, in steps 5, 7 above D = 64, 12 with split keys.
+// With key counts on the device the host cannot know the units; then from as
+// many tiles on as measured to pay on evenly spread counts (us, whole / equal;
+// 192 and 1024 units): D = 64, 256 rows: 4 tiles 17.8 / 18.8 and 53.2 / 58.6, 6
+// tiles 22.3 / 21.1 and 67.0 / 65.8, 32 tiles 63.3 / 44.1 and 211 / 167; D =
+// 128, 128 rows: 8 tiles 23.9 / 24.0 and 76.0 / 86.7, 12 tiles 31.8 / 28.0 and
+// 100 / 99.2; split keys: 16 tiles 26.8 / 27.2 and 77.8 / 104, 32 tiles 42.3 /
+// 38.5 and 130 / 143.
 //
-// Fewer units than SMs: cross_cut_ctas, a join at about 0.6 steps, 1.25 with
-// the wider O above D = 64, cutting at all five to six (the flags, the way
-// through memory). Measured (us, by the parts per unit; 1: not
-// cut, * the choice): 8 heads of 128 rows, D = 64: 500 keys 1* 9.1, 2 10.7;
-// 1508 keys 1 17.2, 2 17.4, 4* 14.3, 12 19.5; 4068 keys 1 36.7, 4 19.8, 6
-// 18.4, 8* 20.0, 19 23.4; 16,356 keys 1 131, 8 32.2, 12 30.6, 16* 28.4, 19 29.8.
-// D = 128: 500 keys 1* 10.8, 2 12.3; 1508 keys 1* 18.6, 3 19.7, 4 16.9, 12
-// 28.2; 4068 keys 1 37.9, 4* 22.8, 8 25.3, 19 34.5. 64 heads of 256 rows,
-// 1508 keys: D = 64 1* 21.0, 2 22.5; D = 128 1* 24.9, 2 28.5.
-int cross_share_ctas(int D, long long units, long long nkv, bool lengths, int sms) {
-  if (units >= sms) {
-    constexpr double kSplitCostSteps = 4.0;
-    const double rounds = static_cast<double>((units + sms - 1) / sms) * static_cast<double>(nkv);
-    const double balanced = static_cast<double>(units) * static_cast<double>(nkv) / sms + kSplitCostSteps;
-    return lengths || balanced < 0.95 * rounds ? sms : 0;
+// Fewer: cross_cut_ctas, in steps of about 1 us, 0.65 us with split keys.
+// Measured (us, by the parts per unit; 1: not cut, * the choice), 128 rows: D =
+// 64, 8 heads: 500 keys 1* 9.1, 2 11.2; 1508 keys 1* 13.3, 4 14.4, 12 20.8; 4068
+// keys 1 27.2, 4* 16.3, 8 17.7, 19 24.8; 16,356 keys 1 90.6, 8 26.1, 10* 26, 19
+// 28.8; 32 heads of 16,356 keys 4* 35.0, all SMs 40.0; 96
+// heads of 256 rows over up to 4096 keys 1 44.5, all SMs* 30.2. D = 128, 8 heads: 500
+// keys 1* 10.8, 2 12.3; 1508 keys 1* 18.6, 3 19.7, 4 16.9, 12 28.2; 4068 keys 1
+// 37.9, 4* 22.8, 8 25.3, 19 34.5.
+int cross_share_ctas(int D, bool split, long long units, long long nkv, bool lengths, int sms) {
+  if (units < sms) {
+    const CutCosts c = split ? CutCosts{4.6, 1.3, 12.0} : D <= 64 ? CutCosts{5.8, 0.6, 3.0} : CutCosts{5.0, 1.25, 4.0};
+    return cross_cut_ctas(units, nkv, lengths, sms, c);
   }
-  return D <= 64 ? cross_cut_ctas(units, nkv, sms, 5.8, 0.6) : cross_cut_ctas(units, nkv, sms, 5.0, 1.25);
+  const double per_sm = static_cast<double>(units) / sms;
+  if (lengths) return static_cast<double>(nkv) >= (split ? 16.0 + 5.0 * per_sm : D <= 64 ? 6.0 : 12.0) ? sms : 0;
+  const double rounds = static_cast<double>((units + sms - 1) / sms) * static_cast<double>(nkv);
+  const double balanced = per_sm * static_cast<double>(nkv) + (split ? 12.0 : D <= 64 ? 5.0 : 7.0);
+  return balanced < 0.95 * rounds ? sms : 0;
 }
 
 // What a unit counts in the equal shares besides its tiles: the tensor cores
@@ -202,8 +218,8 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   p.n_qt = (int)n_qt;
   p.num_units = (int)(bh * n_qt);
   p.nkv_full = (Nk + kKeys - 1) / kKeys;
-  p.key_split = D <= 64 && rows <= kRows && p.nkv_full >= 1;
-  int grid = workspace ? cross_share_ctas(D, p.num_units, p.nkv_full, key_lengths != nullptr, sms) : 0;
+  p.key_split = split_keys(D, rows, p.nkv_full);
+  int grid = workspace ? cross_share_ctas(D, p.key_split, p.num_units, p.nkv_full, key_lengths && B > 1, sms) : 0;
   if (grid > 0) {
     p.stream_k = 1;
     p.unit_cost = unit_cost(D, key_lengths != nullptr);

@@ -297,6 +297,28 @@ def test_units_cut_between_many_sms(c):
         assert torch.equal(go, o) and torch.equal(glse, lse)
 
 
+SPLIT_KEYS = [  # at most 128 rows per key head, D <= 64: the key tiles go to the two sub-tiles in turn
+    (3, 8, 8, 128, 700, 64, BF16, None),           # whole units, an even number of tiles
+    (40, 8, 4, 50, 600, 64, F16, None),            # more units than SMs, an odd number
+    (20, 16, 8, 40, 1000, 32, BF16, [(97 * i) % 1001 for i in range(20)]),  # 0 to 8 tiles each
+    (2, 2, 2, 17, 650, 64, BF16, [513, 1]),
+    (1, 8, 8, 100, 3000, 64, F16, [2945]),         # cut units
+    (30, 8, 8, 20, 9000, 32, F16, [300 * i for i in range(30)]),  # cut units among whole ones
+]
+
+
+@pytest.mark.parametrize("c", SPLIT_KEYS, ids=str)
+def test_key_tiles_in_turn(c):
+    q, k, v, n = inputs(*c)
+    if n is not None:  # a dominant key in one sub-tile only, and scores far below zero in a head
+        k[0, 0, : int(c[-1][0])] *= 0.1
+        k[1 % c[0], -1, min(200, max(int(c[-1][1 % c[0]]) - 1, 0))] = 4 * q[1 % c[0], -1, 0]
+    o, lse = ops().cross_attention_forward(q, k, v, key_lengths=n)
+    check_fwd(o, lse, q, k, v, c[5] ** -0.5, n)
+    again = ops().cross_attention_forward(q, k, v, key_lengths=n)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 CUT_ROWS = [  # the backward's units are key tiles, cut along the query rows
     (1, 8, 2, 1024, 77, 64, BF16, None),
     (2, 4, 4, 2100, 200, 128, F16, [200, 0]),
