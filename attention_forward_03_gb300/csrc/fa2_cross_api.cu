@@ -80,12 +80,14 @@ int cross_share_ctas(int D, bool split, long long units, long long nkv, bool len
 
 // What a unit counts in the equal shares besides its tiles: the tensor cores
 // idle while its last P.V drains and its rows go out. Without it the CTAs with
-// the short units of a padded batch came last (us, by the cost 0, 2, 3, 4: 4 x
-// 16 heads of 2048 rows over 2048, 4096, 6144 and 8192 keys, D = 128: 235, 221,
-// 221, 216; 8 x 8 heads of 1024 rows over 256, 512 .. 2048 keys: D = 128 59.9,
-// 47.2, 46.3, 46.0, D = 64 46.5, 34.2, 34.3, 34.6). Units of one length keep
-// equal tiles: there every CTA has about as many segments as any other (8
-// heads of 4096 rows x 8192 keys, D = 128: 90.6 with cost 0, 94.5 with 4).
+// the short units of a padded batch came last (us, by the cost 0, 2, 3, 4, 6:
+// 4 x 16 heads of 2048 rows over 2048, 4096, 6144 and 8192 keys, D = 128: 220,
+// 203, 208, 202, 204; 8 x 8 heads of 1024 rows over 256, 512 .. 2048 keys: D =
+// 128 55.6, 43.9, 44.3, 45.7, 45.8, D = 64 41.9, 35.4, 35.2, 35.6, 39.7; 32 x
+// 8 heads of 128 rows over 128, 256 .. 4096 keys, D = 64 59.7, 40.3, 38.5,
+// 39.0, 39.4). Units of one length keep equal tiles: there every CTA has about
+// as many segments as any other (8 heads of 4096 rows x 8192 keys, D = 128:
+// 90.6 with cost 0, 94.5 with 4).
 constexpr int unit_cost(int D, bool lengths) { return !lengths ? 0 : D <= 64 ? 3 : 4; }
 
 // Whether the few-keys kernel beats the tcgen05 one. Measured (us, few-keys
