@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
             if (32 * wg < D && pend_q0 + rr < p.N) {
               uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dq_out) +
                                                    (static_cast<size_t>(pend_bh) * p.N + pend_q0 + rr) * D + 32 * wg);
-              const float sc = p.scale;
+              const float sc = cross_grad_scale(p, pend_bh);
 #pragma unroll
               for (int ch = 0; ch < 4; ++ch) {
                 uint32_t w[4];
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         if (p.dq_out) {
           // as above; this thread holds element rr of each query row, so a
           // warp's store is 64 contiguous bytes of one row
-          const float sc = p.scale;
+          const float sc = cross_grad_scale(p, pend_bh);
           uint16_t* to = static_cast<uint16_t*>(p.dq_out) + static_cast<size_t>(pend_bh) * p.N * D + rr;
 #pragma unroll
           for (int h = 0; h < L::kHalves; ++h) {
@@ -988,7 +988,8 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       auto store_chunk = [&](int c, const float (&a)[32], const float (&b)[32]) {
         uint4* dvp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dv) + out_row + c * 64);
         uint4* dkp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dk) + out_row + c * 64);
-        const float sc = p.scale;
+        float sc = p.scale;
+        if constexpr (kCross) sc = cross_grad_scale(p, bh);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (kCross) {  // a row behind the keys: zero whatever dO and Q hold

@@ -144,15 +144,21 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
   }
 }
 
-// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per thread.
+// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per
+// thread; 0 * accumulator in a batch entry (n8 / B elements) of one key.
 template <bool kBf16>
 __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4* __restrict__ acc, uint4* __restrict__ dq,
-                                                                    float scale, long long n8) {
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+                                                                    long long n8, const CrossBwdParams p) {
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x, per = n8 / p.B;
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8; i += stride) {
-    const float4 a = acc[2 * i], b = acc[2 * i + 1];
-    dq[i] = make_uint4(pack_two(a.x * scale, a.y * scale, kBf16), pack_two(a.z * scale, a.w * scale, kBf16),
-                       pack_two(b.x * scale, b.y * scale, kBf16), pack_two(b.z * scale, b.w * scale, kBf16));
+    float scale = p.scale;
+    if (p.key_lengths) {
+      const int b = static_cast<int>(n8 >> 32 ? i / per : static_cast<uint32_t>(i) / static_cast<uint32_t>(per));
+      if (cross_keys(p, b) == 1) scale = 0.f;
+    }
+    const float4 x = acc[2 * i], y = acc[2 * i + 1];
+    dq[i] = make_uint4(pack_two(x.x * scale, x.y * scale, kBf16), pack_two(x.z * scale, x.w * scale, kBf16),
+                       pack_two(y.x * scale, y.y * scale, kBf16), pack_two(y.z * scale, y.w * scale, kBf16));
   }
 }
 
@@ -352,7 +358,7 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
   const long long n8 = bh * rows * (D / 8);
   const int blocks = static_cast<int>(std::max<long long>(1, std::min<long long>((n8 + kEndThreads - 1) / kEndThreads, 8ll * sms)));
   auto finish = bf ? fa2_cross_bwd_finish<true> : fa2_cross_bwd_finish<false>;
-  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), scale, n8);
+  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), n8, p);
   e = cudaGetLastError();
   return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
 }

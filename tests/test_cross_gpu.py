@@ -346,6 +346,24 @@ def test_backward_units_cut_between_many_sms(c):
         assert torch.equal(again[1], grads[1]) and torch.equal(again[2], grads[2])  # a fixed order
 
 
+@pytest.mark.parametrize("c", [(2, 4, 2, 70, 1, 64, BF16, None), (3, 4, 2, 130, 200, 128, F16, [1, 200, 1]),
+                               (2, 2, 2, 300, 90, 96, BF16, [90, 1])], ids=str)
+def test_gradient_over_one_key(c):
+    # the softmax is constant: dQ and dK are zero, not dP - Delta's rounding; a NaN is not lost in it
+    q, k, v, n = inputs(*c)
+    do = upstream(q)
+    o, lse = ops().cross_attention_forward(q, k, v, key_lengths=n)
+    grads = ops().cross_attention_backward(q, k, v, o, lse, do, key_lengths=n)
+    check_bwd(grads, q, k, v, o, lse, do, c[5] ** -0.5, n)
+    one = [b for b in range(c[0]) if n is None or c[-1][b] == 1]
+    for b in one:
+        assert bool((grads[0][b] == 0).all()) and bool((grads[1][b] == 0).all())
+    do[one[0], 0, 5, 7] = float("nan")
+    dq, dk, dv = ops().cross_attention_backward(q, k, v, o, lse, do, key_lengths=n)
+    assert bool(dq[one[0], 0, 5].isnan().all()) and bool((dq[one[0], 1] == 0).all())
+    assert bool(dk[one[0], 0, 0].isnan().any()) and bool(dv[one[0], 0, 0, 7].isnan())
+
+
 def test_two_streams_at_once():
     cs = [(2, 8, 2, 1, 6000, 128, BF16, [6000, 2000]), (1, 4, 4, 400, 6000, 64, F16, [5001])]
     sets = [inputs(*c) for c in cs]
