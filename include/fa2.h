@@ -484,7 +484,9 @@ FA2_API int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes);
  * dO, dQ    : device pointers, contiguous [B, Hq, Nq, D] of `dtype`.
  * dK, dV    : device pointers, contiguous [B, Hkv, Nk, D] of `dtype`. Rows
  *             behind a batch entry's keys are zeros, as is dQ of rows without
- *             keys; K and V there are never used.
+ *             keys; K and V there are never used. A batch entry with one key
+ *             has dQ = dK = 0 (its softmax is constant), NaN where dO is not
+ *             finite.
  * workspace : device memory of at least fa2_cross_bwd_workspace_bytes(...)
  *             bytes, 256-byte aligned; scratch, needs no initialisation, not
  *             shared by calls that run at the same time. May be NULL where

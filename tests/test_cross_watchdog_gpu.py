@@ -67,3 +67,24 @@ def test_a_withheld_tile_of_a_cut_unit_times_out(fa2):
     torch.cuda.synchronize()
     assert fa2.fa2_device_status(clear=True) == 0
     check_cross_fwd(o, lse, q, k, v, 0.125, None)
+
+
+@pytest.mark.parametrize("Nk", [900, 6000])  # whole units and cut ones
+def test_a_withheld_tile_times_out_with_key_tiles_in_turn(fa2, Nk):
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn(2, 4, n, 64, generator=g).bfloat16().cuda() for n in (100, Nk, Nk))
+    fa2.cross_attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    try:
+        fa2.fa2_set_watchdog_ns(20_000_000)  # 20 ms
+        assert fa2.library().fa2_test_withhold_next_load(1) == fa2.FA2_OK
+        fa2.cross_attention_forward(q, k, v)
+        torch.cuda.synchronize()
+        assert fa2.fa2_device_status(clear=True) > 0
+    finally:
+        fa2.library().fa2_test_withhold_next_load(0)
+        fa2.fa2_set_watchdog_ns(0)
+    o, lse = fa2.cross_attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    assert fa2.fa2_device_status(clear=True) == 0
+    check_cross_fwd(o, lse, q, k, v, 0.125, None)
