@@ -97,7 +97,9 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi, bool bf16) {
 // Per row (b, h, i) of the padded [B*H, Npad] grid: Delta_i = <dO_i, O_i>
 // and -LSE_i * log2(e), the offset the main kernel adds to S * scale*log2(e)
 // with one packed FMA per two scores (rows >= N: 0 and -inf, so that P is 0
-// there), and zeroes the row of the fp32 dQ accumulator. D/8 threads per
+// there), and zeroes the row of the fp32 dQ accumulator; and the flags of
+// partial results are taken back, so that a replay of a captured call, which
+// carries the same tag, does not find them set. D/8 threads per
 // row, 8 elements (16 bytes) each, in groups of kLanes (D/8 rounded up to a
 // power of two: the shuffle reduction's width; the extra lanes add zero);
 // the loop bound is a multiple of 32 so that whole warps take part.
@@ -106,8 +108,11 @@ __global__ void __launch_bounds__(kElemThreads) fa2_bwd_prologue(const uint4* __
                                                                  const uint4* __restrict__ dO,
                                                                  const float* __restrict__ LSE,
                                                                  float* __restrict__ dq_acc, float* __restrict__ neg_lse2,
-                                                                 float* __restrict__ delta, int N, int Npad,
-                                                                 long long rows) {
+                                                                 float* __restrict__ delta,
+                                                                 unsigned long long* __restrict__ flags, int N,
+                                                                 int Npad, long long rows) {
+  static_assert(kBwdMaxCtas <= kElemThreads, "a thread per flag");
+  if (blockIdx.x == 0 && threadIdx.x < kBwdMaxCtas) flags[threadIdx.x] = 0ull;
   constexpr int kPer = D / 8;  // threads with data per row
   constexpr int kLanes = kPer <= 4 ? 4 : (kPer <= 8 ? 8 : (kPer <= 16 ? 16 : 32));
   static_assert(kPer <= 32, "head dimension");
@@ -177,13 +182,14 @@ BwdLaunchFn pick_bwd(int d, int dtype, int causal) {
 
 template <int D>
 cudaError_t launch_prologue(bool bf16, const void* O, const void* dO, const float* LSE, float* dq_acc, float* neg_lse2,
-                            float* delta, int N, int Npad, long long rows, int grid, cudaStream_t s) {
+                            float* delta, unsigned long long* flags, int N, int Npad, long long rows, int grid,
+                            cudaStream_t s) {
   const uint4* o = static_cast<const uint4*>(O);
   const uint4* g = static_cast<const uint4*>(dO);
   if (bf16)
-    fa2_bwd_prologue<D, true><<<grid, kElemThreads, 0, s>>>(o, g, LSE, dq_acc, neg_lse2, delta, N, Npad, rows);
+    fa2_bwd_prologue<D, true><<<grid, kElemThreads, 0, s>>>(o, g, LSE, dq_acc, neg_lse2, delta, flags, N, Npad, rows);
   else
-    fa2_bwd_prologue<D, false><<<grid, kElemThreads, 0, s>>>(o, g, LSE, dq_acc, neg_lse2, delta, N, Npad, rows);
+    fa2_bwd_prologue<D, false><<<grid, kElemThreads, 0, s>>>(o, g, LSE, dq_acc, neg_lse2, delta, flags, N, Npad, rows);
   return cudaGetLastError();
 }
 
@@ -264,6 +270,7 @@ extern "C" int fa2_bwd_sched(const void* Q, const void* K, const void* V, const 
   if (!mapped) return record_cuda_error(cudaErrorInvalidValue);
   float* neg_lse2 = reinterpret_cast<float*>(ws + wl.dq_bytes);
   float* delta = reinterpret_cast<float*>(ws + wl.dq_bytes + wl.stat_bytes);
+  unsigned long long* flags = reinterpret_cast<unsigned long long*>(ws + wl.dq_bytes + 2 * wl.stat_bytes + wl.part_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == FA2_BF16;
 
@@ -271,10 +278,10 @@ extern "C" int fa2_bwd_sched(const void* Q, const void* K, const void* V, const 
   const int pgrid = grid_for(rows * (D / 8), sms);
   cudaError_t e;
   switch (D) {
-    case 32: e = launch_prologue<32>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
-    case 64: e = launch_prologue<64>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
-    case 96: e = launch_prologue<96>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
-    default: e = launch_prologue<128>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, N, npad, rows, pgrid, s); break;
+    case 32: e = launch_prologue<32>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, flags, N, npad, rows, pgrid, s); break;
+    case 64: e = launch_prologue<64>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, flags, N, npad, rows, pgrid, s); break;
+    case 96: e = launch_prologue<96>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, flags, N, npad, rows, pgrid, s); break;
+    default: e = launch_prologue<128>(bf, O, dO, LSE, dq_acc, neg_lse2, delta, flags, N, npad, rows, pgrid, s); break;
   }
   if (e != cudaSuccess) return record_cuda_error(e);
 
@@ -318,7 +325,7 @@ extern "C" int fa2_bwd_sched(const void* Q, const void* K, const void* V, const 
     p.stream_k = 1;
     grid = sk_grid;
     p.ws_part = reinterpret_cast<float*>(ws + wl.dq_bytes + 2 * wl.stat_bytes);
-    p.ws_flags = reinterpret_cast<unsigned long long*>(ws + wl.dq_bytes + 2 * wl.stat_bytes + wl.part_bytes);
+    p.ws_flags = flags;
     p.epoch = next_launch_epoch();
   }
   e = pick_bwd(D, dtype, is_causal)(mk, mv, mq, mdo, mdq, p, grid, s);

@@ -482,6 +482,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           fine = wait_flag(p.ws_flags + static_cast<size_t>(cb), p.epoch, wd, kSitePartialFlag);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
+        __syncwarp();
+        // Every thread of the warpgroup has seen the flags: take them back,
+        // so that a replay of a captured launch, which carries the same
+        // tag, does not find them set before its partials are written.
+        mbar_arrive(bar_part);
+        if (rr < 32) {
+          bool seen = wait_bounded(bar_part, part_phase, wd, kSitePartialFlag);
+          seen = __all_sync(0xffffffffu, seen);
+          if (!seen) break;
+          for (int cb = first_c + rr; cb <= last_c; cb += 32) p.ws_flags[cb] = 0ull;
+        }
+        part_phase ^= 1u;
         for (int cb = first_c; cb <= last_c; ++cb)
           nbase = fmaxf(nbase, __ldcg(p.ws_stats + static_cast<size_t>(cb) * 3 * 128 + rr));
         a_own = ex2_approx(base - nbase);

@@ -123,6 +123,8 @@ FA2_API int fa2_fwd_workspace_bytes(int D, size_t* bytes);
  *   device buffer of at least fa2_fwd_workspace_bytes(D) bytes that overlaps
  *   no tensor. Its contents need no initialisation and are scratch after the
  *   call; calls that share a workspace must not run concurrently on the GPU.
+ *   A captured call can be replayed; the replays share the workspace. (After
+ *   a timeout that fa2_device_status reports, the call is captured anew.)
  * The launch is cooperative (all CTAs resident); if that cannot be arranged
  * the call returns FA2_ERR_CUDA.
  * Errors as fa2_fwd, plus FA2_ERR_INVALID_ARG for a workspace that is too
