@@ -11,6 +11,8 @@ import ctypes
 import math
 import os
 
+from .streams import device_guard, empty_on
+
 LIB_NAME = "libfa2_gb300.so"
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), LIB_NAME)
 
@@ -232,6 +234,25 @@ def workspace_for(device, D: int, stream=None):
     return ws
 
 
+def _captured_workspace(q, causal: bool, code_sched: int, stream):
+    """The workspace of a captured attention_forward: its own, since two graphs may be replayed at once; None where
+    the call runs in rounds. `stream` is the caller's argument; q's device is current."""
+    import torch
+    B, H, N, D = q.shape
+    if code_sched == FA2_SCHED_AUTO and fa2_fwd_schedule_for(B, H, N, D, causal, sm_count(q.device)) == FA2_SCHED_UNITS:
+        return None
+    return empty_on(stream, fa2_fwd_workspace_bytes(D), torch.uint8, q.device)
+
+
+def _capturing(stream) -> bool:
+    """Whether a call on `stream` (the caller's argument; None: the current stream) is being captured into a graph."""
+    import torch
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def sm_count(device) -> int:
     import torch
     dev = torch.device(device)
@@ -300,7 +321,8 @@ def attention_forward(q, k, v, scale: float | None = None, is_causal: bool = Fal
     tiles per CTA in rounds, no workspace).
     workspace: optional uint8 CUDA tensor for the balanced schedule; by default
     a cached one per (device, head dim, stream) is used, so calls on different
-    streams never share one.
+    streams never share one, and a captured call gets its own, so that two
+    graphs never share one either.
     The checks here are the ones the C ABI cannot make (tensor metadata); the
     library checks sizes, alignment and overlap itself.
     """
@@ -337,8 +359,11 @@ def attention_forward(q, k, v, scale: float | None = None, is_causal: bool = Fal
     if code_sched == FA2_SCHED_UNITS:
         ws_ptr, ws_bytes = None, 0
     else:
-        ws = workspace if workspace is not None else workspace_for(dev, D, s)
-        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        ws = workspace
+        if ws is None:
+            with device_guard(dev.index):
+                ws = _captured_workspace(q, is_causal, code_sched, stream) if _capturing(stream) else workspace_for(dev, D, s)
+        ws_ptr, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     lib = _lib if _lib is not None else library()
     if torch.cuda.current_device() == dev.index:
         code = lib.fa2_fwd_sched(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, N,

@@ -98,3 +98,30 @@ def test_backward(fa2, c):
         # dK and dV are summed in a fixed order; dQ is not
         assert torch.equal(grads[1], want[1]) and torch.equal(grads[2], want[2]), seed
         assert float((grads[0].double() - want[0].double()).norm()) <= 2e-3 * float(want[0].double().norm()), seed
+
+
+@pytest.mark.parametrize("schedule", ["auto", "balanced"])
+@pytest.mark.parametrize("on_a_stream", [False, True])
+def test_two_graphs_replayed_at_once(fa2, schedule, on_a_stream):
+    # each graph's cut units have partial results of their own
+    sets = [new((1, 8, 8192, 128, BF16, False))[:3] for _ in range(2)]
+    graphs, outs = [], []
+    for i, s in enumerate(sets):
+        fill(s, i)
+        fa2.attention_forward(*s, schedule=schedule)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            arg = {"stream": torch.cuda.current_stream()} if on_a_stream else {}
+            outs.append(fa2.attention_forward(*s, schedule=schedule, **arg))
+        graphs.append(g)
+    want = [fa2.attention_forward(*s, schedule=schedule) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
