@@ -78,8 +78,8 @@ def cross_attention_forward(q, k, v, scale: float | None = None, key_lengths=Non
     key gives O = 0 and LSE = +inf.
     out, lse: caller-owned outputs. workspace: a uint8 CUDA tensor of at least
     fa2_cross_fwd_workspace_bytes(D) bytes (by default one is kept for each
-    device, head dim and current stream; a captured call, and one that names
-    its stream, gets its own).
+    device, head dim, current stream and host thread; a captured call, and one
+    that names its stream, gets its own).
     Runs on `stream` (a torch.cuda.Stream) or the current stream.
     """
     import torch

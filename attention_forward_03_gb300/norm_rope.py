@@ -184,8 +184,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain=None, k_gain=None, cos=No
     gradient; each may be exactly its upstream gradient or its input.
     workspace: optional uint8 CUDA tensor of at least
     fa2_qk_norm_rope_bwd_workspace_bytes(D) bytes (by default one is kept for
-    each device, head dim and current stream; a captured call, and one that
-    names its stream, gets its own).
+    each device, head dim, current stream and host thread; a captured call, and
+    one that names its stream, gets its own).
     """
     like, Hq, Hkv, B, N, D, dt, dev, qs, ks = _check_sides(q, k)
     gain_f32 = _check_gains(q_gain, k_gain, D, dt, dev)

@@ -13,6 +13,8 @@ before, of which the library's own share is 5 us).
 """
 from __future__ import annotations
 
+import threading
+
 
 def stream_handle(index: int, stream, tensors) -> int:
     """The handle of `stream`, or of the current stream of device `index`; records `tensors` (None skipped) on a given one."""
@@ -44,23 +46,30 @@ def empty_on(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-_scratch = {}
+_scratch = threading.local()  # .kept: the workspaces of this host thread
 
 
 def scratch_for(kind, need, device, index, handle, stream):
     """A workspace of `need` bytes for a call on stream `handle` of device `index`.
 
-    To be called with that device current. One per kind, size and current stream is kept: calls on one stream are
-    ordered, so they may share it. A call that names its stream, and one that
-    is being captured (two graphs may be replayed at once), gets its own.
+    To be called with that device current. One per kind, size, current stream
+    and host thread is kept: the calls of a thread on one stream are ordered,
+    so they may share it. Those of two threads are not, where a call is more
+    than one kernel: theirs could alternate. A call that names its stream, and
+    one that is being captured (two graphs may be replayed at once), gets its
+    own.
     """
     import torch
     if stream is not None or torch.cuda.is_current_stream_capturing():
         return empty_on(stream, max(need, 1), torch.uint8, device)
+    try:
+        kept = _scratch.kept
+    except AttributeError:
+        kept = _scratch.kept = {}
     key = (kind, need, index, handle)
-    ws = _scratch.get(key)
+    ws = kept.get(key)
     if ws is None:
-        ws = _scratch[key] = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        ws = kept[key] = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     return ws
 
 
