@@ -75,7 +75,8 @@ def cross_attention_forward(q, k, v, scale: float | None = None, key_lengths=Non
     O is like q, LSE float32 [B, Hq, Nq]. Query head h reads key head
     h // (Hq // Hkv). key_lengths: int32 [B], the keys each batch entry has
     (default: all Nk); what lies behind them is never used. A row without any
-    key gives O = 0 and LSE = +inf.
+    key gives O = 0 and LSE = +inf (not the -inf of an empty sum: merging two
+    attentions by their LSE, replace it); one with a NaN or +inf score gives NaN.
     out, lse: caller-owned outputs. workspace: a uint8 CUDA tensor of at least
     fa2_cross_fwd_workspace_bytes(D) bytes (by default one is kept for each
     device, head dim, current stream and host thread; a captured call, and one

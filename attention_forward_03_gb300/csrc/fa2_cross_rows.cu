@@ -99,14 +99,15 @@ struct TileCursor {
   }
 };
 
-// Elements [4 d, 4 d + 4) of a finished row, and with d = 0 its LSE.
+// Elements [4 d, 4 d + 4) of a finished row, and with d = 0 its LSE (a NaN sum
+// is no row without keys: it stays).
 template <int D, bool kBf16>
 __device__ __forceinline__ void write_row(const CrossRowsParams& p, size_t row, int d, const float4& v, float m,
                                           float sum, float sum_o) {
   const float inv = sum > 0.f ? __frcp_rn(sum_o) : 0.f;
   reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D)[d] =
       make_uint2(pack2(v.x * inv, v.y * inv, kBf16), pack2(v.z * inv, v.w * inv, kBf16));
-  if (d == 0) p.lse[row] = sum > 0.f ? (m + __log2f(sum)) * 0.69314718055994530942f : CUDART_INF_F;
+  if (d == 0) p.lse[row] = sum != 0.f ? (m + __log2f(sum)) * 0.69314718055994530942f : CUDART_INF_F;
 }
 
 // By the whole CTA that holds the first tiles of a cut unit: its own result

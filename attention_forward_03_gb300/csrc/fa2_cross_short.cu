@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(D, kSteps)) fa2_cros
         for (int j = 0; j < 4; ++j) w[j] = pack2(o[4 * i + j][2 * h] * inv, o[4 * i + j][2 * h + 1] * inv, kBf16);
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + at * D + 32 * i + 8 * t) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (t == 0) p.lse[at] = l[h] > 0.f ? (m[h] + __log2f(l[h])) * 0.69314718055994530942f : CUDART_INF_F;
+      if (t == 0) p.lse[at] = l[h] != 0.f ? (m[h] + __log2f(l[h])) * 0.69314718055994530942f : CUDART_INF_F;
     }
   }
 }

@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (live) {
         p.lse[static_cast<size_t>(w.bh) * p.N + row] =
-            (l > 0.f) ? (base + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;
+            (kCross ? l != 0.f : l > 0.f) ? (base + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;  // kCross: NaN stays
       }
       // O_t is read out; the next segment's first P.V may overwrite it once
       // this warpgroup publishes that segment's first P (ordered by bar_p).

@@ -437,7 +437,10 @@ FA2_API int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const v
  *   O[b,h,i,:] = softmax_j(scale <Q[b,h,i,:], K[b,g,j,:]>) V[b,g,:,:],
  *   LSE[b,h,i] = ln sum_j exp(scale <Q[b,h,i,:], K[b,g,j,:]>)
  *   over the keys j < key_lengths[b], with key head g = h / (Hq / Hkv).
- * A row without any key gives O = 0 and LSE = +inf.
+ * A row without any key gives O = 0 and LSE = +inf: the sum is empty and its
+ * logarithm -inf, but with +inf the backward's exp(x - LSE) is 0. To merge two
+ * attentions by their LSE, take such a row's as -inf. A row with a NaN or +inf
+ * score gives NaN, O and LSE.
  *
  * Q, O      : device pointers, contiguous [B, Hq, Nq, D] of `dtype`.
  * K, V      : device pointers, contiguous [B, Hkv, Nk, D] of `dtype`. What
