@@ -119,7 +119,8 @@ def cross_attention_backward(q, k, v, o, lse, do, scale: float | None = None, ke
     """Gradient of cross_attention_forward w.r.t. q, k, v for an upstream gradient `do` of O; returns (dQ, dK, dV).
 
     q, k, v, scale, key_lengths are the forward's, o and lse its outputs for
-    them. dQ is like q; dK and dV are like k, summed over the query heads of
+    them, or the merged ones of a softmax that k and v are a part of (then dQ
+    is the part's share). dQ is like q; dK and dV are like k, summed over the query heads of
     each key head, with zeros behind the key lengths.
     dq, dk, dv: caller-owned outputs. workspace: a uint8 CUDA tensor of at
     least fa2_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, D) bytes

@@ -292,7 +292,8 @@ __device__ __forceinline__ bool bwd_next_segment(BwdCursor& c, BwdSegment& s, co
 // kCross: cross attention (fa2_cross.h). The differences: the walk (a batch
 // entry has as many K/V tiles as its keys fill), keys and queries of
 // different lengths, and rows of K behind the keys zeroed before dQ reads
-// them (their dS is zero, but what lies there can be a NaN).
+// them (their dS is zero, but what lies there can be a NaN), or V's row of a
+// batch entry with one key (fa2_cross_bwd_api.cu says why).
 template <int D, bool kBf16, bool kCausal, bool kCross = false>
 __global__ void __launch_bounds__(bwd_threads(D), 1)
     fa2_bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -568,6 +569,8 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           if constexpr (kCross) {
             if (scores && sg.n_keys < p.Nk && sg.n_keys - sg.kv * kBwdKeys < kBwdKeys)
               cross_zero_rows(sK, L::kPanels, sg.n_keys - sg.kv * kBwdKeys);
+            // one key: the prologue's Delta is <dO, O - V> already, so dP is 0
+            if (scores && sg.n_keys == 1) cross_zero_rows(sV, L::kPanels, 0);
           }
           for (int t = 0; t < n_steps; ++t, ++g) {
             if (!wait_bounded(bar_stage_full(slot), ph, wd, kSiteBwdStageFull, true, 0u)) {
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
             if (32 * wg < D && pend_q0 + rr < p.N) {
               uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dq_out) +
                                                    (static_cast<size_t>(pend_bh) * p.N + pend_q0 + rr) * D + 32 * wg);
-              const float sc = cross_grad_scale(p, pend_bh);
+              const float sc = p.scale;
 #pragma unroll
               for (int ch = 0; ch < 4; ++ch) {
                 uint32_t w[4];
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         if (p.dq_out) {
           // as above; this thread holds element rr of each query row, so a
           // warp's store is 64 contiguous bytes of one row
-          const float sc = cross_grad_scale(p, pend_bh);
+          const float sc = p.scale;
           uint16_t* to = static_cast<uint16_t*>(p.dq_out) + static_cast<size_t>(pend_bh) * p.N * D + rr;
 #pragma unroll
           for (int h = 0; h < L::kHalves; ++h) {
@@ -988,8 +991,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       auto store_chunk = [&](int c, const float (&a)[32], const float (&b)[32]) {
         uint4* dvp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dv) + out_row + c * 64);
         uint4* dkp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dk) + out_row + c * 64);
-        float sc = p.scale;
-        if constexpr (kCross) sc = cross_grad_scale(p, bh);
+        const float sc = p.scale;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (kCross) {  // a row behind the keys: zero whatever dO and Q hold

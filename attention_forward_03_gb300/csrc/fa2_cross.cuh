@@ -230,16 +230,6 @@ __device__ __forceinline__ bool cross_bwd_next_segment(CrossCursor& c, CrossBwdS
   return false;
 }
 
-// What dQ and dK of key head bh are multiplied by. The softmax over one key is
-// constant: there dS = dP - Delta is 0 but for its rounding, which goes no
-// further (0 * x: a NaN or an infinity does). Asked again where it is needed:
-// kept in a register through the step loop it cost 4 % at D = 128 (8 heads of
-// 4096 rows x 8192 keys 310 -> 322 us).
-__device__ __forceinline__ float cross_grad_scale(const CrossBwdParams& p, int bh) {
-  if (!p.key_lengths) return p.Nk == 1 ? 0.f : p.scale;
-  return cross_keys(p, bh / p.heads) == 1 ? 0.f : p.scale;
-}
-
 // A K or V tile's rows [valid, 16-row boundary) in shared memory, zeroed by
 // one thread: what lies behind a batch entry's keys can be anything, and a
 // product of a zero weight with a NaN is a NaN. The products that contract

@@ -49,20 +49,30 @@ __device__ __forceinline__ uint32_t pack_two(float lo, float hi, bool bf16) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+__device__ __forceinline__ float2 unpack_two(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, bool bf16) {
   const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 f, g;
-    if (bf16) {
-      f = make_float2(__uint_as_float(a[i] << 16), __uint_as_float(a[i] & 0xffff0000u));
-      g = make_float2(__uint_as_float(b[i] << 16), __uint_as_float(b[i] & 0xffff0000u));
-    } else {
-      f = __half22float2(*reinterpret_cast<const __half2*>(&a[i]));
-      g = __half22float2(*reinterpret_cast<const __half2*>(&b[i]));
-    }
+    const float2 f = unpack_two(a[i], bf16), g = unpack_two(b[i], bf16);
     s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+  }
+  return s;
+}
+
+// x - v, element by element in 32 bits, in products with y.
+__device__ __forceinline__ float dot8_diff(const uint4& x, const uint4& v, const uint4& y, bool bf16) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {v.x, v.y, v.z, v.w}, c[4] = {y.x, y.y, y.z, y.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_two(a[i], bf16), g = unpack_two(b[i], bf16), h = unpack_two(c[i], bf16);
+    s = fmaf(f.x - g.x, h.x, fmaf(f.y - g.y, h.y, s));
   }
   return s;
 }
@@ -70,6 +80,11 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, bool bf16)
 // Before the main kernel. Per row of the padded [B*Hkv, Npad] grid: Delta_i =
 // <dO_i, O_i> and -LSE_i * log2(e) (rows >= N: 0 and -inf, so that P is 0
 // there), and the row of the fp32 dQ accumulator zeroed, where there is one.
+// In a batch entry with one key, Delta_i = <dO_i, O_i - V_0>, and the main
+// kernel takes V_0 as 0: dP - Delta is then what it was without the rounding
+// of two sums that cancel. With the forward's own O, which is V_0 there, it is
+// exactly 0; with the O and LSE of a larger softmax that the key is a part of,
+// it is that part's.
 // Zeros also for what no unit writes: dK and dV of tiles wholly behind their
 // keys, and without an accumulator dQ of batch entries without keys. And the
 // flags of the partial results taken back, so that a replay of a captured
@@ -79,6 +94,7 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, bool bf16)
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint4* __restrict__ O,
                                                                       const uint4* __restrict__ dO,
+                                                                      const uint4* __restrict__ V,
                                                                       const float* __restrict__ LSE, float* neg_lse2,
                                                                       float* delta, uint4* dk, uint4* dv,
                                                                       const CrossBwdParams p) {
@@ -94,6 +110,7 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
     const int bh = static_cast<int>(it / tiles);
     const int r0 = static_cast<int>(it - static_cast<long long>(bh) * tiles) * kStatRows + threadIdx.x / kLanes;
     const size_t head = static_cast<size_t>(bh) * p.N;
+    const bool one_key = cross_keys(p, bh / p.heads) == 1;
     uint4 x[kPasses], g[kPasses];
 #pragma unroll
     for (int s = 0; s < kPasses; ++s) {
@@ -104,6 +121,7 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
         g[s] = dO[(head + r) * kPer + part];
       }
     }
+    const uint4 v0 = one_key && part < kPer ? V[static_cast<size_t>(bh) * p.Nk * kPer + part] : z;
 #pragma unroll
     for (int s = 0; s < kPasses; ++s) {
       const int r = r0 + s * (kEndThreads / kLanes);
@@ -112,7 +130,7 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
         to[0] = z;
         to[1] = z;
       }
-      float d = dot8(x[s], g[s], kBf16);
+      float d = one_key ? dot8_diff(x[s], v0, g[s], kBf16) : dot8(x[s], g[s], kBf16);
 #pragma unroll
       for (int off = kLanes / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off, kLanes);
       if (part == 0) {
@@ -144,18 +162,12 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
   }
 }
 
-// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per
-// thread; 0 * accumulator in a batch entry (n8 / B elements) of one key.
+// After the main kernel: dQ = dtype(scale * accumulator), 8 elements per thread.
 template <bool kBf16>
 __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4* __restrict__ acc, uint4* __restrict__ dq,
-                                                                    long long n8, const CrossBwdParams p) {
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x, per = n8 / p.B;
+                                                                    long long n8, float scale) {
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8; i += stride) {
-    float scale = p.scale;
-    if (p.key_lengths) {
-      const int b = static_cast<int>(n8 >> 32 ? i / per : static_cast<uint32_t>(i) / static_cast<uint32_t>(per));
-      if (cross_keys(p, b) == 1) scale = 0.f;
-    }
     const float4 x = acc[2 * i], y = acc[2 * i + 1];
     dq[i] = make_uint4(pack_two(x.x * scale, x.y * scale, kBf16), pack_two(x.z * scale, x.w * scale, kBf16),
                        pack_two(y.x * scale, y.y * scale, kBf16), pack_two(y.z * scale, y.w * scale, kBf16));
@@ -163,13 +175,14 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4
 }
 
 template <int D>
-cudaError_t launch_prologue(bool bf, const void* O, const void* dO, const float* LSE, float* neg_lse2, float* delta,
-                            void* dK, void* dV, const CrossBwdParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_prologue(bool bf, const void* O, const void* dO, const void* V, const float* LSE, float* neg_lse2,
+                            float* delta, void* dK, void* dV, const CrossBwdParams& p, int sms, cudaStream_t s) {
   const long long items = static_cast<long long>(p.BH) * (p.Npad / kStatRows);
   const int grid = static_cast<int>(std::min<long long>(items, 8ll * sms));
   auto kern = bf ? fa2_cross_bwd_prologue<D, true> : fa2_cross_bwd_prologue<D, false>;
-  kern<<<grid, kEndThreads, 0, s>>>(static_cast<const uint4*>(O), static_cast<const uint4*>(dO), LSE, neg_lse2, delta,
-                                    static_cast<uint4*>(dK), static_cast<uint4*>(dV), p);
+  kern<<<grid, kEndThreads, 0, s>>>(static_cast<const uint4*>(O), static_cast<const uint4*>(dO),
+                                    static_cast<const uint4*>(V), LSE, neg_lse2, delta, static_cast<uint4*>(dK),
+                                    static_cast<uint4*>(dV), p);
   return cudaGetLastError();
 }
 
@@ -345,10 +358,10 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
     p.dq_acc = nullptr;
   }
   switch (D) {
-    case 32: e = launch_prologue<32>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
-    case 64: e = launch_prologue<64>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
-    case 96: e = launch_prologue<96>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
-    default: e = launch_prologue<128>(bf, O, dO, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    case 32: e = launch_prologue<32>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    case 64: e = launch_prologue<64>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    case 96: e = launch_prologue<96>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    default: e = launch_prologue<128>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
   }
   if (e != cudaSuccess) return record_cuda_error(e);
   e = pick_cross_bwd(D, bf)(mk, mv, mq, mdo, mdq, p, grid, s);
@@ -358,7 +371,7 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
   const long long n8 = bh * rows * (D / 8);
   const int blocks = static_cast<int>(std::max<long long>(1, std::min<long long>((n8 + kEndThreads - 1) / kEndThreads, 8ll * sms)));
   auto finish = bf ? fa2_cross_bwd_finish<true> : fa2_cross_bwd_finish<false>;
-  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), n8, p);
+  finish<<<blocks, kEndThreads, 0, s>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint4*>(dQ), n8, scale);
   e = cudaGetLastError();
   return e == cudaSuccess ? FA2_OK : record_cuda_error(e);
 }

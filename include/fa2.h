@@ -485,13 +485,17 @@ FA2_API int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes);
  *   dQ = scale * dS K,  dK = scale * dS^T Q
  * dK and dV of a key head are sums over its Hq / Hkv query heads.
  *
- * Q, K, V, key_lengths, scale: the forward's. O, LSE: its outputs for them.
+ * Q, K, V, key_lengths, scale: the forward's. O, LSE: its outputs for them, or
+ *             those of a softmax over more keys, these among them (K and V
+ *             given in parts, O and LSE merged): then dK and dV are the part's,
+ *             and dQ its share.
  * dO, dQ    : device pointers, contiguous [B, Hq, Nq, D] of `dtype`.
  * dK, dV    : device pointers, contiguous [B, Hkv, Nk, D] of `dtype`. Rows
  *             behind a batch entry's keys are zeros, as is dQ of rows without
- *             keys; K and V there are never used. A batch entry with one key
- *             has dQ = dK = 0 (its softmax is constant), NaN where dO is not
- *             finite.
+ *             keys; K and V there are never used. In a batch entry with one
+ *             key dP - Delta is <dO, V - O>, element by element: exactly 0
+ *             where O is V (the softmax over one key is constant), NaN where
+ *             dO is not finite.
  * workspace : device memory of at least fa2_cross_bwd_workspace_bytes(...)
  *             bytes, 256-byte aligned; scratch, needs no initialisation, not
  *             shared by calls that run at the same time. May be NULL where
