@@ -149,7 +149,10 @@ struct BwdLayout {
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kCrossStart = kMisc + 16;        // cross attention: CrossStart
   static constexpr int kSmemBytes = kMisc + 16 + 1024;  // + slack for 1 KB alignment
-  static constexpr int kCrossSmemBytes = kSmemBytes + sizeof(CrossStart);
+  // ... and in fp16 every compute warp's maxima for a unit's scale, [2 units][8][4] words, and their barrier
+  static constexpr int kRange = (kCrossStart + static_cast<int>(sizeof(CrossStart)) + 15) / 16 * 16;
+  static constexpr int kRangeBar = kRange + 2 * 8 * 16;
+  static constexpr int kCrossSmemBytes = kRangeBar + 8 + 1024;
   static constexpr uint32_t kColDV = 0;
   static constexpr uint32_t kColDK = kDp;
   static constexpr uint32_t kColS = 2 * kDp;
@@ -293,7 +296,8 @@ __device__ __forceinline__ bool bwd_next_segment(BwdCursor& c, BwdSegment& s, co
 // entry has as many K/V tiles as its keys fill), keys and queries of
 // different lengths, and rows of K behind the keys zeroed before dQ reads
 // them (their dS is zero, but what lies there can be a NaN), or V's row of a
-// batch entry with one key (fa2_cross_bwd_api.cu says why).
+// batch entry with one key (fa2_cross_bwd_api.cu says why). In fp16 P and dS
+// have a scale per unit (cross_unit_shift).
 template <int D, bool kBf16, bool kCausal, bool kCross = false>
 __global__ void __launch_bounds__(bwd_threads(D), 1)
     fa2_bwd_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -303,6 +307,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
   static_assert(!(kCross && kCausal), "cross attention has no causal mask");
   using L = BwdLayout<D>;
   using Seg = std::conditional_t<kCross, CrossBwdSegment, BwdSegment>;
+  constexpr bool kScaled = kCross && !kBf16;
   constexpr bool kTwoIssuers = true;
   constexpr bool kATmem = L::kGradATmem;  // dS^T in TMEM for dK (P^T is there for dV at every D)
   constexpr bool kDqWarp = bwd_threads(D) > 352;  // staged dQ^T added by warp kBwdDqWarp
@@ -383,6 +388,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       mbar_init(bar_dqs_free(w), 1);
     }
     mbar_init(bar_part, kBwdComputeThreads);
+    if constexpr (kScaled) mbar_init(base + L::kRangeBar, kBwdComputeThreads / 32);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -718,6 +724,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
     int slot = 0;
     bool ok = true;
     int pend_bh = 0, pend_q0 = 0;  // head and first row of the step whose dQ^T is pending
+    [[maybe_unused]] float pend_us = 1.f;  // and its unit's 2^-e
 
     // dQ^T of global step `step` (head pend_bh, rows pend_q0 + kCW*wg +
     // [0, kCW)) from TMEM into the fp32 accumulator: this thread holds
@@ -741,6 +748,10 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         tmem_ld32x32_wait(tmem + lane_off + L::kColDQ + 32u * wg, v);
         tc_fence_before_sync();
         mbar_arrive(bar_dq_free);
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) cross_scale2(v[i], v[i + 1], pend_us);
+        }
         if constexpr (kCross) {
           if (p.dq_out) {  // the row's only contribution: out as it is, 64 bytes
             if (32 * wg < D && pend_q0 + rr < p.N) {
@@ -801,6 +812,12 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       for (int h = 0; h < L::kHalves; ++h) tmem_ld32x32_wait(tDQ + 32u * h, v[h]);
       tc_fence_before_sync();
       mbar_arrive(bar_dq_free);
+      if constexpr (kScaled) {
+#pragma unroll
+        for (int h = 0; h < L::kHalves; ++h)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) cross_scale2(v[h][i], v[h][i + 1], pend_us);
+      }
       if constexpr (kCross) {
         if (p.dq_out) {
           // as above; this thread holds element rr of each query row, so a
@@ -878,6 +895,51 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         key_ok = key_row = key < p.N;
         key_rows = p.N;
       }
+      // P and dS are taken 2^e times as large: e, and 2^-e
+      [[maybe_unused]] float up = 0.f, us = 1.f;
+      if constexpr (kScaled) {
+        float most_do = 0.f, most_delta = 0.f;
+        const int n_range = p.Npad / kRangeRows;
+        const float2* const range = p.range + static_cast<size_t>(bh) * n_range;
+#pragma unroll 8
+        for (int i = threadIdx.x; i < n_range; i += kBwdComputeThreads) {
+          const float2 m = __ldg(range + i);
+          most_do = fmaxf(most_do, m.x);
+          most_delta = fmaxf(most_delta, m.y);
+        }
+        bool there = wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull);
+        there = __all_sync(0xffffffffu, there);
+        if (!there) {
+          ok = false;
+          break;
+        }
+        // (with one key V counts as zero, and its row is being made so)
+        const float most_v = key_ok && sg.n_keys > 1 ? cross_row_max<L::kPanels>(smem + L::kV, rr, wg) : 0.f;
+        uint4* const maxima = reinterpret_cast<uint4*>(smem + L::kRange) + (units & 1u) * 8;
+        const uint4 mine = make_uint4(__reduce_max_sync(0xffffffffu, __float_as_uint(most_do)),
+                                      __reduce_max_sync(0xffffffffu, __float_as_uint(most_v)),
+                                      __reduce_max_sync(0xffffffffu, __float_as_uint(most_delta)), 0u);
+        if (lane == 0) {
+          maxima[warp] = mine;
+          mbar_arrive(base + L::kRangeBar);
+        }
+        there = wait_bounded(base + L::kRangeBar, units & 1u, wd, kSiteBwdKvFull);
+        there = __all_sync(0xffffffffu, there);
+        if (!there) {
+          ok = false;
+          break;
+        }
+        uint4 m = maxima[0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) {
+          const uint4 o = maxima[w];
+          m = make_uint4(max(m.x, o.x), max(m.y, o.y), max(m.z, o.z), 0u);
+        }
+        const int e = cross_unit_shift(
+            fmaf(static_cast<float>(D) * __uint_as_float(m.x), __uint_as_float(m.y), __uint_as_float(m.z)));
+        up = static_cast<float>(e);
+        us = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      }
       for (int i = sg.i_begin; i < sg.i_end; ++i, ++g) {
         bool got = wait_bounded(bar_s_full, g & 1u, wd, kSiteBwdSFull);
         got = got && wait_bounded(bar_stage_full(slot), ph, wd, kSiteBwdStageFull);
@@ -910,8 +972,12 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           uint32_t pk[16], dk[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 nl = nl4[j / 4];
+            float4 nl = nl4[j / 4];
             const float4 dl = dl4[j / 4];
+            if constexpr (kScaled) {
+              fadd2_acc(nl.x, nl.y, up, up);
+              fadd2_acc(nl.z, nl.w, up, up);
+            }
             float e[4], pr[4], ds[4];
             ffma2(e[0], e[1], __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]), c, nl.x, nl.y);
             ffma2(e[2], e[3], __uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3]), c, nl.z, nl.w);
@@ -967,6 +1033,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           break;
         }
         pend_bh = bh;
+        if constexpr (kScaled) pend_us = us;
         pend_q0 = i * L::kSR;
         if (++slot == L::kStages) {
           slot = 0;
@@ -991,7 +1058,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       auto store_chunk = [&](int c, const float (&a)[32], const float (&b)[32]) {
         uint4* dvp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dv) + out_row + c * 64);
         uint4* dkp = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.dk) + out_row + c * 64);
-        const float sc = p.scale;
+        const float sc = kScaled ? p.scale * us : p.scale;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (kCross) {  // a row behind the keys: zero whatever dO and Q hold
@@ -1002,8 +1069,12 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           }
           const float* x = a + 8 * q;
           const float* y = b + 8 * q;
-          dvp[q] = make_uint4(pack2(x[0], x[1], kBf16), pack2(x[2], x[3], kBf16), pack2(x[4], x[5], kBf16),
-                              pack2(x[6], x[7], kBf16));
+          if constexpr (kScaled)
+            dvp[q] = make_uint4(pack2(x[0] * us, x[1] * us, kBf16), pack2(x[2] * us, x[3] * us, kBf16),
+                                pack2(x[4] * us, x[5] * us, kBf16), pack2(x[6] * us, x[7] * us, kBf16));
+          else
+            dvp[q] = make_uint4(pack2(x[0], x[1], kBf16), pack2(x[2], x[3], kBf16), pack2(x[4], x[5], kBf16),
+                                pack2(x[6], x[7], kBf16));
           dkp[q] = make_uint4(pack2(y[0] * sc, y[1] * sc, kBf16), pack2(y[2] * sc, y[3] * sc, kBf16),
                               pack2(y[4] * sc, y[5] * sc, kBf16), pack2(y[6] * sc, y[7] * sc, kBf16));
         }

@@ -230,6 +230,62 @@ __device__ __forceinline__ bool cross_bwd_next_segment(CrossCursor& c, CrossBwdS
   return false;
 }
 
+// fp16 in the backward. P and dS = P (dP - Delta) are rounded to 16 bits for
+// their products, and with P around 1 / Nk they soon lie among the subnormals,
+// below 2^-14, where a step is 2^-24 whatever the value: dO of 1e-3 and 8192
+// keys left 0.6 % of dQ and dK wrong, dO of 1e-4 5 %. So a unit (a K/V tile)
+// takes both 2^e times as large, by e in the exponent, and its fp32 sums 2^-e
+// times (exact). e is the largest, up to 14, that dS is sure to have room for:
+// |P| <= 1, |dP - Delta| <= D max |dO_id| max |V_jd| + max |Delta_i| over the
+// head's query rows and the tile's keys, and 2^e times that is at most 2^15,
+// half of what fp16 holds. (With normally distributed dO and V it is 2^7 times
+// the usual dP, so dS keeps its 11 bits to P = 2^-21.) A NaN is none of the
+// maxima; an infinity makes e 0.
+// The maxima of dO and Delta come from the prologue, which reads both anyway,
+// V's from the tile in shared memory. Measured (us, unscaled / scaled): 64
+// heads of 1000 rows over up to 1500 keys, D = 64, 72.0 / 75.3; 8 heads of 4096
+// rows x 8192 keys, D = 128, 313 / 325; 32 heads of 4096 rows x 77 keys, D = 64,
+// 36.9 / 37.1; 1024 heads of 128 rows x 257 keys, D = 64, 114 / 124 (units of
+// one step, where what a unit's start adds shows most). With one scale for a
+// head, V read by the prologue too: a second kernel that shifts -LSE * log2(e)
+// by e, 82.0 for the first of these; a cluster of blocks per head in the
+// prologue, 79.2 for the first and 172 for the last.
+__device__ __forceinline__ int cross_unit_shift(float bound) {
+  const float room = 32768.f / bound;  // 2 at least: an exponent of at least 1
+  return room >= 2.f ? min(static_cast<int>(__float_as_uint(room) >> 23) - 127, 14) : 0;
+}
+
+// Two fp32 values (their bits) times s.
+__device__ __forceinline__ void cross_scale2(uint32_t& a, uint32_t& b, float s) {
+  asm("{\n"
+      ".reg .b64 X, S;\n"
+      "mov.b64 X, {%0, %1};\n"
+      "mov.b64 S, {%2, %2};\n"
+      "mul.rn.f32x2 X, X, S;\n"
+      "mov.b64 {%0, %1}, X;\n"
+      "}\n"
+      : "+r"(a), "+r"(b)
+      : "f"(s));
+}
+
+// The largest absolute value in a thread's share of its row of the V tile (8 or
+// 4 of the row's 16-byte chunks, in an order that spreads the rows of a quarter
+// warp over the banks).
+template <int kPanels>
+__device__ __forceinline__ float cross_row_max(const uint8_t* tile, int row, int half) {
+  __half2 m = __half2half2(__ushort_as_half(0));
+#pragma unroll
+  for (int i = 0; i < 4 * kPanels; ++i) {
+    const int at = kPanels == 2 ? half * kPanelBytes + row * 128 + ((i ^ (row & 7)) << 4)
+                                : row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + at);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[k])));
+  }
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 // A K or V tile's rows [valid, 16-row boundary) in shared memory, zeroed by
 // one thread: what lies behind a batch entry's keys can be anything, and a
 // product of a zero weight with a NaN is a NaN. The products that contract

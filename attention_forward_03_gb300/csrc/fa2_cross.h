@@ -20,6 +20,7 @@ struct CrossParams : Params {  // N: query rows per key head; BH: B * Hkv
   int key_split;               // a unit's sub-tiles are its keys' (D <= 64, N <= 128)
 };
 
+constexpr int kRangeRows = 64;  // divides a step's rows
 struct CrossBwdParams : BwdParams {  // N: query rows per key head; nkv: K/V tiles of Nk keys
   int Nk;
   int B;
@@ -29,6 +30,10 @@ struct CrossBwdParams : BwdParams {  // N: query rows per key head; nkv: K/V til
   // only step, and goes out scaled and rounded ([B*Hkv, N, D]; NULL otherwise,
   // then it is added into dq_acc).
   void* dq_out;
+  // fp16: the largest |dO_id| and |Delta_i| of every kRangeRows query rows,
+  // [B*Hkv][Npad / kRangeRows], from which a unit's scale is taken
+  // (cross_unit_shift in fa2_cross.cuh).
+  const float2* range;
 };
 
 // Keys of batch entry b.

@@ -19,7 +19,7 @@ namespace fa2 {
 namespace {
 
 constexpr int kEndThreads = 256;
-constexpr int kStatRows = 64;   // query rows a block takes at a time (divides a step's rows)
+constexpr int kStatRows = kRangeRows;  // query rows a block takes at a time (divides a step's rows)
 constexpr int kZeroRows = 128;  // dK, dV rows a block writes zeros to at a time
 
 size_t round_up_256(size_t x) { return (x + 255) / 256 * 256; }
@@ -88,7 +88,8 @@ __device__ __forceinline__ float dot8_diff(const uint4& x, const uint4& v, const
 // Zeros also for what no unit writes: dK and dV of tiles wholly behind their
 // keys, and without an accumulator dQ of batch entries without keys. And the
 // flags of the partial results taken back, so that a replay of a captured
-// call, which carries the same tag, does not find them set.
+// call, which carries the same tag, does not find them set. In fp16 also what
+// a unit's scale is taken from (cross_unit_shift), into `range`.
 // A block takes 64 rows of a head at a time, D/8 threads of 16 bytes per row
 // in groups of a power of two, all loads of a pass before its sums.
 template <int D, bool kBf16>
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
                                                                       const uint4* __restrict__ V,
                                                                       const float* __restrict__ LSE, float* neg_lse2,
                                                                       float* delta, uint4* dk, uint4* dv,
-                                                                      const CrossBwdParams p) {
+                                                                      float2* range, const CrossBwdParams p) {
   constexpr int kPer = D / 8;
   constexpr int kLanes = kPer <= 4 ? 4 : (kPer <= 8 ? 8 : 16);
   constexpr int kPasses = kStatRows * kLanes / kEndThreads;
@@ -122,6 +123,8 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
       }
     }
     const uint4 v0 = one_key && part < kPer ? V[static_cast<size_t>(bh) * p.Nk * kPer + part] : z;
+    [[maybe_unused]] __half2 most_do = __half2half2(__ushort_as_half(0));
+    [[maybe_unused]] float most_delta = 0.f;
 #pragma unroll
     for (int s = 0; s < kPasses; ++s) {
       const int r = r0 + s * (kEndThreads / kLanes);
@@ -133,11 +136,32 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_prologue(const uint
       float d = one_key ? dot8_diff(x[s], v0, g[s], kBf16) : dot8(x[s], g[s], kBf16);
 #pragma unroll
       for (int off = kLanes / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off, kLanes);
+      if constexpr (!kBf16) {
+        const uint32_t w[4] = {g[s].x, g[s].y, g[s].z, g[s].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most_do = __hmax2(most_do, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+        if (r < p.N) most_delta = fmaxf(most_delta, fabsf(d));
+      }
       if (part == 0) {
         const size_t at = static_cast<size_t>(bh) * p.Npad + r;
         delta[at] = r < p.N ? d : 0.f;
         neg_lse2[at] = r < p.N ? -(LSE[head + r] * 1.4426950408889634f) : -CUDART_INF_F;
       }
+    }
+    if constexpr (!kBf16) {
+      __shared__ uint2 warps[kEndThreads / 32];
+      const float m = fmaxf(__low2float(most_do), __high2float(most_do));
+      const uint2 mine = make_uint2(__reduce_max_sync(0xffffffffu, __float_as_uint(m)),
+                                    __reduce_max_sync(0xffffffffu, __float_as_uint(most_delta)));
+      if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = mine;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        uint2 all = mine;
+#pragma unroll
+        for (int w = 1; w < kEndThreads / 32; ++w) all = make_uint2(max(all.x, warps[w].x), max(all.y, warps[w].y));
+        range[it] = make_float2(__uint_as_float(all.x), __uint_as_float(all.y));
+      }
+      __syncthreads();
     }
   }
   if (p.ws_flags && blockIdx.x == 0 && threadIdx.x < kBwdMaxCtas) p.ws_flags[threadIdx.x] = 0ull;
@@ -176,13 +200,14 @@ __global__ void __launch_bounds__(kEndThreads) fa2_cross_bwd_finish(const float4
 
 template <int D>
 cudaError_t launch_prologue(bool bf, const void* O, const void* dO, const void* V, const float* LSE, float* neg_lse2,
-                            float* delta, void* dK, void* dV, const CrossBwdParams& p, int sms, cudaStream_t s) {
+                            float* delta, void* dK, void* dV, float2* range, const CrossBwdParams& p, int sms,
+                            cudaStream_t s) {
   const long long items = static_cast<long long>(p.BH) * (p.Npad / kStatRows);
   const int grid = static_cast<int>(std::min<long long>(items, 8ll * sms));
   auto kern = bf ? fa2_cross_bwd_prologue<D, true> : fa2_cross_bwd_prologue<D, false>;
   kern<<<grid, kEndThreads, 0, s>>>(static_cast<const uint4*>(O), static_cast<const uint4*>(dO),
                                     static_cast<const uint4*>(V), LSE, neg_lse2, delta, static_cast<uint4*>(dK),
-                                    static_cast<uint4*>(dV), p);
+                                    static_cast<uint4*>(dV), range, p);
   return cudaGetLastError();
 }
 
@@ -353,15 +378,21 @@ extern "C" int fa2_cross_bwd(const void* Q, const void* K, const void* V, const 
     p.ws_flags = reinterpret_cast<unsigned long long*>(ws + wl.dq_bytes + 2 * wl.stat_bytes + wl.part_bytes);
     p.epoch = next_launch_epoch();
   }
+  // fp16's maxima, one float2 per 64 rows, lie where nothing is written before
+  // the main kernel has ended: in dQ, or, where that kernel writes dQ itself, in
+  // the accumulator that it then has no use for (both hold at least 64 bytes per row).
+  float2* range = static_cast<float2*>(dQ);
   if (Nk <= kBwdKeys) {
+    range = reinterpret_cast<float2*>(dq_acc);
     p.dq_out = dQ;
     p.dq_acc = nullptr;
   }
+  p.range = range;
   switch (D) {
-    case 32: e = launch_prologue<32>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
-    case 64: e = launch_prologue<64>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
-    case 96: e = launch_prologue<96>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
-    default: e = launch_prologue<128>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, p, sms, s); break;
+    case 32: e = launch_prologue<32>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, range, p, sms, s); break;
+    case 64: e = launch_prologue<64>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, range, p, sms, s); break;
+    case 96: e = launch_prologue<96>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, range, p, sms, s); break;
+    default: e = launch_prologue<128>(bf, O, dO, V, LSE, neg_lse2, delta, dK, dV, range, p, sms, s); break;
   }
   if (e != cudaSuccess) return record_cuda_error(e);
   e = pick_cross_bwd(D, bf)(mk, mv, mq, mdo, mdq, p, grid, s);

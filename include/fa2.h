@@ -503,8 +503,12 @@ FA2_API int fa2_cross_fwd_workspace_bytes(int D, size_t* bytes);
  * Every gradient is fully overwritten, rounded to nearest-even, and overlaps
  * nothing. dQ is summed with fp32 atomic adds in no fixed order (up to Nk =
  * 128 there is one term per row and no sum); dK and dV are summed in a fixed
- * one. The other arguments and the errors are
- * fa2_cross_fwd's, with FA2_ERR_INVALID_ARG for a missing workspace.
+ * one. P and dS are rounded to `dtype` for their products; in fp16 both are
+ * scaled before that by a power of two, chosen from the sizes of dO, O and V,
+ * so that a small dO or many keys do not leave them among the subnormals
+ * (fa2_bwd rounds them as they are). dQ may hold scratch until the call is
+ * done. The other arguments and the errors are fa2_cross_fwd's, with
+ * FA2_ERR_INVALID_ARG for a missing workspace.
  */
 FA2_API int fa2_cross_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
                           const float* LSE, void* dQ, void* dK, void* dV, const int* key_lengths, int B, int Hq,
