@@ -308,10 +308,9 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
   using L = BwdLayout<D>;
   using Seg = std::conditional_t<kCross, CrossBwdSegment, BwdSegment>;
   constexpr bool kScaled = kCross && !kBf16;
-  constexpr bool kTwoIssuers = true;
   constexpr bool kATmem = L::kGradATmem;  // dS^T in TMEM for dK (P^T is there for dV at every D)
   constexpr bool kDqWarp = bwd_threads(D) > 352;  // staged dQ^T added by warp kBwdDqWarp
-  constexpr uint32_t kReaders = kTwoIssuers ? 2 : 1;  // issuer threads reading a ring slot and K/V
+  constexpr uint32_t kReaders = 2;  // issuer threads reading a ring slot and K/V
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -468,7 +467,10 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
       if (units > 0) wait_bounded(bar_kv_full, (units - 1) & 1u, wd, kSiteBwdDrain, false, kNapNs);
     }
     __syncwarp();
-  } else if (warp == kBwdMmaWarp || (kTwoIssuers && warp == kBwdGradWarp)) {
+  } else if (warp >= kBwdMmaWarp && warp <= kBwdGradWarp) {
+    // (The range, not `== kBwdMmaWarp || == kBwdGradWarp`: with that the
+    // compiler's code for cross attention in bf16 at D = 128 took 348 us
+    // instead of 310, 8 heads of 4096 rows x 8192 keys.)
     // The issuers poll their barriers without sleeping: each step is a chain
     // of hand-offs between them and the compute warpgroups, and a sleeping
     // waiter wakes late (measured: 0 to +2.3 % across the backward workloads).
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         for (int kk = 0; kk < kBwdKeys / 16; ++kk) one(kk);
       };
 
-      if constexpr (kTwoIssuers) {
+      {
         // Two issuers walk the same step sequence: warp 8 the scores, warp 9
         // the gradients. Each releases a ring slot and K/V after its own
         // MMAs that read them (a commit tracks only its thread's MMAs).
@@ -621,81 +623,6 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
           }
           if (!ok) break;
           if (!scores) mma_commit(bar_acc_full);
-          mma_commit(bar_kv_empty);
-          ++units;
-        }
-      } else {
-        int slot = 0;
-        uint32_t ph = 0;
-        uint32_t g = 0;      // global query-step counter of this CTA
-        uint32_t units = 0;
-        bool ok = true;
-        // Takes the next ring slot (Q_i, dO_i loaded) and, once the compute
-        // threads hold the previous step's S^T / dP^T, issues this step's.
-        auto start_step = [&](uint32_t step) -> int {
-          const int s = slot;
-          if (!wait_bounded(bar_stage_full(s), ph, wd, kSiteBwdStageFull, true, 0u)) return -1;
-          if (step > 0 && !wait_bounded(bar_s_free, (step - 1) & 1u, wd, kSiteBwdSFree, true, 0u)) return -1;
-          tc_fence_after_sync();
-          issue_sdp(s);
-          mma_commit(bar_s_full);
-          if (++slot == L::kStages) {
-            slot = 0;
-            ph ^= 1u;
-          }
-          return s;
-        };
-        auto wcur = first_segment_cursor();
-        Seg sg;
-        while (ok && advance(wcur, sg)) {
-          const int n_steps = sg.i_end - sg.i_begin;
-          int key_steps = kBwdKeys / 16;  // 16-key steps of the tile with keys
-          if constexpr (kCross) key_steps = cross_key_steps(sg.n_keys - sg.kv * kBwdKeys);
-          if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
-            ok = false;
-            break;
-          }
-          int cur = start_step(g);
-          if (cur < 0) {
-            ok = false;
-            break;
-          }
-          for (int t = 0; t < n_steps; ++t, ++g) {
-            // the next step's scores first: the tensor core computes them
-            // while the compute threads form P^T and dS^T of this one
-            int nxt = -1;
-            if (t + 1 < n_steps) {
-              nxt = start_step(g + 1);
-              if (nxt < 0) {
-                ok = false;
-                break;
-              }
-            }
-            if (!wait_bounded(bar_p_full, g & 1u, wd, kSiteBwdPFull, true, 0u)) {
-              ok = false;
-              break;
-            }
-            // the unit's first accumulation overwrites dV / dK: the previous
-            // unit's epilogue must have loaded them
-            if (t == 0 && units > 0 && !wait_bounded(bar_acc_free, (units - 1) & 1u, wd, kSiteBwdAccFree, true, 0u)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            issue_grads(cur, t > 0);
-            mma_commit(bar_stage_empty(cur));
-            if (g > 0 && !wait_bounded(bar_dq_free, (g - 1) & 1u, wd, kSiteBwdDqFree, true, 0u)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            issue_dq(key_steps);
-            mma_commit(bar_p_free);
-            mma_commit(bar_dq_full);
-            cur = nxt;
-          }
-          if (!ok) break;
-          mma_commit(bar_acc_full);
           mma_commit(bar_kv_empty);
           ++units;
         }
