@@ -42,39 +42,6 @@ __device__ __forceinline__ int cross_keys(const P& p, int b) {
   return p.key_lengths ? min(max(__ldg(p.key_lengths + b), 0), p.Nk) : p.Nk;
 }
 
-// What cutting units costs, in steps of the busiest SM: cutting them at all
-// (the flags, the way through memory), every result that a unit's first holder
-// joins to its own, and shares that do not end where units do (then a CTA
-// works on parts of two units).
-struct CutCosts {
-  double cut, join, uneven;
-};
-
-// Fewer units than SMs: how many CTAs share their steps equally, or 0 for
-// whole units. The first holder of a unit joins the other holders' results one
-// after another, so more CTAs are not always faster. Tried are whole parts per
-// unit and all SMs. With key counts on the device (`lengths`) the longest unit
-// is taken to have `unit_steps` steps and the mean 0.6 of them, as with evenly
-// spread counts; shares then end where they may, and every second one in a
-// unit of its own.
-inline int cross_cut_ctas(long long units, long long unit_steps, bool lengths, int sms, const CutCosts& c) {
-  double best = 0.95 * static_cast<double>(unit_steps);
-  int ctas = 0;
-  const auto consider = [&](long long n, long long joins, double uneven) {
-    const double share = lengths ? 0.6 * static_cast<double>(units * unit_steps) / static_cast<double>(n)
-                                 : static_cast<double>((units * unit_steps + n - 1) / n);
-    const double cost = share + c.cut + c.join * static_cast<double>(joins) + uneven;
-    if (cost < best) {
-      best = cost;
-      ctas = static_cast<int>(n);
-    }
-  };
-  for (long long parts = 2; parts <= unit_steps && parts * units <= sms; ++parts)
-    consider(parts * units, lengths ? parts : parts - 1, lengths ? 0.5 * c.uneven : 0.0);
-  if (units * unit_steps > sms) consider(sms, (sms + units - 1) / units, lengths ? 0.5 * c.uneven : c.uneven);
-  return ctas;
-}
-
 // The forward on the tensor-core kernel of fa2_kernel.cuh.
 template <int D, bool kBf16>
 cudaError_t launch_cross_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,

@@ -10,6 +10,7 @@
 
 #include "fa2.h"
 #include "fa2_cross.h"
+#include "fa2_cross_schedule.h"
 
 namespace fa2 {
 namespace {
@@ -33,49 +34,6 @@ CrossFn pick_cross(int d, bool bf) {
     case 96: return bf ? launch_cross_fwd<96, true> : launch_cross_fwd<96, false>;
     default: return bf ? launch_cross_fwd<128, true> : launch_cross_fwd<128, false>;
   }
-}
-
-// Whether a unit's two sub-tiles take its key tiles in turn (fa2_kernel.cuh):
-// with at most 128 rows per key head there is no second sub-tile of rows, and
-// from 5 key tiles on the overlap is worth the joining of the two (us, with /
-// without, 1024 such heads, D = 64: 300 keys 46.4 / 42.5, 512 keys 43.1 /
-// 43.9, 768 keys 54.0 / 59.0, 4096 keys 177 / 238; 8 heads, in the best number
-// of parts, 4068 keys 16.3 / 18.3). Above D = 64 the tensor cores have more to
-// do and the gain is below a tenth (1 head per SM, 16384 keys, D = 128: 114 /
-// 131; 256 heads of 4096 keys 91.5 / 94.7), the loss at 257 keys as large.
-bool split_keys(int D, long long rows, long long nkv) { return D <= 64 && rows <= kRows && nkv > 4; }
-
-// How many CTAs share the K/V-tile steps equally, with a merge of the units
-// that they cut, or 0 for whole units in rounds.
-//
-// At least one unit per SM: equal shares when that saves the busiest SM 5 %
-// with what the cuts cost, in steps 5, 7 above D = 64, 12 with split keys.
-// With key counts on the device the host cannot know the units; then from as
-// many tiles on as measured to pay on evenly spread counts (us, whole / equal;
-// 192 and 1024 units): D = 64, 256 rows: 4 tiles 17.8 / 18.8 and 53.2 / 58.6, 6
-// tiles 22.3 / 21.1 and 67.0 / 65.8, 32 tiles 63.3 / 44.1 and 211 / 167; D =
-// 128, 128 rows: 8 tiles 23.9 / 24.0 and 76.0 / 86.7, 12 tiles 31.8 / 28.0 and
-// 100 / 99.2; split keys: 16 tiles 26.8 / 27.2 and 77.8 / 104, 32 tiles 42.3 /
-// 38.5 and 130 / 143.
-//
-// Fewer: cross_cut_ctas, in steps of about 1 us, 0.65 us with split keys.
-// Measured (us, by the parts per unit; 1: not cut, * the choice), 128 rows: D =
-// 64, 8 heads: 500 keys 1* 9.1, 2 11.2; 1508 keys 1* 13.3, 4 14.4, 12 20.8; 4068
-// keys 1 27.2, 4* 16.3, 8 17.7, 19 24.8; 16,356 keys 1 90.6, 8 26.1, 10* 26, 19
-// 28.8; 32 heads of 16,356 keys 4* 35.0, all SMs 40.0; 96
-// heads of 256 rows over up to 4096 keys 1 44.5, all SMs* 30.2. D = 128, 8 heads: 500
-// keys 1* 10.8, 2 12.3; 1508 keys 1* 18.6, 3 19.7, 4 16.9, 12 28.2; 4068 keys 1
-// 37.9, 4* 22.8, 8 25.3, 19 34.5.
-int cross_share_ctas(int D, bool split, long long units, long long nkv, bool lengths, int sms) {
-  if (units < sms) {
-    const CutCosts c = split ? CutCosts{4.6, 1.3, 12.0} : D <= 64 ? CutCosts{5.8, 0.6, 3.0} : CutCosts{5.0, 1.25, 4.0};
-    return cross_cut_ctas(units, nkv, lengths, sms, c);
-  }
-  const double per_sm = static_cast<double>(units) / sms;
-  if (lengths) return static_cast<double>(nkv) >= (split ? 16.0 + 5.0 * per_sm : D <= 64 ? 6.0 : 12.0) ? sms : 0;
-  const double rounds = static_cast<double>((units + sms - 1) / sms) * static_cast<double>(nkv);
-  const double balanced = per_sm * static_cast<double>(nkv) + (split ? 12.0 : D <= 64 ? 5.0 : 7.0);
-  return balanced < 0.95 * rounds ? sms : 0;
 }
 
 // What a unit counts in the equal shares besides its tiles: the tensor cores
@@ -183,6 +141,18 @@ extern "C" int fa2_cross_fwd(const void* Q, const void* K, const void* V, void* 
   p.heads = Hkv;
   p.key_lengths = key_lengths;
   char* const ws = static_cast<char*>(workspace);
+  // At most 16 rows (what its products hold): the rows kernel. Measured (us,
+  // rows kernel / tcgen05; the latter takes as long for 17 rows as for 16): 16
+  // rows, D = 64: 8 heads of 300 keys 8.4 / 8.2, 1500 9.5 / 14.2, 16,384 15.4 /
+  // 26.4; 48 heads 8.5 / 8.1, 11.7 / 15.0, 39.1 / 42.6; 512 heads of 300 keys
+  // 21.1 / 24.6, 4096 89.7 / 96.2. D = 128: 8 heads of 300 keys 10.2 / 9.4, 1500
+  // 12.1 / 18.1, 16,384 20.9 / 39.6; 48 heads 10.9 / 9.6, 16.6 / 18.4, 69.6 /
+  // 73.3; 512 heads of 300 keys 27.9 / 29.7, 4096 172 / 172. One row is up to 20 %
+  // faster than 16 on the rows kernel, the same on the other. Over at most 128
+  // keys the few-keys kernel would be as fast or faster, which this rule leaves
+  // aside (us, rows / few keys, 1 row): D = 64, 8 heads of 77 keys 4.6 / 4.2, 512
+  // heads of 32 keys 9.0 / 4.0, 128 keys 10.2 / 8.4; D = 128, 8 heads of 128 keys
+  // 5.1 / 5.5, 512 heads of 32 keys 10.2 / 6.6, 128 keys 13.3 / 13.1.
   if (workspace && rows <= kFewRows) {
     const int grid = static_cast<int>(
         std::min<long long>(std::min(sms, kFewRowsMaxCtas), bh * ((static_cast<long long>(Nk) + kFewRowsKeys - 1) / kFewRowsKeys)));

@@ -14,6 +14,7 @@
 
 #include "fa2.h"
 #include "fa2_cross.h"
+#include "fa2_cross_schedule.h"
 
 namespace fa2 {
 namespace {
@@ -221,37 +222,6 @@ CrossBwdFn pick_cross_bwd(int d, bool bf) {
     case 96: return bf ? launch_cross_bwd<96, true> : launch_cross_bwd<96, false>;
     default: return bf ? launch_cross_bwd<128, true> : launch_cross_bwd<128, false>;
   }
-}
-
-// How many CTAs share all query steps equally, with a merge of the units that
-// they cut, or 0 for whole units in rounds.
-//
-// At least one unit per SM: when that saves the busiest SM at least 5 %, with
-// 2 steps for a cut unit's partial results. With key counts on the device and
-// more than one key tile per head always, as the shares follow the counts (us,
-// equal shares / whole units: 64 heads of 1024 rows over up to 1500 keys, D =
-// 64 73.5 / 98.8, D = 128 115 / 156; 64 rows 28.7 / 35.6; but 1024 heads over
-// up to 100 keys, one tile each, 256 rows 75.4 / 68.4). In rounds the key
-// tiles of a head run at the same time and share its Q, dO and dQ; where those
-// are more than the L2 cache holds, equal shares have to save a quarter (256
-// heads of 2048 rows x 257 keys, D = 128: 545 us equal, 418 whole; D = 64 266
-// and 250).
-//
-// Fewer: cross_cut_ctas. Measured (us, by the parts per unit; 1: not cut, *
-// the choice): 8 heads over 77 keys, D = 64: 256 rows 1* 10.7, 2 12.7; 1024
-// rows 1 21.3, 4* 16.3, 12 18.7; 4096 rows 1 62.5, 8* 24.5, 19 26.9; 16,384
-// rows 1 231, 8 51.7, 16* 41.8, 19 42.8. D = 128: 256 rows 1* 14.8, 4 18.9;
-// 1024 rows 1 29.8, 4* 22.7, 12 33.3; 4096 rows 1 93.3, 6 38.1, 8* 37.6, 19
-// 43.4; 16,384 rows 1 348, 12 74.7, 19 70.1.
-int cross_bwd_share_ctas(int D, long long units, long long nq, bool lengths, long long q_bytes, int sms) {
-  if (units >= sms) {
-    constexpr long long kSplitCostSteps = 2;
-    const long long rounds = (units + sms - 1) / sms * nq;
-    constexpr long long kL2Bytes = 128ll << 20;
-    const int most = q_bytes > kL2Bytes ? 75 : 95;  // percent of the rounds
-    return lengths || 100 * ((units * nq + sms - 1) / sms + kSplitCostSteps) < most * rounds ? sms : 0;
-  }
-  return cross_cut_ctas(units, nq, lengths, sms, D <= 64 ? CutCosts{1.5, 0.6, 2.0} : CutCosts{2.3, 1.0, 10.0});
 }
 
 }  // namespace
