@@ -550,8 +550,10 @@ __global__ void __launch_bounds__(kThreadsNr, kPairs == 1 ? 2 : 1)
 
 // d gain = the sum of the blocks' partials: 32 interleaved runs of blocks, each
 // in block order, then the runs in theirs, the same order on every launch. One
-// block per 32 elements and side. Launched while the backward still runs
-// (programmatic dependent launch); it waits for it here.
+// block per 32 elements and side. Launched as a programmatic dependent of the
+// backward, which never triggers it: its blocks may start when the last of the
+// backward's has exited, so that only the launch itself overlaps, and wait
+// here until the partials are visible.
 constexpr int kGainRuns = 32;
 __global__ void __launch_bounds__(32 * kGainRuns) fa2_norm_rope_gain_kernel(const float* partials, void* dq_gain,
                                                                             void* dk_gain, int q_blocks, int blocks,
