@@ -554,78 +554,76 @@ __global__ void __launch_bounds__(bwd_threads(D), 1)
         for (int kk = 0; kk < kBwdKeys / 16; ++kk) one(kk);
       };
 
-      {
-        // Two issuers walk the same step sequence: warp 8 the scores, warp 9
-        // the gradients. Each releases a ring slot and K/V after its own
-        // MMAs that read them (a commit tracks only its thread's MMAs).
-        const bool scores = warp == kBwdMmaWarp;
-        int slot = 0;
-        uint32_t ph = 0;
-        uint32_t g = 0;
-        uint32_t units = 0;
-        bool ok = true;
-        auto cur = first_segment_cursor();
-        Seg sg;
-        while (ok && advance(cur, sg)) {
-          const int n_steps = sg.i_end - sg.i_begin;
-          int key_steps = kBwdKeys / 16;  // 16-key steps of the tile with keys
-          if constexpr (kCross) key_steps = cross_key_steps(sg.n_keys - sg.kv * kBwdKeys);
-          if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
+      // Two issuers walk the same step sequence: warp 8 the scores, warp 9
+      // the gradients. Each releases a ring slot and K/V after its own
+      // MMAs that read them (a commit tracks only its thread's MMAs).
+      const bool scores = warp == kBwdMmaWarp;
+      int slot = 0;
+      uint32_t ph = 0;
+      uint32_t g = 0;
+      uint32_t units = 0;
+      bool ok = true;
+      auto cur = first_segment_cursor();
+      Seg sg;
+      while (ok && advance(cur, sg)) {
+        const int n_steps = sg.i_end - sg.i_begin;
+        int key_steps = kBwdKeys / 16;  // 16-key steps of the tile with keys
+        if constexpr (kCross) key_steps = cross_key_steps(sg.n_keys - sg.kv * kBwdKeys);
+        if (!wait_bounded(bar_kv_full, units & 1u, wd, kSiteBwdKvFull, true, 0u)) {
+          ok = false;
+          break;
+        }
+        if constexpr (kCross) {
+          if (scores && sg.n_keys < p.Nk && sg.n_keys - sg.kv * kBwdKeys < kBwdKeys)
+            cross_zero_rows(sK, L::kPanels, sg.n_keys - sg.kv * kBwdKeys);
+          // one key: the prologue's Delta is <dO, O - V> already, so dP is 0
+          if (scores && sg.n_keys == 1) cross_zero_rows(sV, L::kPanels, 0);
+        }
+        for (int t = 0; t < n_steps; ++t, ++g) {
+          if (!wait_bounded(bar_stage_full(slot), ph, wd, kSiteBwdStageFull, true, 0u)) {
             ok = false;
             break;
           }
-          if constexpr (kCross) {
-            if (scores && sg.n_keys < p.Nk && sg.n_keys - sg.kv * kBwdKeys < kBwdKeys)
-              cross_zero_rows(sK, L::kPanels, sg.n_keys - sg.kv * kBwdKeys);
-            // one key: the prologue's Delta is <dO, O - V> already, so dP is 0
-            if (scores && sg.n_keys == 1) cross_zero_rows(sV, L::kPanels, 0);
-          }
-          for (int t = 0; t < n_steps; ++t, ++g) {
-            if (!wait_bounded(bar_stage_full(slot), ph, wd, kSiteBwdStageFull, true, 0u)) {
+          if (scores) {
+            if (g > 0 && !wait_bounded(bar_s_free, (g - 1) & 1u, wd, kSiteBwdSFree, true, 0u)) {
               ok = false;
               break;
             }
-            if (scores) {
-              if (g > 0 && !wait_bounded(bar_s_free, (g - 1) & 1u, wd, kSiteBwdSFree, true, 0u)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              issue_sdp(slot);
-              mma_commit(bar_s_full);
-              mma_commit(bar_stage_empty(slot));
-            } else {
-              if (!wait_bounded(bar_p_full, g & 1u, wd, kSiteBwdPFull, true, 0u)) {
-                ok = false;
-                break;
-              }
-              if (t == 0 && units > 0 &&
-                  !wait_bounded(bar_acc_free, (units - 1) & 1u, wd, kSiteBwdAccFree, true, 0u)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              issue_grads(slot, t > 0);
-              mma_commit(bar_stage_empty(slot));
-              if (g > 0 && !wait_bounded(bar_dq_free, (g - 1) & 1u, wd, kSiteBwdDqFree, true, 0u)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              issue_dq(key_steps);
-              mma_commit(bar_p_free);
-              mma_commit(bar_dq_full);
+            tc_fence_after_sync();
+            issue_sdp(slot);
+            mma_commit(bar_s_full);
+            mma_commit(bar_stage_empty(slot));
+          } else {
+            if (!wait_bounded(bar_p_full, g & 1u, wd, kSiteBwdPFull, true, 0u)) {
+              ok = false;
+              break;
             }
-            if (++slot == L::kStages) {
-              slot = 0;
-              ph ^= 1u;
+            if (t == 0 && units > 0 &&
+                !wait_bounded(bar_acc_free, (units - 1) & 1u, wd, kSiteBwdAccFree, true, 0u)) {
+              ok = false;
+              break;
             }
+            tc_fence_after_sync();
+            issue_grads(slot, t > 0);
+            mma_commit(bar_stage_empty(slot));
+            if (g > 0 && !wait_bounded(bar_dq_free, (g - 1) & 1u, wd, kSiteBwdDqFree, true, 0u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            issue_dq(key_steps);
+            mma_commit(bar_p_free);
+            mma_commit(bar_dq_full);
           }
-          if (!ok) break;
-          if (!scores) mma_commit(bar_acc_full);
-          mma_commit(bar_kv_empty);
-          ++units;
+          if (++slot == L::kStages) {
+            slot = 0;
+            ph ^= 1u;
+          }
         }
+        if (!ok) break;
+        if (!scores) mma_commit(bar_acc_full);
+        mma_commit(bar_kv_empty);
+        ++units;
       }
       // Drain: the CTA must not exit (or free TMEM) with MMAs in flight.
       const uint32_t drain = warp == kBwdMmaWarp ? bar_drain : bar_drain2;
