@@ -8,6 +8,11 @@
     O, LSE = cross_attention_forward(q, k, v, key_lengths=n)      # keys of another length
     dQ, dK, dV = cross_attention_backward(q, k, v, O, LSE, dO, key_lengths=n)
 
+    paged_cache_append(k, v, k_cache, v_cache, table, n)          # serving: keys and values in pages
+    O, LSE = paged_attention_forward(q, k_cache, v_cache, table, n)
+    w = paged_key_weights(q, LSE, k_cache, table, n, weights=w)   # which cached keys matter ...
+    n, kept = paged_cache_evict(k_cache, v_cache, w, table, n, new_table, keep)  # ... and stay
+
 The compute runs in libfa2_gb300.so (build it with
 ``attention_forward_03_gb300.build.build()``); the binding fails loudly if it
 is missing.
@@ -24,4 +29,7 @@ from .cross import (  # noqa: F401
 )
 from .norm_rope import (  # noqa: F401
     fa2_qk_norm_rope_bwd_workspace_bytes, qk_norm_rope_backward, qk_norm_rope_forward,
+)
+from .paged import (  # noqa: F401
+    fa2_paged_fwd_workspace_bytes, paged_attention_forward, paged_cache_append, paged_cache_evict, paged_key_weights,
 )

@@ -524,6 +524,151 @@ FA2_API int fa2_cross_bwd(const void* Q, const void* K, const void* V, const voi
 FA2_API int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D, size_t* bytes);
 
 /*
+ * The paged key/value cache. Keys and values of many sequences lie in the
+ * pages of two caches; the four calls below write a batch's new tokens into
+ * them, attend over them, add up what each cached key weighs, and cut the
+ * sequences down to the keys that weigh most. The pages (the documents this
+ * library follows elsewhere) have no counterpart to them. All share:
+ *
+ * k_cache, v_cache: device pointers, [pages, Hkv, page_size, D] views of
+ *             `dtype` with the strides below, 16-byte aligned. page_size is
+ *             16, 32, 64, 128 or 256. The two may interleave.
+ * block_table : device pointer, [B, max_pages] int32, rows a stride apart:
+ *             position p of sequence b is slot p % page_size of page
+ *             block_table[b][p / page_size]. Entries behind a sequence's last
+ *             page are not used. A page number outside [0, pages) touches no
+ *             memory; each call says what its positions count as.
+ * key_lengths : device pointer, [B] int32: the sequences' positions, the
+ *             call's new tokens included (values outside [0, max_pages *
+ *             page_size] count as the nearer end).
+ * query_starts: device pointer, [B + 1] int32, ascending: sequence b's new
+ *             tokens are the rows query_starts[b] .. query_starts[b + 1] - 1 of
+ *             the T tokens, and stand at its last positions (of more tokens
+ *             than positions the first ones have none). NULL: every sequence
+ *             has T / B tokens (T is a multiple of B then).
+ * strides   : HOST pointer to element strides, listed with each call.
+ *             Strides of dimensions longer than 1 are multiples of 8 (the
+ *             tables': any), not negative, those of the caches positive and
+ *             below 2^39; no view reaches further than 2^44 elements.
+ * T, B, Hq, Hkv: sizes >= 0, Hq a multiple of Hkv.
+ *             max_pages * page_size, T and T * Hq / Hkv are at most 2^30.
+ * D         : 32, 64, 96 or 128.
+ * scale, dtype, stream: as fa2_fwd.
+ * The tables, lengths and starts do not change while a call runs; what they
+ * hold is bounded where it is read. Asynchronous and allocation-free as
+ * fa2_fwd. Errors as fa2_fwd, FA2_ERR_UNSUPPORTED also for the page size.
+ */
+
+/*
+ * fa2_paged_append — the new tokens' keys and values into their positions.
+ *
+ * K, V      : device pointers, [T, Hkv, D] views of `dtype`, 16-byte aligned;
+ *             they and the tables overlap neither cache.
+ * weights   : device pointer, contiguous [pages, Hkv, page_size] fp32, or NULL:
+ *             the written positions' weights (fa2_paged_key_weights) become 0.
+ * strides   : K token, head; V token, head; k_cache page, head, slot; v_cache
+ *             page, head, slot; block_table row (11).
+ * Tokens without a position and those whose page number is not one are not
+ * written. No two tokens have one position.
+ */
+FA2_API int fa2_paged_append(const void* K, const void* V, void* k_cache, void* v_cache, float* weights,
+                             const int* block_table, const int* key_lengths, const int* query_starts,
+                             const long long* strides, int T, int B, int Hkv, int D, int pages, int page_size,
+                             int max_pages, int dtype, struct CUstream_st* stream);
+
+/*
+ * fa2_paged_fwd — attention of the new tokens over their sequences' positions:
+ *   O[t,h,:] = softmax_p(scale <Q[t,h,:], K_p>) V_p,  LSE[t,h] = ln sum_p exp(...)
+ *   over the positions p of token t's sequence, with is_causal those up to
+ *   t's own, of key head h / (Hq / Hkv).
+ * A row without any position gives O = 0 and LSE = +inf, as in fa2_cross_fwd;
+ * one with a NaN or +inf score, or that sees a position whose page number is
+ * not one, NaN. Rows of O and LSE that are no sequence's tokens are left as
+ * they were. What lies behind a sequence's positions is never used; a NaN or
+ * an infinity in V at one of them may reach every new token of the sequence,
+ * those before it too (a zero weight times a NaN).
+ *
+ * Q         : device pointer, [T, Hq, D] view of `dtype`, 16-byte aligned.
+ * O, LSE    : device pointers, contiguous [T, Hq, D] of `dtype` (16-byte
+ *             aligned) and [T, Hq] fp32. They and the workspace overlap neither
+ *             an input (from a cache's first element to its last) nor each other.
+ * strides   : Q token, head; k_cache page, head, slot; v_cache page, head,
+ *             slot; block_table row (9).
+ * max_query_length: the most new tokens that a sequence has, or any larger
+ *             number (T). Kernels are chosen by it; the results do not depend
+ *             on its being right.
+ * workspace : device memory of at least fa2_paged_fwd_workspace_bytes(D)
+ *             bytes, 16-byte aligned; scratch, needs no initialisation, not
+ *             shared by calls that run at the same time. A captured call can
+ *             be replayed, also after the tables' contents changed; the
+ *             replays share the workspace. (After a timeout that
+ *             fa2_device_status reports, the call is captured anew.)
+ * pages and max_pages are at least 1 where there is a token.
+ */
+FA2_API int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_cache, void* O, float* LSE,
+                          const int* block_table, const int* key_lengths, const int* query_starts,
+                          const long long* strides, int T, int B, int Hq, int Hkv, int D, int pages, int page_size,
+                          int max_pages, int max_query_length, float scale, int is_causal, int dtype, void* workspace,
+                          size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * fa2_paged_fwd_workspace_bytes — bytes of device workspace fa2_paged_fwd
+ * takes on the current device for head dimension D, whatever the other sizes.
+ * Returns FA2_OK, FA2_ERR_INVALID_ARG (bytes NULL), FA2_ERR_UNSUPPORTED or
+ * FA2_ERR_CUDA.
+ */
+FA2_API int fa2_paged_fwd_workspace_bytes(int D, size_t* bytes);
+
+/*
+ * fa2_paged_key_weights — what every cached key weighs in the new tokens'
+ * softmax rows, per key head:
+ *   out[slot] = weights[slot] + sum of exp(scale <Q[t,h,:], K_p> - LSE[t,h])
+ *   over the sequence's new tokens t that see position p and the Hq / Hkv query
+ *   heads h of the key head.
+ * LSE       : device pointer, contiguous [T, Hq] fp32: fa2_paged_fwd's, for the
+ *             same Q, caches, tables, scale and is_causal.
+ * weights, out: device pointers, contiguous [pages, Hkv, page_size] fp32;
+ *             weights NULL stands for zeros; out is `weights` itself or
+ *             overlaps nothing. Every position of every sequence is written
+ *             (also of one without new tokens), those whose page number is not
+ *             one aside; no two sequences share one. Sums are fp32, in a fixed
+ *             order.
+ * strides   : Q token, head; k_cache page, head, slot; block_table row (6).
+ * max_query_length: as for fa2_paged_fwd.
+ */
+FA2_API int fa2_paged_key_weights(const void* Q, const float* LSE, const void* k_cache, const float* weights,
+                                  float* out, const int* block_table, const int* key_lengths, const int* query_starts,
+                                  const long long* strides, int T, int B, int Hq, int Hkv, int D, int pages,
+                                  int page_size, int max_pages, int max_query_length, float scale, int is_causal,
+                                  int dtype, struct CUstream_st* stream);
+
+/*
+ * fa2_paged_evict — per key head, `keep` positions of every sequence to new
+ * pages: the last `recent` and, of the others, the keep - recent of the
+ * greatest weight (of equal ones the earlier; a NaN is above +inf, zeros of
+ * both signs are equal); all of a sequence that has no more than `keep`.
+ *
+ * weights   : device pointer, contiguous [pages, Hkv, page_size] fp32: read,
+ *             and written in the new pages.
+ * new_table : device pointer, [B, new_max_pages] int32: the pages that the kept
+ *             keys, values and weights are copied to, in order, from position 0
+ *             on. None is a page that a sequence has positions in (pages are
+ *             read and written at once), and it is another table than
+ *             block_table. An entry outside [0, pages) is not written to.
+ * new_lengths: device pointer, [B] int32, overwritten with min(length, keep).
+ * kept      : device pointer, contiguous [B, Hkv, keep] int32, overwritten with
+ *             the kept positions, ascending, and -1 behind them.
+ * strides   : k_cache page, head, slot; v_cache page, head, slot; block_table
+ *             row; new_table row (8).
+ * 0 <= recent <= keep <= new_max_pages * page_size. A position whose page
+ * number is not one counts as the least weight and is copied as zeros.
+ */
+FA2_API int fa2_paged_evict(void* k_cache, void* v_cache, float* weights, const int* block_table,
+                            const int* key_lengths, const int* new_table, int* new_lengths, int* kept,
+                            const long long* strides, int B, int Hkv, int D, int pages, int page_size, int max_pages,
+                            int new_max_pages, int keep, int recent, int dtype, struct CUstream_st* stream);
+
+/*
  * fa2_device_status — read the device-side watchdog word of the current
  * device, synchronising `stream` first. *status receives 0 when no kernel of
  * this library has timed out waiting on one of its internal barriers since
@@ -547,7 +692,7 @@ FA2_API int fa2_set_watchdog_ns(unsigned long long ns);
  * fa2_test_withhold_next_load — test hook for the watchdog. When enable is
  * nonzero, the next launch of this library (process-wide, one launch only:
  * a forward kernel, the main kernel of fa2_bwd or fa2_cross_bwd, or a kernel
- * of fa2_cross_fwd that waits for tiles) withholds its first K/V
+ * of fa2_cross_fwd or fa2_paged_fwd that waits for tiles) withholds its first K/V
  * tile: the waits for that tile run out after the watchdog time, the kernel
  * records the wait site in the watchdog word, winds down without leaving
  * work in flight, and its outputs (O/LSE, or dQ/dK/dV) are left unspecified.

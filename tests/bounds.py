@@ -98,3 +98,51 @@ def check_cross_bwd(grads, q, k, v, o, lse, do, scale, n):
         if n is not None and name != "dq":  # zeros behind the keys, exactly
             for b in range(k.shape[0]):
                 assert bool((got[b, :, min(max(int(n[b]), 0), k.shape[2]):] == 0).all()), name
+
+
+def check_paged_attention(o, lse, q, kc, vc, batch, scale, causal=True):
+    """As cross attention's forward, over a paged cache; rows of no sequence are not looked at."""
+    from oracle import paged
+    want_o, want_l, a, size = paged.attention(q, kc, vc, *batch, scale, causal)
+    u = torch.finfo(q.dtype).eps / 2
+    s32 = (16 * size + 32) * E32
+    tol = u * (a + want_o.abs()) * (1 + u) + s32 * a
+    if q.dtype == torch.float16:  # weights below 2^-14 are off by 2^-25
+        most = float(vc.float().nan_to_num(0.0).abs().max()) * batch[0].shape[1] * kc.shape[2]
+        tol = tol + 2.0 ** -25 * (most + 1)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    mine = torch.zeros(q.shape[0], dtype=torch.bool)
+    for _, t0, count, _, _ in paged.sequences(*batch, q.shape[0], kc.shape[2]):
+        mine[t0:t0 + count] = True
+    o, lse, want_o, want_l, tol = o[mine], lse[mine], want_o[mine], want_l[mine], tol[mine]
+    empty = want_l.isinf()
+    assert torch.equal(lse.isinf(), empty) and bool((lse[empty] > 0).all())
+    assert bool((o[empty] == 0).all())
+    assert torch.equal(lse.isnan(), want_l.isnan()) and torch.equal(o.isnan(), want_o.isnan())
+    bad = (o - want_o).abs() > tol
+    assert not bad.any(), f"O: {int(bad.sum())} of {bad.numel()}, worst {float(((o - want_o).abs() / tol.clamp(min=1e-30)).nan_to_num(0).max())} tolerances"
+    fine = ~empty & ~want_l.isnan()
+    dl = (lse - want_l)[fine].abs()
+    tl = s32 + 4 * E32 * want_l[fine].abs()
+    assert bool((dl <= tl).all()), f"LSE off by {float((dl / tl).max())} tolerances"
+
+
+def check_key_weights(out, q, lse, kc, weights, batch, scale, causal=True):
+    """Every term is off, relative to itself, by what its exponent is off: 16 steps of 2^-24 of the score's products
+    (bounds of cross attention), 4 of |LSE| (its product with log2 e, the subtraction) and 32 for the exponential; the
+    sum of `rows` terms in 32 bits adds a step each at most, the sum with the old weight one of the result."""
+    from oracle import paged
+    want, rows, size = paged.key_weights(q, lse, kc, weights, *batch, scale, causal)
+    fin = lse[lse.isfinite()]
+    most = float(fin.abs().max()) if fin.numel() else 0.0
+    out = out.cpu().double()
+    mine = torch.zeros(want.shape, dtype=torch.bool)
+    for _, _, _, n, ids in paged.sequences(*batch, q.shape[0], kc.shape[2]):
+        for i, pg in enumerate(ids):
+            if 0 <= pg < kc.shape[0]:
+                mine[pg, :, :min(kc.shape[2], n - i * kc.shape[2])] = True
+    out, want = out[mine], want[mine]
+    tol = (16 * size + 4 * most + 32 + rows) * E32 * want.abs() + E32 * want.abs() + 2.0 ** -126
+    assert torch.equal(out.isnan(), want.isnan())
+    bad = (out - want).abs() > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, worst {float(((out - want).abs() / tol).nan_to_num(0).max())} tolerances"
