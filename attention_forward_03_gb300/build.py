@@ -26,7 +26,8 @@ SOURCES = ["fa2_api.cu", "fa2_noalloc.cu", "fa2_host.cu", "fa2_fwd_d32.cu", "fa2
            "fa2_cross_api.cu", "fa2_cross_rows.cu", "fa2_cross_short.cu",
            "fa2_cross_d32.cu", "fa2_cross_d64.cu", "fa2_cross_d96.cu", "fa2_cross_d128.cu",
            "fa2_cross_bwd_api.cu", "fa2_cross_bwd_d32.cu", "fa2_cross_bwd_d64.cu", "fa2_cross_bwd_d96.cu",
-           "fa2_cross_bwd_d128.cu", "fa2_paged_api.cu", "fa2_paged_rows.cu", "fa2_paged_weigh.cu", "fa2_paged_append.cu"]
+           "fa2_cross_bwd_d128.cu", "fa2_paged_api.cu", "fa2_paged_rows.cu", "fa2_paged_weigh.cu", "fa2_paged_append.cu",
+           "fa2_paged_d32.cu", "fa2_paged_d64.cu", "fa2_paged_d96.cu", "fa2_paged_d128.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

@@ -57,6 +57,17 @@ constexpr size_t paged_rows_workspace_bytes(int grid, int d) {  // ws_o [grid][1
 cudaError_t launch_paged_rows(int D, bool bf16, const CUtensorMap& k, const CUtensorMap& v, const PagedAttnParams& p,
                               int grid, cudaStream_t stream);
 
+// More rows (fa2_paged_kernel.cuh, instantiated in fa2_paged_d{32,64,96,128}.cu).
+// q: map (D, head, token) with boxes of 64 elements x group heads x sub-tile
+// tokens; k, v: as above with boxes of min(page size, 128) slots.
+struct PagedTileParams : PagedAttnParams {
+  int sub_tokens;   // tokens of a sub-tile: 128 / group
+  int page_rows;    // positions of a page in one K/V tile: min(page size, 128)
+};
+template <int D, bool kBf16>
+cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                               const PagedTileParams& p, int grid, cudaStream_t stream);
+
 // ------------------------------------------------------------ key weights
 struct PagedWeighParams : PagedBatch {
   const void* q;

@@ -120,6 +120,20 @@ bool encode_cache_map(CUtensorMap* m, const void* ptr, const PagedStrides& c, co
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// (D, head, token) of the queries, boxes of 64 elements x `heads` heads x `tokens` tokens.
+bool encode_query_map(CUtensorMap* m, const void* ptr, long long token, long long head, int T, int Hq, int D, int dtype,
+                      unsigned heads, unsigned tokens) {
+  const EncodeFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T}, one = (cuuint64_t)D * 2;
+  const cuuint64_t strides[2] = {Hq > 1 ? (cuuint64_t)head * 2 : one, T > 1 ? (cuuint64_t)token * 2 : one};
+  const cuuint32_t box[3] = {64, heads, tokens}, step[3] = {1, 1, 1};
+  return enc(m, dtype == FA2_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Whether any output meets any of the other ranges (inputs, or a later output); empty ranges meet nothing.
 struct Range {
   const void* at;
@@ -140,7 +154,20 @@ size_t tokens_reach(int T, long long token, int heads, long long head, int D) {
   return static_cast<size_t>((T - 1) * token * (T > 1) + (heads - 1) * head * (heads > 1) + D) * 2;
 }
 
-size_t fwd_workspace_bytes(int sms, int D) { return paged_rows_workspace_bytes(std::min(sms, kPagedRowsMaxCtas), D); }
+// The rows kernel's partial results, then the tiles kernel's.
+size_t rows_workspace(int sms, int D) { return paged_rows_workspace_bytes(std::min(sms, kPagedRowsMaxCtas), D); }
+size_t fwd_workspace_bytes(int sms, int D) { return rows_workspace(sms, D) + stream_k_workspace_bytes(sms, D); }
+
+using TilesFn = cudaError_t (*)(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const PagedTileParams&, int,
+                                cudaStream_t);
+TilesFn pick_tiles(int d, bool bf) {
+  switch (d) {
+    case 32: return bf ? launch_paged_tiles<32, true> : launch_paged_tiles<32, false>;
+    case 64: return bf ? launch_paged_tiles<64, true> : launch_paged_tiles<64, false>;
+    case 96: return bf ? launch_paged_tiles<96, true> : launch_paged_tiles<96, false>;
+    default: return bf ? launch_paged_tiles<128, true> : launch_paged_tiles<128, false>;
+  }
+}
 
 int cuda_result(cudaError_t e) { return e == cudaSuccess ? FA2_OK : record_cuda_error(e); }
 
@@ -220,12 +247,12 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   if (static_cast<int64_t>(T) * group > (1 << 30)) return FA2_ERR_INVALID_ARG;
   if (pages == 0 || max_pages == 0) return FA2_ERR_INVALID_ARG;
   if (!Q || !k_cache || !v_cache || !O || !LSE || !strides || !workspace) return FA2_ERR_INVALID_ARG;
-  PagedAttnParams p = {};
+  PagedTileParams p = {};
   rc = fill_batch(p, z, block_table, key_lengths, query_starts, strides[8]);
   if (rc != FA2_OK) return rc;
   const PagedStrides ks = {strides[2], strides[3], strides[4]}, vs = {strides[5], strides[6], strides[7]};
   const long long tokens[2] = {T, Hq};
-  if (!strides_ok(strides, tokens, 2, 0) || !cache_strides_ok(ks, z) || !cache_strides_ok(vs, z)) return FA2_ERR_INVALID_ARG;
+  if (!strides_ok(strides, tokens, 2, 8) || strides[0] >= 1ll << 39 || strides[1] >= 1ll << 39 || !cache_strides_ok(ks, z) || !cache_strides_ok(vs, z)) return FA2_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(O, 16) || !aligned(LSE, 4) ||
       !aligned(workspace, 16))
     return FA2_ERR_ALIGN;
@@ -252,20 +279,47 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   p.status = status;
   p.watchdog_ns = watchdog_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CUtensorMap mk, mv;
-  if (!encode_cache_map(&mk, k_cache, ks, z, 16u) || !encode_cache_map(&mv, v_cache, vs, z, 16u))
-    return record_cuda_error(cudaErrorInvalidValue);
-  const int grid = std::min(sms, kPagedRowsMaxCtas);
-  p.rows_from = 1;
-  p.rows_to = INT_MAX;
+  // Sequences of at most 16 rows per key head run on the rows kernel, those of
+  // more on the tensor cores (unless a token alone has more rows than a
+  // sub-tile); each kernel passes over the other's. Only the device knows the
+  // sequences' tokens, so both are launched unless the sizes rule one out.
+  const int64_t most = static_cast<int64_t>(query_starts ? std::min(T, max_query_length) : p.each) * group;
+  const int64_t least = static_cast<int64_t>(query_starts ? 1 : p.each) * group;
+  const bool tiles = most > kPagedRows && group <= kRows, rows_too = !tiles || least <= kPagedRows;
   p.test_withhold = take_test_withhold();
   char* const ws = static_cast<char*>(workspace);
-  p.ws_o = reinterpret_cast<float*>(ws);
-  p.ws_stats = p.ws_o + static_cast<size_t>(grid) * kPagedRows * D;
-  p.ws_flags = reinterpret_cast<unsigned long long*>(ws + paged_rows_workspace_bytes(grid, D) -
-                                                     (static_cast<size_t>(grid) * 8 + 255) / 256 * 256);
+  const bool bf = dtype == FA2_BF16;
+  if (rows_too) {
+    CUtensorMap mk, mv;
+    if (!encode_cache_map(&mk, k_cache, ks, z, 16u) || !encode_cache_map(&mv, v_cache, vs, z, 16u))
+      return record_cuda_error(cudaErrorInvalidValue);
+    const int grid = std::min(sms, kPagedRowsMaxCtas);
+    p.rows_from = 1;
+    p.rows_to = tiles ? kPagedRows : INT_MAX;
+    p.ws_o = reinterpret_cast<float*>(ws);
+    p.ws_stats = p.ws_o + static_cast<size_t>(grid) * kPagedRows * D;
+    p.ws_flags = reinterpret_cast<unsigned long long*>(ws + rows_workspace(sms, D) -
+                                                       (static_cast<size_t>(grid) * 8 + 255) / 256 * 256);
+    p.epoch = next_launch_epoch();
+    const cudaError_t e = launch_paged_rows(D, bf, mk, mv, p, grid, s);
+    if (e != cudaSuccess) return record_cuda_error(e);
+  }
+  if (!tiles) return FA2_OK;
+  CUtensorMap mq, mk, mv;
+  p.sub_tokens = kRows / group;
+  p.page_rows = std::min(page_size, kKeys);
+  if (!encode_query_map(&mq, Q, p.q_token, p.q_head, T, Hq, D, dtype, group, p.sub_tokens) ||
+      !encode_cache_map(&mk, k_cache, ks, z, p.page_rows) || !encode_cache_map(&mv, v_cache, vs, z, p.page_rows))
+    return record_cuda_error(cudaErrorInvalidValue);
+  p.rows_from = rows_too ? kPagedRows + 1 : 1;
+  p.rows_to = INT_MAX;
+  const size_t slots = static_cast<size_t>(sms) * kSubTiles;
+  p.ws_o = reinterpret_cast<float*>(ws + rows_workspace(sms, D));
+  p.ws_stats = p.ws_o + slots * D * 128;
+  p.ws_flags = reinterpret_cast<unsigned long long*>(
+      ws + rows_workspace(sms, D) + (slots * (static_cast<size_t>(D) * 128 + 3 * 128) * sizeof(float) + 255) / 256 * 256);
   p.epoch = next_launch_epoch();
-  return cuda_result(launch_paged_rows(D, dtype == FA2_BF16, mk, mv, p, grid, s));
+  return cuda_result(pick_tiles(D, bf)(mq, mk, mv, p, sms, s));
 }
 
 extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void* k_cache, const float* weights,

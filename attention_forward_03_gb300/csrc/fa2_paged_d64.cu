@@ -1,0 +1,11 @@
+// Attention over a paged cache on the tensor cores (fa2_paged_kernel.cuh), head dimension 64.
+#include "fa2_paged_kernel.cuh"
+
+namespace fa2 {
+
+template cudaError_t launch_paged_tiles<64, true>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                                  const PagedTileParams&, int, cudaStream_t);
+template cudaError_t launch_paged_tiles<64, false>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                                   const PagedTileParams&, int, cudaStream_t);
+
+}  // namespace fa2

@@ -1,0 +1,618 @@
+// Attention of a batch's new tokens over a paged cache on the tensor cores:
+// sequences with more than 16 query rows per key head (chunks of prompts, whole
+// prompts). The design is that of fa2_kernel.cuh (persistent CTAs, TMA loads,
+// tcgen05 products accumulating in tensor memory, one softmax warpgroup per
+// 128-row sub-tile, equal shares of all K/V tiles per CTA with a merge of the
+// units that are cut); what is different:
+//
+//   rows      a sub-tile is 128 / group tokens of one sequence with all the
+//             query heads of one key head, row = token * group + head: one box
+//             of the map (D, head, token) of q. K and V are read once for all
+//             of them. Rows past the sequence's tokens see no key.
+//   tiles     128 positions, from one box per page of the map (D, slot, head,
+//             page) of the cache: the producer warp's lanes hold one page
+//             number each, read a tile ahead, and each issues its page's boxes.
+//             Pages past the last position are not loaded; a page number that
+//             is none leaves NaN in K's rows (written by the lane) and zeros in
+//             V's (out of the map).
+//   mask      a row sees its token's position and the earlier ones, so units
+//             have different numbers of tiles; the walk (fa2_paged_walk.cuh)
+//             counts them in closed form.
+//   output    through the warp's own rows of the P buffer (its own buffer where
+//             P lives in tensor memory), so that a row's 256 bytes go out
+//             together; rows of a next sequence may follow, so no box is stored.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "fa2_cross.cuh"
+#include "fa2_paged_walk.cuh"
+
+namespace fa2 {
+
+template <int D>
+struct PagedLayout {
+  static constexpr int kPanels = (D + 63) / 64;
+  static constexpr int kDp = kPanels * 64;
+  static constexpr int kTileBytes = kPanels * kPanelBytes;
+  static constexpr bool kPInTmem = kPanels == 1;
+  static constexpr int kStages = kPanels == 2 ? 3 : 10;
+  static constexpr int kNpv = D == 32 ? 64 : D;  // N of P.V, as in fa2_kernel.cuh
+  static constexpr int kQBytes = kSubTiles * kTileBytes;
+  static constexpr int kPOffset = kQBytes;  // P and the rows on their way out; with P in tensor memory those alone
+  static constexpr int kPBytes = kPInTmem ? kPanelBytes : kPTileBytes;  // per sub-tile
+  static constexpr int kRingOffset = kPOffset + kSubTiles * kPBytes;
+  static constexpr int kBarOffset = kRingOffset + kStages * kTileBytes;
+  // q_full, q_empty, ring full (K)[S], ring full (V)[S], ring empty[S], s_full[2], s_free[2], p_full[2], p_free[2],
+  // o_full[2], drain[2], part[2]
+  static constexpr int kNumBars = 2 + 3 * kStages + 2 * 7;
+  static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
+  static constexpr int kStartOffset = kMiscOffset + 16;
+  static constexpr int kSmemBytes = kStartOffset + static_cast<int>(sizeof(PagedStart)) + 1024;
+  static constexpr uint32_t kColO = 2 * kKeys;
+  static constexpr uint32_t kColP = kColO + 2 * kDp;
+  static_assert(kColO + 2 * kDp + (kPInTmem ? 2 * kKeys / 2 : 0) <= kTmemCols, "TMEM budget");
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kStartOffset % alignof(PagedStart) == 0, "alignment");
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa2_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const PagedTileParams p) {
+  using L = PagedLayout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const uint32_t sQ = base, sP = base + L::kPOffset, sRing = base + L::kRingOffset, bars = base + L::kBarOffset;
+  const uint32_t bar_q_full = bars, bar_q_empty = bars + 8;
+  // K and V tiles have "full" barriers of their own in every slot, as in fa2_kernel.cuh
+  auto bar_full = [&](int s, uint32_t is_v) { return bars + 16 + 8u * (is_v * L::kStages + s); };
+  auto bar_empty = [&](int s) { return bars + 16 + 8u * (2 * L::kStages + s); };
+  const uint32_t bar_s_full0 = bars + 16 + 24u * L::kStages;  // these: [sub-tile]
+  const uint32_t bar_s_free0 = bar_s_full0 + 16;
+  const uint32_t bar_p_full0 = bar_s_free0 + 16;
+  const uint32_t bar_p_free0 = bar_p_full0 + 16;
+  const uint32_t bar_o_full0 = bar_p_free0 + 16;
+  const uint32_t bar_drain = bar_o_full0 + 16;  // [issuer]
+  const uint32_t bar_part0 = bar_drain + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOffset);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOffset + 4);
+  PagedStart* const start = reinterpret_cast<PagedStart*>(smem + L::kStartOffset);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (warp == 0) {
+    const PagedStart st = paged_start(p);
+    if (lane == 0) *start = st;
+  }
+  if (threadIdx.x == 32) {
+    mbar_init(bar_q_full, 1);
+    mbar_init(bar_q_empty, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(bar_full(s, 0u), 1);
+      mbar_init(bar_full(s, 1u), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_s_full0 + 8 * t, 1);
+      mbar_init(bar_s_free0 + 8 * t, 4 * 32);
+      mbar_init(bar_p_full0 + 8 * t, 4 * 32);
+      mbar_init(bar_p_free0 + 8 * t, 1);
+      mbar_init(bar_o_full0 + 8 * t, 1);
+      mbar_init(bar_drain + 8 * t, 1);
+      mbar_init(bar_part0 + 8 * t, 4 * 32);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  Watchdog wd;
+  wd.status = p.status;
+  wd.abort_flag = abort_flag;
+  wd.limit_ns = p.watchdog_ns;
+  // Sub-tiles with tokens.
+  auto live_subtiles = [&](const PagedSegment& s) { return s.token + p.sub_tokens >= s.n ? 1 : kSubTiles; };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == kLoadWarp) {
+      // ---------------------------------------------------------- producer
+      // Ring order per segment [b, e): K_b, then for each j: K_{j+1}, V_j —
+      // the order the MMA issuers consume and release them.
+      if (lane == 0) {
+        tma_prefetch_map(&tmQ);
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+      }
+      const uint64_t keep = l2_policy_evict_last();          // K/V: re-read by every unit of the head
+      const uint64_t stream_once = l2_policy_evict_first();  // Q: read once
+      const uint32_t q_bytes = static_cast<uint32_t>(p.sub_tokens * p.group * 128 * L::kPanels);
+      const uint32_t page_bytes = static_cast<uint32_t>(p.page_rows * 128 * L::kPanels);
+      const int in_page = (1 << p.page_shift) - 1;
+      int slot = 0;
+      uint32_t ring_ph = 0, issued = 0, q_round = 0;
+      uint32_t types = 0, kbits = 0, vbits = 0;  // as in fa2_kernel.cuh
+      bool ok = true;
+      PagedCursor cur = paged_first(p, *start);
+      PagedSegment w;
+      // This lane's page of tile j: pages of a tile are dealt to the lanes.
+      auto position = [&](int j) { return j * kKeys + lane * p.page_rows; };
+      auto has_page = [&](int j) { return lane * p.page_rows < kKeys && position(j) < w.keys; };
+      auto entry = [&](int j) { return j < w.kv_end && has_page(j) ? paged_entry(p, w.b, position(j)) : -1; };
+      auto load_tile = [&](const CUtensorMap* map, int j, int page, uint32_t is_v) -> bool {
+        bool free = lane != 0 || wait_bounded(bar_empty(slot), ring_ph ^ 1u, wd, kSiteLoadRingEmpty, true, kNapNs);
+        free = __all_sync(0xffffffffu, free);
+        if (!free) return false;
+        const uint32_t full = bar_full(slot, is_v);
+        const uint32_t dst = sRing + static_cast<uint32_t>(slot * L::kTileBytes + lane * p.page_rows * 128);
+        const bool mine = has_page(j), there = mine && page_ok(p, page);
+        if (mine && !there && !is_v) {  // no such page: its scores are NaN
+          for (int pn = 0; pn < L::kPanels; ++pn)
+            for (int r = 0; r < p.page_rows * 8; ++r)
+              st_shared_v4(dst + static_cast<uint32_t>(pn * kPanelBytes + r * 16), 0x7fff7fffu, 0x7fff7fffu,
+                           0x7fff7fffu, 0x7fff7fffu);
+          fence_proxy_async_shared();
+        }
+        const bool load = mine && (there || is_v);
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, load));
+        if (!(p.test_withhold && issued == 0)) {  // test hook: the first tile never arrives
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * page_bytes);
+          __syncwarp();
+          if (load)
+            for (int pn = 0; pn < L::kPanels; ++pn)
+              tma_load_4d_hint(dst + static_cast<uint32_t>(pn * kPanelBytes), map, full, pn * 64,
+                               position(j) & in_page, w.head, there ? page : p.pages, keep);
+        }
+        types = (types & ~(1u << slot)) | (is_v << slot);
+        if (is_v) vbits ^= 1u << slot; else kbits ^= 1u << slot;
+        ++issued;
+        if (++slot == L::kStages) {
+          slot = 0;
+          ring_ph ^= 1u;
+        }
+        return true;
+      };
+      while (ok && paged_next(cur, w, p)) {
+        int now = entry(w.kv_begin), next = entry(w.kv_begin + 1);
+        if (q_round > 0) {
+          bool free = lane != 0 || wait_bounded(bar_q_empty, (q_round - 1) & 1u, wd, kSiteLoadQEmpty, true, kNapNs);
+          ok = __all_sync(0xffffffffu, free);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          const int n_sub = live_subtiles(w);
+          mbar_arrive_expect_tx(bar_q_full, n_sub * q_bytes);
+          for (int t = 0; t < n_sub; ++t)
+            for (int pn = 0; pn < L::kPanels; ++pn)
+              tma_load_3d_hint(sQ + t * L::kTileBytes + pn * kPanelBytes, &tmQ, bar_q_full, pn * 64,
+                               w.head * p.group, w.t0 + w.token + t * p.sub_tokens, stream_once);
+        }
+        ++q_round;
+        ok = load_tile(&tmK, w.kv_begin, now, 0u);
+        for (int j = w.kv_begin; j < w.kv_end && ok; ++j) {
+          const int after = entry(j + 2);
+          if (j + 1 < w.kv_end) ok = load_tile(&tmK, j + 1, next, 0u);
+          if (ok) ok = load_tile(&tmV, j, now, 1u);
+          now = next;
+          next = after;
+        }
+      }
+      // Drain: every copy issued must have landed before the CTA may exit.
+      if (lane == 0) {
+        const uint32_t first = issued > static_cast<uint32_t>(L::kStages) ? issued - L::kStages : 0u;
+        for (uint32_t i = first; i < issued; ++i) {  // the latest tile of each slot
+          const int s = static_cast<int>(i % L::kStages);
+          const uint32_t is_v = (types >> s) & 1u;
+          const uint32_t par = (((is_v ? vbits : kbits) >> s) & 1u) ^ 1u;
+          wait_bounded(bar_full(s, is_v), par, wd, kSiteDrain, false, kNapNs);
+        }
+        if (q_round > 0) wait_bounded(bar_q_full, (q_round - 1) & 1u, wd, kSiteDrain, false, kNapNs);
+      }
+      __syncwarp();
+    } else if (warp < kMmaWarp + kIssuers) {
+      // ------------------------------------- MMA issuers: 0 every S, 1 every P.V
+      if (lane == 0) {
+        const int me = warp - kMmaWarp;
+        constexpr uint32_t idesc_s = make_idesc_f16(kBf16, kKeys, false);
+        constexpr uint32_t idesc_o = make_idesc_f16(kBf16, L::kNpv, true);
+        constexpr uint32_t kHi = desc_hi_sw128(1024);
+        auto issue_s = [&](int t, int slot) {
+          const uint32_t qa = desc_lo_sw128(sQ, 16) + static_cast<uint32_t>((t * L::kTileBytes) >> 4);
+          const uint32_t ka = desc_lo_sw128(sRing, 16) + static_cast<uint32_t>(slot * (L::kTileBytes >> 4));
+          const uint32_t dt = tmem + static_cast<uint32_t>(t * kKeys);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = static_cast<uint32_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
+            mma_ss_w(dt, qa + off, kHi, ka + off, kHi, idesc_s, kk > 0 ? 1u : 0u);
+          }
+        };
+        // `tail`: only the tile's first `steps` ones of 16 positions, those with keys
+        auto issue_pv = [&](int t, int slot, bool acc, auto tail, [[maybe_unused]] int steps) {
+          const uint32_t pa = desc_lo_sw128(sP, 16) + static_cast<uint32_t>((t * L::kPBytes) >> 4);
+          const uint32_t va = desc_lo_sw128(sRing, kPanelBytes) + static_cast<uint32_t>(slot * (L::kTileBytes >> 4));
+          const uint32_t dt = tmem + L::kColO + static_cast<uint32_t>(t * L::kDp);
+          const uint32_t pt = tmem + L::kColP + static_cast<uint32_t>(t * (kKeys / 2));
+          auto one = [&](int kk) {
+            const uint32_t vb = va + static_cast<uint32_t>((kk * 16 * 128) >> 4);
+            const uint32_t acc_kk = (acc || kk > 0) ? 1u : 0u;
+            if constexpr (L::kPInTmem) {
+              mma_ts_w(dt, pt + 8u * kk, vb, kHi, idesc_o, acc_kk);
+            } else {
+              const uint32_t po = static_cast<uint32_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
+              mma_ss_w(dt, pa + po, kHi, vb, kHi, idesc_o, acc_kk);
+            }
+          };
+          if constexpr (tail.value) {
+#pragma unroll 1
+            for (int kk = 0; kk < steps; ++kk) one(kk);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk) one(kk);
+          }
+        };
+        auto k_index = [](int j, int b) { return j == b ? 0 : 2 * (j - b) - 1; };
+        auto v_index = [](int j, int b, int e) { return j == e - 1 ? 2 * (j - b) + 1 : 2 * (j - b) + 2; };
+        uint32_t bits = 0u;  // parity of the next use of each slot's full barrier of this issuer's type
+        auto take = [&](uint32_t idx, uint32_t is_v) -> int {
+          const int s = static_cast<int>(idx % L::kStages);
+          const uint32_t par = (bits >> s) & 1u;
+          bits ^= 1u << s;
+          return wait_bounded(bar_full(s, is_v), par, wd, kSiteMmaRingFull, true, kNapNs) ? s : -1;
+        };
+        uint32_t base_idx = 0;  // global load index of the current segment's first tile
+        bool ok = true;
+        PagedCursor cur = paged_first(p, *start);
+        PagedSegment w;
+        if (me == 0) {
+          uint32_t q_round = 0, s_free_ph[2] = {0u, 0u};
+          bool s_out[2] = {false, false};  // an S issued whose TMEM the softmax has not released yet
+          while (ok && paged_next(cur, w, p)) {
+            const int b = w.kv_begin, e = w.kv_end;
+            const int n_sub = live_subtiles(w);
+            if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) break;
+            ++q_round;
+            for (int j = b; j < e && ok; ++j) {
+              const int slot_k = take(base_idx + k_index(j, b), 0u);
+              if (slot_k < 0) { ok = false; break; }
+              for (int t = 0; t < n_sub; ++t) {
+                if (s_out[t]) {
+                  if (!wait_bounded(bar_s_free0 + 8 * t, s_free_ph[t], wd, kSiteMmaSFree, true, kNapNs)) { ok = false; break; }
+                  s_free_ph[t] ^= 1u;
+                }
+                tc_fence_after_sync();
+                issue_s(t, slot_k);
+                mma_commit(bar_s_full0 + 8 * t);
+                s_out[t] = true;
+              }
+              if (!ok) break;
+              mma_commit(bar_empty(slot_k));
+              if (j == e - 1) mma_commit(bar_q_empty);
+            }
+            base_idx += 2u * static_cast<uint32_t>(e - b);
+          }
+        } else {
+          uint32_t p_full_ph[2] = {0u, 0u};
+          while (ok && paged_next(cur, w, p)) {
+            const int b = w.kv_begin, e = w.kv_end;
+            const int n_sub = live_subtiles(w);
+            auto tile = [&](int j, auto tail) {
+              const int slot_v = take(base_idx + v_index(j, b, e), 1u);
+              if (slot_v < 0) { ok = false; return; }
+              int steps = kKeys / 16;
+              if constexpr (tail.value) {
+                // rows behind the keys up to the last product's 16: zeros
+                const int valid = w.keys - j * kKeys;
+                steps = cross_key_steps(valid);
+                cross_zero_rows(sRing + static_cast<uint32_t>(slot_v * L::kTileBytes), L::kPanels, valid);
+              }
+              for (int t = 0; t < n_sub; ++t) {
+                if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
+                p_full_ph[t] ^= 1u;
+                tc_fence_after_sync();
+                issue_pv(t, slot_v, j > b, tail, steps);
+                mma_commit(bar_p_free0 + 8 * t);
+                if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
+              }
+              mma_commit(bar_empty(slot_v));
+            };
+            // the unit's last tile may be short
+            const int e_full = e == w.nkv && w.keys < e * kKeys ? e - 1 : e;
+            for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
+            if (e_full < e && ok) tile(e_full, std::true_type{});
+            base_idx += 2u * static_cast<uint32_t>(e - b);
+          }
+        }
+        // Drain: all issued tensor-core work completes before TMEM is released.
+        mma_commit(bar_drain + 8 * me);
+        wait_bounded(bar_drain + 8 * me, 0u, wd, kSiteDrain, false, kNapNs);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ------------------------------------------------- softmax warpgroups
+    const int t = warp >> 2;                 // sub-tile
+    const int wr = warp & 3;
+    const int rr = wr * 32 + lane;           // row within the sub-tile
+    const uint32_t lane_off = static_cast<uint32_t>(wr * 32) << 16;
+    const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(t * kKeys);
+    const uint32_t tO = tmem + lane_off + L::kColO + static_cast<uint32_t>(t * L::kDp);
+    const uint32_t tP = tmem + lane_off + L::kColP + static_cast<uint32_t>(t * (kKeys / 2));
+    const uint32_t bar_s = bar_s_full0 + 8 * t, bar_sf = bar_s_free0 + 8 * t, bar_p = bar_p_full0 + 8 * t;
+    const uint32_t bar_pf = bar_p_free0 + 8 * t, bar_o = bar_o_full0 + 8 * t, bar_part = bar_part0 + 8 * t;
+    // this thread's row in shared memory: 128 bytes per 64 keys (or columns of O), 16-byte chunks
+    // placed by the 128-byte swizzle (chunk c of row r at c ^ (r % 8))
+    const uint32_t p_tile = sP + static_cast<uint32_t>(t * L::kPBytes);
+    const uint32_t p_row = p_tile + static_cast<uint32_t>(rr * 128);
+    const uint32_t p_xor = static_cast<uint32_t>(rr & 7);
+    const float c = p.scale_log2;
+    const int row_token = rr / p.group, row_head = rr - row_token * p.group;
+    uint32_t s_phase = 0, o_phase = 0, part_phase = 0;
+    uint32_t p_count = 0;  // P tiles published so far
+    bool ok = true;
+    PagedCursor cur = paged_first(p, *start);
+    PagedSegment w;
+    while (ok && paged_next(cur, w, p)) {
+      if (t >= live_subtiles(w)) continue;
+      const int token = w.token + t * p.sub_tokens + row_token;
+      const bool live = row_token < p.sub_tokens && token < w.n;
+      int limit = 0;  // this row's keys: [0, limit)
+      if (live) limit = p.causal ? min(max(w.length - w.n + token + 1, 0), w.length) : w.length;
+      float m_raw = -CUDART_INF_F;  // running max of the raw scores seen so far
+      float base2 = -CUDART_INF_F;  // exponent base (log2 units) that l and O are relative to
+      float l = 0.f, l_o = 0.f;     // sum of p; normaliser of O (see fa2_kernel.cuh)
+      for (int j = w.kv_begin; j < w.kv_end; ++j) {
+        bool got = wait_bounded(bar_s, s_phase, wd, kSiteSoftmaxSFull);
+        got = __all_sync(0xffffffffu, got);
+        if (!got) { ok = false; break; }
+        s_phase ^= 1u;
+        tc_fence_after_sync();
+        uint32_t sr[128];
+        tmem_ld32x128_wait(tS, sr);
+        tc_fence_before_sync();
+        mbar_arrive(bar_sf);  // S is in registers: the next scores may be computed
+        float s[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(sr[i]);
+        const int kv0 = j * kKeys;
+        if (kv0 + kKeys > limit) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (kv0 + i >= limit) s[i] = -CUDART_INF_F;
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = fmax3(s[32 * q], s[32 * q + 1], s[32 * q + 2]);
+#pragma unroll
+          for (int i = 3; i < 31; i += 2) mx[q] = fmax3(mx[q], s[32 * q + i], s[32 * q + i + 1]);
+          mx[q] = fmaxf(mx[q], s[32 * q + 31]);
+        }
+        const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+        m_raw = fmaxf(m_raw, m_tile);
+        // the base moves only when the max has passed it by 2^kRescaleLog2 (or on the first key)
+        const float cand = m_raw * c;
+        float alpha = 1.f;
+        if (m_raw != -CUDART_INF_F && (base2 == -CUDART_INF_F || cand - base2 > kRescaleLog2)) {
+          alpha = ex2_approx(base2 - cand);
+          base2 = cand;
+        }
+        const float nb = (base2 == -CUDART_INF_F) ? 0.f : -base2;
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          float x0, x1;
+          ffma2_bcast(x0, x1, s[2 * i], s[2 * i + 1], c, nb);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          fadd2_acc(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], p0, p1);
+          pk[i] = pack2(p0, p1, kBf16);
+        }
+        // the previous P.V is complete before its P is overwritten and O rescaled
+        if (p_count > 0) {
+          bool fr = wait_bounded(bar_pf, (p_count - 1) & 1u, wd, kSiteSoftmaxPFree);
+          fr = __all_sync(0xffffffffu, fr);
+          if (!fr) { ok = false; break; }
+          tc_fence_after_sync();
+        }
+        if constexpr (L::kPInTmem) {
+          tmem_st32x32(tP, *reinterpret_cast<const uint32_t(*)[32]>(pk));
+          tmem_st32x32(tP + 32, *reinterpret_cast<const uint32_t(*)[32]>(pk + 32));
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < 16; ++ch) {
+            const uint32_t addr = p_row + static_cast<uint32_t>((ch >> 3) * kPanelBytes) +
+                                  ((static_cast<uint32_t>(ch & 7) ^ p_xor) << 4);
+            st_shared_v4(addr, pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+          }
+        }
+        if (j > w.kv_begin && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32x32_wait(tO + cc, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32x32(tO + cc, o);
+          }
+        }
+        tmem_wait_st();
+        if constexpr (!L::kPInTmem) fence_proxy_async_shared();
+        tc_fence_before_sync();
+        mbar_arrive(bar_p);
+        ++p_count;
+        const float lt = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        // the largest weight enters O's normaliser as it is rounded (fa2_kernel.cuh)
+        float x0, x1;
+        ffma2_bcast(x0, x1, m_tile, m_tile, c, nb);
+        const float px = ex2_approx(x0), pxr = round16(px, kBf16);
+        l = l * alpha + lt;
+        l_o = l_o * alpha + (lt + (pxr - px));
+      }
+      if (!ok) break;
+      // -------------------------------------------------------- epilogue
+      bool got = wait_bounded(bar_o, o_phase, wd, kSiteSoftmaxOFull);
+      got = __all_sync(0xffffffffu, got);
+      if (!got) break;
+      o_phase ^= 1u;
+      tc_fence_after_sync();
+      if (w.kv_begin > 0) {
+        // Not the unit's first tiles: the unnormalised partial (O, base, l, l_o) to the owner.
+        const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + t;
+        float* po = p.ws_o + slot * D * 128;
+        float* ps = p.ws_stats + slot * 3 * 128;
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o[32];
+          tmem_ld32x32_wait(tO + cc, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) __stcg(po + (cc + i) * 128 + rr, __uint_as_float(o[i]));
+        }
+        __stcg(ps + rr, base2);
+        __stcg(ps + 128 + rr, l);
+        __stcg(ps + 256 + rr, l_o);
+        __threadfence();
+        mbar_arrive(bar_part);
+        if (rr < 32) {
+          bool done = wait_bounded(bar_part, part_phase, wd, kSitePartialWrite);
+          done = __all_sync(0xffffffffu, done);
+          if (!done) break;
+          if (rr == 0) store_release(p.ws_flags + slot, p.epoch);
+        }
+        part_phase ^= 1u;
+        tc_fence_before_sync();
+        continue;
+      }
+      // Owner (or whole unit): fold in the partials of the CTAs that took the rest of it, if any.
+      float a_own = 1.f, nbase = base2;
+      int first_c = blockIdx.x + 1, last_c = blockIdx.x;  // partial holders [first_c, last_c]
+      if (w.kv_end < w.nkv) {
+        while (last_c + 1 < start->shares && paged_share_begin(*start, last_c + 1) < w.unit_end) ++last_c;
+        bool fine = true;
+        for (int cb = first_c + (rr & 31); cb <= last_c && fine; cb += 32)
+          fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSitePartialFlag);
+        fine = __all_sync(0xffffffffu, fine);
+        if (!fine) break;
+        __syncwarp();  // what one lane acquired is visible to all
+        // every thread of the warpgroup has seen the flags: taken back, so that a
+        // replay of a captured launch, which carries the same tag, does not find them
+        mbar_arrive(bar_part);
+        if (rr < 32) {
+          bool seen = wait_bounded(bar_part, part_phase, wd, kSitePartialFlag);
+          seen = __all_sync(0xffffffffu, seen);
+          if (!seen) break;
+          for (int cb = first_c + rr; cb <= last_c; cb += 32) p.ws_flags[static_cast<size_t>(cb) * 2 + t] = 0ull;
+        }
+        part_phase ^= 1u;
+        for (int cb = first_c; cb <= last_c; ++cb)
+          nbase = fmaxf(nbase, __ldcg(p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128 + rr));
+        // 0 for a partial that saw no key (and for one of two: no difference of infinities)
+        a_own = base2 == -CUDART_INF_F ? 0.f : ex2_approx(base2 - nbase);
+        l *= a_own;
+        l_o *= a_own;
+        for (int cb = first_c; cb <= last_c; ++cb) {
+          const float* ps = p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128;
+          const float bc = __ldcg(ps + rr), a = bc == -CUDART_INF_F ? 0.f : ex2_approx(bc - nbase);
+          l += a * __ldcg(ps + 128 + rr);
+          l_o += a * __ldcg(ps + 256 + rr);
+        }
+        base2 = nbase;
+      }
+      const float inv = l > 0.f ? __frcp_rn(l_o) : 0.f;
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t o[32];
+        tmem_ld32x32_wait(tO + cc, o);
+        float of[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]) * a_own;
+        for (int cb = first_c; cb <= last_c; ++cb) {
+          const size_t slot = static_cast<size_t>(cb) * 2 + t;
+          const float bc = __ldcg(p.ws_stats + slot * 3 * 128 + rr), a = bc == -CUDART_INF_F ? 0.f : ex2_approx(bc - nbase);
+          const float* po = p.ws_o + slot * D * 128;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) of[i] = fmaf(a, __ldcg(po + (cc + i) * 128 + rr), of[i]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pk[i] = pack2(of[8 * q + 2 * i] * inv, of[8 * q + 2 * i + 1] * inv, kBf16);
+          const int c8 = cc / 8 + q;
+          st_shared_v4(p_row + static_cast<uint32_t>((c8 >> 3) * kPanelBytes) + ((static_cast<uint32_t>(c8 & 7) ^ p_xor) << 4),
+                       pk[0], pk[1], pk[2], pk[3]);
+        }
+      }
+      // O_t is read out; the next segment's first P.V may overwrite it once this
+      // warpgroup publishes that segment's first P (ordered by bar_p).
+      tc_fence_before_sync();
+      // the warp's rows, whole rows at a time: 16-byte chunks of a row by neighbouring lanes
+      const long long out_row =
+          live ? (static_cast<long long>(w.t0 + token) * p.heads + w.head) * p.group + row_head : -1ll;
+      __syncwarp();
+      constexpr int kChunks = D / 8;
+#pragma unroll 4
+      for (int i = 0; i < kChunks; ++i) {
+        const int at = i * 32 + lane, r = at / kChunks, ch = at - r * kChunks;
+        const long long to = __shfl_sync(0xffffffffu, out_row, r);
+        const uint8_t* from = smem + L::kPOffset + t * L::kPBytes + (ch >> 3) * kPanelBytes + (wr * 32 + r) * 128 +
+                              (((ch & 7) ^ (r & 7)) << 4);
+        if (to >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + to * D)[ch] = *reinterpret_cast<const uint4*>(from);
+      }
+      __syncwarp();  // read before the next segment's P is written there
+      if (live) p.lse[out_row] = l != 0.f ? (base2 + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;  // NaN stays
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                               const PagedTileParams& p, int grid, cudaStream_t stream) {
+  auto kern = fa2_paged_kernel<D, kBf16>;
+  constexpr int smem = PagedLayout<D>::kSmemBytes;
+  static PerDeviceOnce prepared;
+  const cudaError_t e = once_per_device(prepared, [&]() -> cudaError_t {
+    cudaFuncAttributes fa;
+    cudaError_t r = cudaFuncGetAttributes(&fa, kern);
+    if (r != cudaSuccess) return r;
+    // The in-kernel register split assumes exactly kLaunchRegs per thread at launch.
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  // the holder of a cut unit waits for other CTAs: all are resident, or the launch fails
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, q, k, v, p);
+}
+
+}  // namespace fa2

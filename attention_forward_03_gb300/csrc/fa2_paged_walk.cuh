@@ -1,0 +1,222 @@
+// The work-unit walk of attention over a paged cache on the tensor cores
+// (fa2_paged_kernel.cuh): as the one of cross attention in fa2_cross.cuh, with
+// units whose number of K/V tiles depends on the sequence and, under the causal
+// mask, on the unit's last token.
+#pragma once
+#include "fa2_paged.cuh"
+
+namespace fa2 {
+
+// A sub-tile is 128 rows (tokens of one sequence, query heads of one key head), a unit two of them.
+
+// The sum of floor((a i + b) / m) over i < n, for n, m > 0 and a, b >= 0: whole
+// parts out, then the lattice points under the line counted the other way
+// round, as in Euclid's algorithm. a n + b stays below 2^31.
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long sum = 0;
+  for (;;) {
+    if (a >= m) {
+      sum += static_cast<long long>(n) * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += static_cast<long long>(n) * (b / m);
+      b %= m;
+    }
+    const unsigned y = a * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const unsigned t = m;
+    m = a;
+    a = t;
+  }
+}
+
+struct PagedUnits {  // of one sequence
+  PagedSeq s;
+  int units;  // per key head; 0: none of this kernel's
+};
+
+__device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
+
+__device__ __forceinline__ PagedUnits paged_units(const PagedTileParams& p, int b) {
+  PagedUnits u;
+  u.s = paged_seq(p, b);
+  const int rows = u.s.n * p.group, per = 2 * p.sub_tokens;
+  u.units = rows >= p.rows_from && rows <= p.rows_to ? (u.s.n + per - 1) / per : 0;
+  return u;
+}
+
+// Positions that token i of the sequence sees.
+__device__ __forceinline__ int paged_seen(const PagedTileParams& p, const PagedSeq& s, int i) {
+  return p.causal ? min(max(s.length - s.n + i + 1, 0), s.length) : s.length;
+}
+
+// What a unit counts in the equal shares besides its tiles: the tensor cores
+// idle while its last P.V drains and its rows go out.
+constexpr int kPagedUnitCost = 3;
+
+// Positions that a unit's last token sees, which no other one of it exceeds.
+__device__ __forceinline__ int unit_keys(const PagedTileParams& p, const PagedSeq& s, int unit) {
+  return paged_seen(p, s, min((unit + 1) * 2 * p.sub_tokens, s.n) - 1);
+}
+
+// Steps of the first m of a sequence's units of one key head.
+__device__ __forceinline__ long long steps_before(const PagedTileParams& p, const PagedUnits& u, int m) {
+  long long tiles = 0;
+  if (!p.causal) {
+    tiles = static_cast<long long>(m) * key_tiles(u.s.length);
+  } else {
+    const int per = 2 * p.sub_tokens, c = u.s.length - u.s.n;
+    int full = min(m, u.units - 1);
+    if (m == u.units) tiles += key_tiles(u.s.length);  // the last unit sees every position
+    // units of tokens before the first position: one masked tile
+    const int none = c < 0 ? min(full, -c / per) : 0;
+    tiles += none;
+    full -= none;
+    if (full > 0)
+      tiles += floor_sum(static_cast<unsigned>(full), kKeys, static_cast<unsigned>(per),
+                         static_cast<unsigned>(c + (none + 1) * per + kKeys - 1));
+  }
+  return tiles + static_cast<long long>(m) * kPagedUnitCost;
+}
+
+// Where this CTA's share begins, found once per CTA.
+struct PagedStart {
+  long long total;  // steps of the whole call
+  int shares;       // CTAs with a share
+  int b, head, unit;
+  int from;         // steps of that unit before the share
+};
+
+__device__ __forceinline__ long long paged_share_begin(const PagedStart& st, int c) {
+  return c >= st.shares ? st.total : st.total * c / st.shares;
+}
+
+// By one whole warp.
+__device__ __forceinline__ PagedStart paged_start(const PagedTileParams& p) {
+  PagedStart st = {};
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const PagedUnits u = paged_units(p, b);
+    if (u.units) sum += p.heads * steps_before(p, u, u.units);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  st.total = sum;
+  st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), sum));
+  if (static_cast<int>(blockIdx.x) >= st.shares) return st;
+  const long long want = paged_share_begin(st, blockIdx.x);
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    long long mine = 0;
+    if (b < p.B) {
+      const PagedUnits u = paged_units(p, b);
+      if (u.units) mine = p.heads * steps_before(p, u, u.units);
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      st.b = b0 + l;
+      before += __shfl_sync(0xffffffffu, upto - mine, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  const PagedUnits u = paged_units(p, st.b);
+  if (u.units == 0) {  // only should the tables have changed meanwhile
+    st.shares = 0;
+    return st;
+  }
+  const long long per_head = steps_before(p, u, u.units);
+  long long r = want - before;
+  st.head = static_cast<int>(min(r / per_head, p.heads - 1ll));
+  r -= st.head * per_head;
+  // the last unit that starts at or before step r, 32 candidates at a time
+  int lo = 0, hi = u.units;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, m = lo + (lane + 1) * step;
+    const bool ok = m < hi && steps_before(p, u, m) <= r;
+    lo += __popc(__ballot_sync(0xffffffffu, ok)) * step;
+    hi = min(hi, lo + step);
+  }
+  st.unit = lo;
+  st.from = static_cast<int>(r - steps_before(p, u, lo));
+  return st;
+}
+
+struct PagedSegment {
+  int b, head;
+  int token, t0, n, length;  // the unit's first token in the sequence; the sequence
+  int keys;                  // positions that the unit's tokens see at most
+  int kv_begin, kv_end;      // K/V tiles of this segment
+  int nkv;                   // of the whole unit
+  long long unit_end;        // step one past the unit's last
+};
+
+struct PagedCursor {
+  PagedUnits u;
+  int b, head, unit, from;
+  long long step, end;
+};
+
+__device__ __forceinline__ PagedCursor paged_first(const PagedTileParams& p, const PagedStart& st) {
+  PagedCursor c;
+  c.b = st.b;
+  c.head = st.head;
+  c.unit = st.unit;
+  c.from = st.from;
+  c.step = paged_share_begin(st, blockIdx.x);
+  c.end = paged_share_begin(st, blockIdx.x + 1);
+  c.u = paged_units(p, st.b);
+  return c;
+}
+
+// Next segment of this CTA. Every role walks the same sequence. A share that
+// ends among the steps of a unit that stand for no tile has no tile of it; the
+// next share then holds all of them.
+__device__ __forceinline__ bool paged_next(PagedCursor& c, PagedSegment& s, const PagedTileParams& p) {
+  while (c.step < c.end) {
+    s.b = c.b;
+    s.head = c.head;
+    s.token = c.unit * 2 * p.sub_tokens;
+    s.t0 = c.u.s.t0;
+    s.n = c.u.s.n;
+    s.length = c.u.s.length;
+    s.keys = unit_keys(p, c.u.s, c.unit);
+    s.nkv = key_tiles(s.keys);
+    const int per_unit = s.nkv + kPagedUnitCost, from = min(c.from, per_unit);
+    const int to = static_cast<int>(min(static_cast<long long>(per_unit), from + (c.end - c.step)));
+    s.unit_end = c.step - from + per_unit;
+    s.kv_begin = max(from - kPagedUnitCost, 0);
+    s.kv_end = max(to - kPagedUnitCost, 0);
+    c.step += to - from;
+    c.from = 0;
+    if (++c.unit >= c.u.units) {
+      c.unit = 0;
+      if (++c.head >= p.heads) {
+        c.head = 0;
+        do {
+          if (++c.b >= p.B) {
+            c.step = c.end;
+            break;
+          }
+          c.u = paged_units(p, c.b);
+        } while (c.u.units == 0);
+      }
+    }
+    if (s.kv_end > s.kv_begin) return true;
+  }
+  return false;
+}
+
+}  // namespace fa2

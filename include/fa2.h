@@ -548,8 +548,8 @@ FA2_API int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk
  *             has T / B tokens (T is a multiple of B then).
  * strides   : HOST pointer to element strides, listed with each call.
  *             Strides of dimensions longer than 1 are multiples of 8 (the
- *             tables': any), not negative, those of the caches positive and
- *             below 2^39; no view reaches further than 2^44 elements.
+ *             tables': any), not negative, those of the caches and of Q
+ *             positive and below 2^39; no view reaches further than 2^44 elements.
  * T, B, Hq, Hkv: sizes >= 0, Hq a multiple of Hkv.
  *             max_pages * page_size, T and T * Hq / Hkv are at most 2^30.
  * D         : 32, 64, 96 or 128.
