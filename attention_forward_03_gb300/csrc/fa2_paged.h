@@ -70,17 +70,21 @@ cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const
 
 // ------------------------------------------------------------ key weights
 struct PagedWeighParams : PagedBatch {
-  const void* q;
-  long long q_token, q_head;
   const float* lse;           // [T][Hq]
-  const void* k;
-  PagedStrides ks;
   const float* in;            // [pages][heads][page size], or NULL: zeros
   float* out;
   int group, causal;
   float scale_log2;
+  // a block of query rows: tokens, heads of the group, blocks that a group takes, columns of its product
+  int block_tokens, block_heads, head_blocks, columns;
+  int page_rows;              // as in PagedTileParams
+  int* status;
+  unsigned long long watchdog_ns;
+  int test_withhold;
 };
-cudaError_t launch_paged_weigh(int D, bool bf16, const PagedWeighParams& p, int sms, cudaStream_t stream);
+// q: map (D, head, token) with boxes of 64 elements x block heads x block tokens; k: as for launch_paged_tiles.
+cudaError_t launch_paged_weigh(int D, bool bf16, const CUtensorMap& q, const CUtensorMap& k, const PagedWeighParams& p,
+                               int grid, cudaStream_t stream);
 
 // --------------------------------------------------------- append, evict
 struct PagedAppendParams : PagedBatch {

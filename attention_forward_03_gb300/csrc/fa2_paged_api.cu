@@ -340,15 +340,15 @@ extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void
   PagedWeighParams p = {};
   rc = fill_batch(p, z, block_table, key_lengths, query_starts, strides[5]);
   if (rc != FA2_OK) return rc;
-  p.ks = PagedStrides{strides[2], strides[3], strides[4]};
+  const PagedStrides ks = {strides[2], strides[3], strides[4]};
   const long long tokens[2] = {T, Hq};
-  if (!strides_ok(strides, tokens, 2, 0) || !cache_strides_ok(p.ks, z)) return FA2_ERR_INVALID_ARG;
+  if (!strides_ok(strides, tokens, 2, 8) || strides[0] >= 1ll << 39 || strides[1] >= 1ll << 39 || !cache_strides_ok(ks, z)) return FA2_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(LSE, 4) || !aligned(weights, 4) || !aligned(out, 4))
     return FA2_ERR_ALIGN;
   const size_t pool = static_cast<size_t>(pages) * Hkv * page_size * 4;
   const Range outs[1] = {{out, pool}};
   const Range ins[7] = {{T > 0 ? Q : nullptr, T > 0 ? tokens_reach(T, strides[0], Hq, strides[1], D) : 0},
-                        {k_cache, cache_reach(p.ks, z)}, {LSE, static_cast<size_t>(T) * Hq * 4},
+                        {k_cache, cache_reach(ks, z)}, {LSE, static_cast<size_t>(T) * Hq * 4},
                         {key_lengths, static_cast<size_t>(B) * 4}, {query_starts, static_cast<size_t>(B + 1) * 4},
                         {block_table, static_cast<size_t>((B - 1) * p.table_stride + max_pages) * 4},
                         {weights == out ? nullptr : weights, pool}};
@@ -357,17 +357,28 @@ extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void
   int* status = nullptr;
   rc = current_device_facts(&sms, &status);
   if (rc != FA2_OK) return rc;
-  p.q = Q;
-  p.q_token = strides[0];
-  p.q_head = strides[1];
   p.lse = LSE;
-  p.k = k_cache;
   p.in = weights;
   p.out = out;
   p.group = group;
   p.causal = is_causal != 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  return cuda_result(launch_paged_weigh(D, dtype == FA2_BF16, p, sms, reinterpret_cast<cudaStream_t>(stream)));
+  p.block_heads = std::max(1, std::min(group, kRows));
+  p.head_blocks = (group + kRows - 1) / kRows;
+  // No larger blocks than the sequences fill: a block is loaded and multiplied whole.
+  const int most = query_starts ? std::min(T, max_query_length) : p.each;
+  p.block_tokens = std::max(1, std::min(kRows / p.block_heads, most));
+  p.columns = (p.block_tokens * p.block_heads + 15) / 16 * 16;
+  p.page_rows = std::min(page_size, kKeys);
+  p.status = status;
+  p.watchdog_ns = watchdog_limit_ns();
+  CUtensorMap mq, mk;
+  if (!encode_cache_map(&mk, k_cache, ks, z, p.page_rows)) return record_cuda_error(cudaErrorInvalidValue);
+  if (T == 0) mq = mk;  // not read
+  else if (!encode_query_map(&mq, Q, strides[0], strides[1], T, Hq, D, dtype, p.block_heads, p.block_tokens))
+    return record_cuda_error(cudaErrorInvalidValue);
+  p.test_withhold = take_test_withhold();
+  return cuda_result(launch_paged_weigh(D, dtype == FA2_BF16, mq, mk, p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int fa2_paged_evict(void* k_cache, void* v_cache, float* weights, const int* block_table,
