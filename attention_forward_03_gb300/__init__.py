@@ -31,5 +31,6 @@ from .norm_rope import (  # noqa: F401
     fa2_qk_norm_rope_bwd_workspace_bytes, qk_norm_rope_backward, qk_norm_rope_forward,
 )
 from .paged import (  # noqa: F401
-    fa2_paged_fwd_workspace_bytes, paged_attention_forward, paged_cache_append, paged_cache_evict, paged_key_weights,
+    fa2_paged_fwd_workspace_bytes, fa2_paged_key_weights_workspace_bytes, paged_attention_forward, paged_cache_append,
+    paged_cache_evict, paged_key_weights,
 )

@@ -74,7 +74,8 @@ SIGNATURES = {
                                                                       ctypes.c_size_t, _VP]),
     "fa2_paged_fwd_workspace_bytes": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "fa2_paged_key_weights": (ctypes.c_int, [_VP] * 9 + [ctypes.c_int] * 9 + [ctypes.c_float, ctypes.c_int,
-                                                                              ctypes.c_int, _VP]),
+                                                                              ctypes.c_int, _VP, ctypes.c_size_t, _VP]),
+    "fa2_paged_key_weights_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(ctypes.c_size_t)]),
     "fa2_paged_evict": (ctypes.c_int, [_VP] * 9 + [ctypes.c_int] * 10 + [_VP]),
     "fa2_device_status": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_int), ctypes.c_int]),
     "fa2_set_watchdog_ns": (ctypes.c_int, [ctypes.c_ulonglong]),

@@ -322,11 +322,22 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   return cuda_result(pick_tiles(D, bf)(mq, mk, mv, p, sms, s));
 }
 
+extern "C" int fa2_paged_key_weights_workspace_bytes(size_t* bytes) {
+  if (!bytes) return FA2_ERR_INVALID_ARG;
+  int sms = 0;
+  int* status = nullptr;
+  const int rc = current_device_facts(&sms, &status);
+  if (rc != FA2_OK) return rc;
+  *bytes = paged_weigh_workspace_bytes(sms);
+  return FA2_OK;
+}
+
 extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void* k_cache, const float* weights,
                                      float* out, const int* block_table, const int* key_lengths,
                                      const int* query_starts, const long long* strides, int T, int B, int Hq, int Hkv,
                                      int D, int pages, int page_size, int max_pages, int max_query_length, float scale,
-                                     int is_causal, int dtype, struct CUstream_st* stream) {
+                                     int is_causal, int dtype, void* workspace, size_t workspace_bytes,
+                                     struct CUstream_st* stream) {
   const Sizes z = {T, B, Hkv, D, pages, page_size, max_pages, dtype};
   int rc = check_sizes(z);
   if (rc != FA2_OK) return rc;
@@ -336,27 +347,29 @@ extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void
   if (Hq % Hkv != 0 || (Hq == 0 && T > 0)) return FA2_ERR_INVALID_ARG;
   const int group = Hq / Hkv;
   if (static_cast<int64_t>(T) * group > (1 << 30)) return FA2_ERR_INVALID_ARG;
-  if ((T > 0 && (!Q || !LSE)) || !k_cache || !out || !strides) return FA2_ERR_INVALID_ARG;
+  if ((T > 0 && (!Q || !LSE)) || !k_cache || !out || !strides || !workspace) return FA2_ERR_INVALID_ARG;
   PagedWeighParams p = {};
   rc = fill_batch(p, z, block_table, key_lengths, query_starts, strides[5]);
   if (rc != FA2_OK) return rc;
   const PagedStrides ks = {strides[2], strides[3], strides[4]};
   const long long tokens[2] = {T, Hq};
   if (!strides_ok(strides, tokens, 2, 8) || strides[0] >= 1ll << 39 || strides[1] >= 1ll << 39 || !cache_strides_ok(ks, z)) return FA2_ERR_INVALID_ARG;
-  if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(LSE, 4) || !aligned(weights, 4) || !aligned(out, 4))
+  if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(LSE, 4) || !aligned(weights, 4) || !aligned(out, 4) ||
+      !aligned(workspace, 16))
     return FA2_ERR_ALIGN;
   const size_t pool = static_cast<size_t>(pages) * Hkv * page_size * 4;
-  const Range outs[1] = {{out, pool}};
+  const Range outs[2] = {{out, pool}, {workspace, workspace_bytes}};
   const Range ins[7] = {{T > 0 ? Q : nullptr, T > 0 ? tokens_reach(T, strides[0], Hq, strides[1], D) : 0},
                         {k_cache, cache_reach(ks, z)}, {LSE, static_cast<size_t>(T) * Hq * 4},
                         {key_lengths, static_cast<size_t>(B) * 4}, {query_starts, static_cast<size_t>(B + 1) * 4},
                         {block_table, static_cast<size_t>((B - 1) * p.table_stride + max_pages) * 4},
                         {weights == out ? nullptr : weights, pool}};
-  if (any_overlap(outs, 1, ins, 7)) return FA2_ERR_INVALID_ARG;
+  if (any_overlap(outs, 2, ins, 7)) return FA2_ERR_INVALID_ARG;
   int sms = 0;
   int* status = nullptr;
   rc = current_device_facts(&sms, &status);
   if (rc != FA2_OK) return rc;
+  if (workspace_bytes < paged_weigh_workspace_bytes(sms)) return FA2_ERR_INVALID_ARG;
   p.lse = LSE;
   p.in = weights;
   p.out = out;
@@ -378,6 +391,9 @@ extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void
   else if (!encode_query_map(&mq, Q, strides[0], strides[1], T, Hq, D, dtype, p.block_heads, p.block_tokens))
     return record_cuda_error(cudaErrorInvalidValue);
   p.test_withhold = take_test_withhold();
+  p.ws_sums = static_cast<float*>(workspace);
+  p.ws_flags = reinterpret_cast<unsigned long long*>(p.ws_sums + static_cast<size_t>(sms) * 2 * kKeys);
+  p.epoch = next_launch_epoch();
   return cuda_result(launch_paged_weigh(D, dtype == FA2_BF16, mq, mk, p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

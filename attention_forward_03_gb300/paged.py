@@ -32,11 +32,18 @@ _STRIDES9 = struct.Struct("=9q").pack
 _STRIDES8 = struct.Struct("=8q").pack
 _STRIDES6 = struct.Struct("=6q").pack
 _fwd_bytes = {}
+_weights_bytes = {}
 
 
 def fa2_paged_fwd_workspace_bytes(D: int) -> int:
     n = ctypes.c_size_t(0)
     _check(library().fa2_paged_fwd_workspace_bytes(int(D), ctypes.byref(n)), "fa2_paged_fwd_workspace_bytes")
+    return n.value
+
+
+def fa2_paged_key_weights_workspace_bytes() -> int:
+    n = ctypes.c_size_t(0)
+    _check(library().fa2_paged_key_weights_workspace_bytes(ctypes.byref(n)), "fa2_paged_key_weights_workspace_bytes")
     return n.value
 
 
@@ -106,6 +113,11 @@ def _check_pool(name, t, shape, dev):
 def _like(name, t, shape, dtype, dev):
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the caches' device")
+
+
+def _check_workspace(workspace, need, dev):
+    if workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on q's device")
 
 
 def _device_of(t):
@@ -205,8 +217,8 @@ def paged_attention_forward(q, k_cache, v_cache, block_table, key_lengths, query
             need = _fwd_bytes[(dev, D)] = fa2_paged_fwd_workspace_bytes(D)
         if workspace is None:
             workspace = scratch_for("paged_fwd", need, q.device, dev, handle, stream)
-        elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
-            raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on q's device")
+        else:
+            _check_workspace(workspace, need, dev)
         code = library().fa2_paged_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                                        lse.data_ptr(), block_table.data_ptr(), lengths, starts,
                                        _STRIDES9(*qs, *ks, *vs, row), T, B, Hq, Hkv, D, pages, page, width,
@@ -219,7 +231,7 @@ def paged_attention_forward(q, k_cache, v_cache, block_table, key_lengths, query
 
 def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=None, scale: float | None = None,
                       is_causal: bool = True, max_query_length: int | None = None, weights=None, out=None,
-                      stream=None):
+                      workspace=None, stream=None):
     """What every cached key weighs in the new tokens' softmax rows, added to `weights`; returns out.
 
     out[slot] = weights[slot] + sum of exp(scale <q_i, k> - LSE_i) over the
@@ -230,7 +242,9 @@ def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=No
     where it is not given (without either, a new tensor of zeros). Every
     position of every sequence is written, nothing else is; two sequences share
     no position. The sums have a fixed order.
-    max_query_length: as for paged_attention_forward.
+    max_query_length: as for paged_attention_forward. workspace: a uint8 CUDA
+    tensor of at least fa2_paged_key_weights_workspace_bytes() bytes (kept by
+    default, as paged_attention_forward's is).
     Runs on `stream` (a torch.cuda.Stream) or the current stream.
     """
     import torch
@@ -251,7 +265,8 @@ def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=No
         out = weights
     elif out is not weights:
         _check_pool("out", out, shape, dev)
-    handle = stream_handle(dev, stream, (q, lse, k_cache, block_table, key_lengths, query_starts, weights, out))
+    handle = stream_handle(dev, stream, (q, lse, k_cache, block_table, key_lengths, query_starts, weights, out,
+                                         workspace))
     if out is None:
         out = empty_on(stream, shape[:3], torch.float32, q.device)
         if stream is None:
@@ -262,11 +277,19 @@ def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=No
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with device_guard(dev):
+        need = _weights_bytes.get(dev)
+        if need is None:
+            need = _weights_bytes[dev] = fa2_paged_key_weights_workspace_bytes()
+        if workspace is None:
+            workspace = scratch_for("paged_key_weights", need, q.device, dev, handle, stream)
+        else:
+            _check_workspace(workspace, need, dev)
         code = library().fa2_paged_key_weights(q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), w, out.data_ptr(),
                                                block_table.data_ptr(), lengths, starts, _STRIDES6(*qs, *ks, row), T, B,
                                                Hq, Hkv, D, pages, page, width,
                                                T if max_query_length is None else max_query_length, scale,
-                                               1 if is_causal else 0, dtc, handle)
+                                               1 if is_causal else 0, dtc, workspace.data_ptr(), workspace.nbytes,
+                                               handle)
     if code != FA2_OK:
         _check(code, "fa2_paged_key_weights")
     return out

@@ -635,12 +635,22 @@ FA2_API int fa2_paged_fwd_workspace_bytes(int D, size_t* bytes);
  *             order.
  * strides   : Q token, head; k_cache page, head, slot; block_table row (6).
  * max_query_length: as for fa2_paged_fwd.
+ * workspace : as for fa2_paged_fwd, at least
+ *             fa2_paged_key_weights_workspace_bytes() bytes.
  */
 FA2_API int fa2_paged_key_weights(const void* Q, const float* LSE, const void* k_cache, const float* weights,
                                   float* out, const int* block_table, const int* key_lengths, const int* query_starts,
                                   const long long* strides, int T, int B, int Hq, int Hkv, int D, int pages,
                                   int page_size, int max_pages, int max_query_length, float scale, int is_causal,
-                                  int dtype, struct CUstream_st* stream);
+                                  int dtype, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * fa2_paged_key_weights_workspace_bytes — bytes of device workspace
+ * fa2_paged_key_weights takes on the current device, whatever the sizes.
+ * Returns FA2_OK, FA2_ERR_INVALID_ARG (bytes NULL), FA2_ERR_UNSUPPORTED or
+ * FA2_ERR_CUDA.
+ */
+FA2_API int fa2_paged_key_weights_workspace_bytes(size_t* bytes);
 
 /*
  * fa2_paged_evict — per key head, `keep` positions of every sequence to new
@@ -692,7 +702,7 @@ FA2_API int fa2_set_watchdog_ns(unsigned long long ns);
  * fa2_test_withhold_next_load — test hook for the watchdog. When enable is
  * nonzero, the next launch of this library (process-wide, one launch only:
  * a forward kernel, the main kernel of fa2_bwd or fa2_cross_bwd, or a kernel
- * of fa2_cross_fwd or fa2_paged_fwd that waits for tiles) withholds its first K/V
+ * of fa2_cross_fwd, fa2_paged_fwd or fa2_paged_key_weights that waits for tiles) withholds its first K/V
  * tile: the waits for that tile run out after the watchdog time, the kernel
  * records the wait site in the watchdog word, winds down without leaving
  * work in flight, and its outputs (O/LSE, or dQ/dK/dV) are left unspecified.

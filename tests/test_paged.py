@@ -25,7 +25,8 @@ GOOD = {
     "fwd": dict(SIZES, Hq=8, Q=A, kc=3 * A, vc=4 * A, O=8 * A, LSE=9 * A, table=5 * A, lengths=6 * A, starts=7 * A,
                 strides=(*TOKENS, *CACHE, *CACHE, 10), most=4, scale=0.125, causal=1, dtype=0, ws=10 * A, wsb=1 << 30),
     "weights": dict(SIZES, Hq=8, Q=A, LSE=9 * A, kc=3 * A, w=11 * A, out=12 * A, table=5 * A, lengths=6 * A,
-                    starts=7 * A, strides=(*TOKENS, *CACHE, 10), most=4, scale=0.125, causal=1, dtype=0),
+                    starts=7 * A, strides=(*TOKENS, *CACHE, 10), most=4, scale=0.125, causal=1, dtype=0, ws=10 * A,
+                    wsb=1 << 30),
     "evict": dict(SIZES, kc=3 * A, vc=4 * A, w=11 * A, table=5 * A, lengths=6 * A, new=7 * A, new_lengths=8 * A,
                   kept=9 * A, strides=(*CACHE, *CACHE, 10, 4), new_width=4, keep=50, recent=8, dtype=0),
 }
@@ -48,7 +49,7 @@ def call(lib, op, **over):
     if op == "weights":
         return c.fa2_paged_key_weights(a["Q"], a["LSE"], a["kc"], a["w"], a["out"], a["table"], a["lengths"],
                                        a["starts"], strides, a["T"], a["B"], a["Hq"], a["Hkv"], a["D"], *tail,
-                                       a["most"], a["scale"], a["causal"], a["dtype"], None)
+                                       a["most"], a["scale"], a["causal"], a["dtype"], a["ws"], a["wsb"], None)
     return c.fa2_paged_evict(a["kc"], a["vc"], a["w"], a["table"], a["lengths"], a["new"], a["new_lengths"], a["kept"],
                              strides, a["B"], a["Hkv"], a["D"], *tail, a["new_width"], a["keep"], a["recent"],
                              a["dtype"], None)
@@ -89,7 +90,8 @@ CASES += [
     ("fwd", dict(LSE=8 * A + 64), INVALID), ("fwd", dict(O=3 * A + 1024), INVALID), ("fwd", dict(ws=5 * A), INVALID),
     ("fwd", dict(pages=0), INVALID), ("fwd", dict(width=0), INVALID), ("fwd", dict(Hkv=0), INVALID),
     ("fwd", strided("fwd", 0, 20), INVALID), ("fwd", strided("fwd", 2, 1 << 45), INVALID),
-    ("weights", dict(out=None), INVALID), ("weights", dict(out=3 * A), INVALID), ("weights", dict(out=11 * A + 64), INVALID),
+    ("weights", dict(out=None), INVALID), ("weights", dict(ws=None), INVALID), ("weights", dict(ws=10 * A + 8), ALIGN),
+    ("weights", dict(ws=12 * A), INVALID), ("weights", dict(out=3 * A), INVALID), ("weights", dict(out=11 * A + 64), INVALID),
     ("weights", dict(out=9 * A), INVALID), ("weights", dict(out=12 * A + 2), ALIGN), ("weights", strided("weights", 4, 4), INVALID),
     ("evict", dict(w=None), INVALID), ("evict", dict(new=None), INVALID), ("evict", dict(kept=None), INVALID),
     ("evict", dict(new_lengths=None), INVALID), ("evict", dict(new=5 * A), INVALID), ("evict", dict(keep=65), INVALID),
