@@ -82,10 +82,10 @@ struct PagedWeighParams : PagedBatch {
   unsigned long long watchdog_ns;
   int test_withhold;
   unsigned long long epoch;
-  float* ws_sums;             // [grid][2][128]
-  unsigned long long* ws_flags;  // [grid][2]
+  float* ws_sums;             // [grid][256]
+  unsigned long long* ws_flags;  // [grid]
 };
-constexpr size_t paged_weigh_workspace_bytes(int grid) { return static_cast<size_t>(grid) * 2 * (kKeys * sizeof(float) + 8); }
+constexpr size_t paged_weigh_workspace_bytes(int grid) { return static_cast<size_t>(grid) * (2 * kKeys * sizeof(float) + 8); }
 // q: map (D, head, token) with boxes of 64 elements x block heads x block tokens; k: as for launch_paged_tiles.
 cudaError_t launch_paged_weigh(int D, bool bf16, const CUtensorMap& q, const CUtensorMap& k, const PagedWeighParams& p,
                                int grid, cudaStream_t stream);

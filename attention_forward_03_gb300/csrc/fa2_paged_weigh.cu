@@ -17,21 +17,26 @@
 // share of all steps; a unit that is cut between CTAs is finished by the one
 // that holds its first block, which adds the sums that the following CTAs left
 // in the workspace (they did so at the start of their shares, long before).
-//   warps 0-7     two warpgroups, one per tile: thread = key
+//   warps 0-7     two warpgroups, which take the steps in turn: thread = key of
+//                 either tile
 //   warps 8, 9    one thread each issues the products of one tile
 //   warps 10, 11  load one tile's K each (one box per page, a page number per
 //                 lane, read a unit ahead); warp 10 the blocks of query rows too
 // A block of query rows is up to 128 / group tokens with all heads of the
 // group (of more than 128 heads: one token, 128 heads). Where all rows of a
-// sequence fit into one block it stays for all units of a key head. S^T has
-// two buffers of 128 columns per tile in tensor memory, read out at once (in
-// four parts of 32 columns, which share a wait with the products under way,
-// a tile's exponentials took 1.3 us). The rows' LSE are laid out once per warp
-// and block in shared memory, as factors of the exponent.
+// sequence fit into one block it stays for all units of a key head. Each
+// warpgroup has a buffer of 128 columns per tile in tensor memory. The rows'
+// LSE are laid out once per warp and block in shared memory, as factors of the
+// exponent; a thread reads them once for its two keys (a warpgroup per tile,
+// with twice the reads and what a step takes besides its exponentials not
+// overlapped with another's: 1.45 us a step).
+// A unit's sums of the warpgroup that did not take its last step go through
+// shared memory to the other, which writes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "fa2_paged_walk.cuh"
 
@@ -47,6 +52,17 @@ __device__ __forceinline__ void tmem_ld32x8_wait(uint32_t taddr, uint32_t (&r)[8
       : "memory");
 }
 
+// 32 columns from each of two places, and the wait for them.
+__device__ __forceinline__ void tmem_ld32x32_two_wait(uint32_t from0, uint32_t from1, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]), "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31]), "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]), "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47]), "=&r"(r[48]), "=&r"(r[49]), "=&r"(r[50]), "=&r"(r[51]), "=&r"(r[52]), "=&r"(r[53]), "=&r"(r[54]), "=&r"(r[55]), "=&r"(r[56]), "=&r"(r[57]), "=&r"(r[58]), "=&r"(r[59]), "=&r"(r[60]), "=&r"(r[61]), "=&r"(r[62]), "=&r"(r[63])
+      : "r"(from0), "r"(from1)
+      : "memory");
+}
+
 enum : int {
   kSiteWeighKEmpty = 61,
   kSiteWeighQEmpty = 62,
@@ -55,12 +71,11 @@ enum : int {
   kSiteWeighSFree = 65,
   kSiteWeighSFull = 66,
   kSiteWeighPart = 67,
-  kSiteWeighFlag = 68,
-  kSiteWeighDrain = 69,
+  kSiteWeighTaken = 68,
+  kSiteWeighFlag = 69,
+  kSiteWeighDrain = 70,
 };
 
-// Steps of a unit besides those of its blocks: loads that wait, the sum's way out.
-constexpr int kWeighUnitCost = 1;
 constexpr int kUnitKeys = 2 * kKeys;
 
 // Units and blocks of query rows of one key head of a sequence.
@@ -85,11 +100,28 @@ __device__ __forceinline__ int first_block(const PagedWeighParams& p, const Weig
   return p.causal && w.blocks && token > 0 ? token / p.block_tokens * p.head_blocks : 0;
 }
 
+// What the steps of a unit with tokens of its own count more: blocks that some
+// rows see and others do not, about half a step each (without it the CTAs with
+// a chunk's last units came 6 us after the others' 33).
+__device__ __forceinline__ int own_cost(const PagedWeighParams& p, const WeighSeq& w) {
+  return p.causal ? min(w.blocks, kUnitKeys / p.block_tokens * p.head_blocks) / 2 : 0;
+}
+
+// Steps of a unit besides those of its blocks: loads that wait, the sum's way
+// out; of a key head's first one also the rows' (without it the CTA with a
+// batch's shortest sequences, single tokens over up to 256 positions, came
+// last: 51 us, the others 38 to 44).
+__device__ __forceinline__ int unit_cost(const PagedWeighParams& p, const WeighSeq& w, int unit) {
+  return (unit == 0 ? 2 : 1) + ((unit + 1) * kUnitKeys > w.s.length - w.s.n ? own_cost(p, w) : 0);
+}
+
 // Steps of the first m units of a key head.
 __device__ __forceinline__ long long weigh_before(const PagedWeighParams& p, const WeighSeq& w, int m) {
-  long long steps = static_cast<long long>(m) * (w.blocks + kWeighUnitCost);
+  long long steps = static_cast<long long>(m) * (w.blocks + 1) + (m > 0 ? 1 : 0);
   if (p.causal && w.blocks) {
     const int c = w.s.length - w.s.n, j0 = c > 0 ? (c + kUnitKeys - 1) / kUnitKeys : 0;
+    const int j1 = c > 0 ? c / kUnitKeys : 0;  // the first unit with tokens of its own
+    if (m > j1) steps += static_cast<long long>(m - j1) * own_cost(p, w);
     if (m > j0)
       steps -= p.head_blocks * floor_sum(static_cast<unsigned>(m - j0), static_cast<unsigned>(p.block_tokens), kUnitKeys,
                                          static_cast<unsigned>(j0 * kUnitKeys - c));
@@ -209,10 +241,10 @@ __device__ __forceinline__ bool weigh_next(WeighCursor& c, WeighSegment& u, cons
     u.s = c.w.s;
     u.blocks = c.w.blocks;
     u.first = min(first_block(p, c.w, c.unit), u.blocks);
-    const int per_unit = u.blocks - u.first + kWeighUnitCost, from = min(c.from, per_unit);
+    const int cost = unit_cost(p, c.w, c.unit), per_unit = u.blocks - u.first + cost, from = min(c.from, per_unit);
     const int to = static_cast<int>(min(static_cast<long long>(per_unit), from + (c.end - c.step)));
-    u.begin = u.first + max(from - kWeighUnitCost, 0);
-    u.end = u.first + max(to - kWeighUnitCost, 0);
+    u.begin = u.first + max(from - cost, 0);
+    u.end = u.first + max(to - cost, 0);
     c.step += to - from;
     c.from = 0;
     const bool any = u.end > u.begin || (u.first == u.blocks && to == per_unit);
@@ -246,15 +278,16 @@ struct WeighLayout {
   static constexpr int kSmallRows = 32;  // blocks of at most so many rows: more room for K
   static constexpr int kSmallBytes = kPanels * kSmallRows * 128;
   // stages of each tile's K and of Q, with blocks of up to 128 rows and with small ones
-  static constexpr int kK = kPanels == 2 ? 1 : 3, kQ = kPanels == 2 ? 4 : 6;
+  static constexpr int kK = kPanels == 2 ? 2 : 4, kQ = kPanels == 2 ? 2 : 4;
   static constexpr int kKSmall = kPanels == 2 ? 3 : 6, kQSmall = kPanels == 2 ? 2 : 4;
   static constexpr int kMostK = kKSmall, kMostQ = kQ > kQSmall ? kQ : kQSmall;
   static constexpr int kWide = 2 * kK * kTileBytes + kQ * kTileBytes;
   static constexpr int kNarrow = 2 * kKSmall * kTileBytes + kQSmall * kSmallBytes;
   static constexpr int kLseOffset = kWide > kNarrow ? kWide : kNarrow;  // [8 warps][128] floats
-  static constexpr int kBarOffset = kLseOffset + 8 * 128 * 4;
-  // k_full, k_empty [tile][K], q_full, q_empty [Q], s_full, s_free [tile][2], part[2], drain[2]
-  static constexpr int kNumBars = 4 * kMostK + 2 * kMostQ + 12;
+  static constexpr int kPartOffset = kLseOffset + 8 * 128 * 4;          // [2 warpgroups][128] pairs of floats
+  static constexpr int kBarOffset = kPartOffset + 2 * 128 * 8;
+  // k_full, k_empty [tile][K], q_full, q_empty [Q], s_full [warpgroup][tile], s_free, part, taken, flag [warpgroup], drain[2]
+  static constexpr int kNumBars = 4 * kMostK + 2 * kMostQ + 14;
   static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
   static constexpr int kStartOffset = kMiscOffset + 16;
   static constexpr int kSmemBytes = kStartOffset + static_cast<int>(sizeof(WeighStart)) + 1024;
@@ -283,8 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_q_full = [&](int s) { return bars + 8u * (4 * L::kMostK + s); };
   auto bar_q_empty = [&](int s) { return bars + 8u * (4 * L::kMostK + L::kMostQ + s); };
   const uint32_t rest = bars + 8u * (4 * L::kMostK + 2 * L::kMostQ);
-  const uint32_t bar_s_full0 = rest, bar_s_free0 = rest + 32;      // [tile][2]
-  const uint32_t bar_part0 = rest + 64, bar_drain0 = rest + 80;    // [tile]
+  const uint32_t bar_s_full0 = rest;                               // [warpgroup][tile]
+  // [warpgroup]: its buffers have been read; its sums of a unit are in shared memory; those
+  // have been read; steps of joining a cut unit
+  const uint32_t bar_s_free0 = rest + 32, bar_part0 = rest + 48, bar_taken0 = rest + 64, bar_flag0 = rest + 80;
+  const uint32_t bar_drain0 = rest + 96;                           // [issuer]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOffset);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOffset + 4);
   WeighStart* const start = reinterpret_cast<WeighStart*>(smem + L::kStartOffset);
@@ -304,13 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_q_full(s), 1);
       mbar_init(bar_q_empty(s), 2);  // both issuers pass every block
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar_s_full0 + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar_s_full0 + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s_free0 + 8 * i, 128);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar_part0 + 8 * t, 128);
-      mbar_init(bar_drain0 + 8 * t, 1);
+      mbar_init(bar_part0 + 8 * i, 128);
+      mbar_init(bar_taken0 + 8 * i, 128);
+      mbar_init(bar_flag0 + 8 * i, 128);
+      mbar_init(bar_drain0 + 8 * i, 1);
     }
     *abort_flag = 0;
     mbar_init_fence();
@@ -459,15 +495,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = wait_bounded(bar_q_full(qs), q_ph, wd, kSiteWeighQFull, true, kNapNs);
               if (!ok) break;
             }
+            const uint32_t wg = step & 1u, use = step++ >> 1;  // whose step, and which of its
             if (live) {
-              const int buf = 2 * t + (step & 1);
-              // the buffer's use before the last, if any, has been read
-              ok = wait_bounded(bar_s_free0 + 8 * buf, ((step >> 1) & 1u) ^ 1u, wd, kSiteWeighSFree, true, kNapNs);
+              const uint32_t buf = 2 * wg + t;
+              // the warpgroup's step before has been read
+              ok = wait_bounded(bar_s_free0 + 8 * wg, (use & 1u) ^ 1u, wd, kSiteWeighSFree, true, kNapNs);
               if (!ok) break;
-              ++step;
               tc_fence_after_sync();
               const uint32_t qa = desc_lo_sw128(sQ, 16) + ((static_cast<uint32_t>(qs) * q_slot) >> 4);
-              const uint32_t dt = tmem + static_cast<uint32_t>(buf * 128);
+              const uint32_t dt = tmem + buf * 128;
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t k_off = static_cast<uint32_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4);
@@ -495,12 +531,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    // ------------------------------------------ exponentials: thread = key
-    const int t = warp >> 2, key_lane = (warp & 3) * 32 + lane;
-    const uint32_t tS0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(t * 256);
+    // ---------------------- exponentials: thread = a key of either tile
+    const uint32_t wg = warp >> 2;
+    const int key_lane = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 256;
+    const uint32_t bar_full = bar_s_full0 + 16 * wg, bar_free = bar_s_free0 + 8 * wg, bar_flag = bar_flag0 + 8 * wg;
     float* const lse = reinterpret_cast<float*>(smem + L::kLseOffset) + warp * 128;
+    const float4* const l4 = reinterpret_cast<const float4*>(lse);
+    float2* const part = reinterpret_cast<float2*>(smem + L::kPartOffset) + key_lane;  // [warpgroup][128]
     const float c = p.scale_log2;
-    uint32_t step = 0, part_ph = 0;
+    uint32_t step = 0, full_ph[2] = {0u, 0u}, part_ph = 0, taken_ph = 1, flag_ph = 0;
     // this lane's four columns: where their LSE lie, from the block's first token and head on
     int at[4];
 #pragma unroll
@@ -508,8 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col = 4 * lane + i, token = col / p.block_heads;
       at[i] = token * p.heads * p.group + (col - token * p.block_heads);
     }
-    // a block's first token, its rows (columns of the product), and their factors of the exponent
-    auto read_block = [&](const WeighSegment& u, int q, int& token0, int& valid, float (&neg)[4]) {
+    // a block's first token, its rows (columns of the product), and their LSE (used a step
+    // later: nothing is done with them here that would wait for them)
+    auto read_block = [&](const WeighSegment& u, int q, int& token0, int& valid, float (&row_lse)[4]) {
       int hb = 0;
       if (p.head_blocks > 1) {  // blocks of one token
         token0 = q / p.head_blocks;
@@ -521,73 +562,126 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float* from = p.lse + (static_cast<long long>(u.s.t0 + token0) * p.heads + u.head) * p.group + hb * p.block_heads;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) neg[i] = 4 * lane + i < valid ? __ldg(from + at[i]) * -1.4426950408889634f : 0.f;
+      for (int i = 0; i < 4; ++i)
+        if (4 * lane + i < valid) row_lse[i] = __ldg(from + at[i]);
     };
-    // this thread's page of a segment, read a segment ahead
-    auto entry = [&](const WeighSegment& u) {
+    // this thread's page of a segment's tile
+    auto entry = [&](const WeighSegment& u, int t) {
       const int key = u.unit * kUnitKeys + t * kKeys + key_lane;
       return key < u.s.length ? paged_entry(p, u.b, key) : -1;
     };
     WeighCursor cur = weigh_cursor(p, *start);
-    WeighSegment u, ahead;
-    bool ok = true, more = weigh_next(cur, ahead, p);
-    int next_page = more ? entry(ahead) : -1;
-    while (more && ok) {
-      u = ahead;
-      const int page = next_page;
+    WeighSegment u;
+    bool ok = true;
+    int laid_b = -1, laid_head = -1;  // whose only block's factors are laid out
+    while (ok && weigh_next(cur, u, p)) {
       const long long unit_end = cur.step;  // one past the unit's last step here, or where the share ends
-      more = weigh_next(cur, ahead, p);
-      if (more) next_page = entry(ahead);
-      if (!has_tile(u, t)) continue;
-      const int key = u.unit * kUnitKeys + t * kKeys + key_lane;
+      const int steps = u.end - u.begin;
+      // who finishes the segment: the warpgroup of its last step
+      const bool finishes = steps > 0 ? ((step + steps - 1) & 1u) == wg : wg == 0;
+      int q = u.begin + static_cast<int>((step ^ wg) & 1u);
+      step += steps;
+      if (q >= u.end && !finishes) continue;
+      const int key = u.unit * kUnitKeys + key_lane;
+      const bool two = has_tile(u, 1);
       const bool owner = u.begin == u.first;  // of the unit's first block
-      long long to = -1;
-      float old = 0.f;
-      if (owner && page_ok(p, page)) {
-        to = ((static_cast<long long>(page) * p.heads + u.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-        if (p.in) old = p.in[to];
+      int page0 = -1, page1 = -1;             // asked for now, used at the end
+      if (finishes && owner) {
+        page0 = entry(u, 0);
+        page1 = entry(u, 1);
       }
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      float neg[4];
-      int token0 = 0, valid = u.s.n * p.group;  // (of the only block, which is laid out already)
-      const bool loads = loads_rows(u);
-      if (loads && u.begin < u.end) read_block(u, u.begin, token0, valid, neg);
-      for (int q = u.begin; q < u.end; ++q, ++step) {
-        // the columns that see this key: [lo, now)
-        const int now = valid;
-        const int lo = p.causal ? min(max(key - (u.s.length - u.s.n) - token0, 0), p.block_tokens) * p.block_heads : 0;
-        if (loads) {
+      float acc0[4] = {0.f, 0.f, 0.f, 0.f}, acc1[4] = {0.f, 0.f, 0.f, 0.f};
+      float row_lse[4] = {0.f, 0.f, 0.f, 0.f};
+      const bool laid = u.blocks == 1 && laid_b == u.b && laid_head == u.head;
+      int token0 = 0, valid = u.s.n * p.group;  // (of the only block, when it is laid out)
+      if (q < u.end && !laid) read_block(u, q, token0, valid, row_lse);
+      for (; q < u.end; q += 2) {
+        // the columns that see this thread's keys: [lo0, now) and [lo1, now)
+        const int now = valid, behind = key - (u.s.length - u.s.n) - token0;
+        const int lo0 = p.causal ? min(max(behind, 0), p.block_tokens) * p.block_heads : 0;
+        const int lo1 = p.causal ? min(max(behind + kKeys, 0), p.block_tokens) * p.block_heads : 0;
+        if (!laid) {
+          constexpr float kLog2e = 1.4426950408889634f;
           __syncwarp();  // the block before has been read
-          *reinterpret_cast<float4*>(lse + 4 * lane) = make_float4(neg[0], neg[1], neg[2], neg[3]);
+          *reinterpret_cast<float4*>(lse + 4 * lane) =
+              make_float4(-kLog2e * row_lse[0], -kLog2e * row_lse[1], -kLog2e * row_lse[2], -kLog2e * row_lse[3]);
           __syncwarp();
-          if (q + 1 < u.end) read_block(u, q + 1, token0, valid, neg);
+          if (q + 2 < u.end) read_block(u, q + 2, token0, valid, row_lse);
         }
-        const uint32_t half = step & 1u, buf = 2 * t + half, tS = tS0 + 128 * half;
-        bool got = wait_bounded(bar_s_full0 + 8 * buf, (step >> 1) & 1u, wd, kSiteWeighSFull);
+        bool got = wait_bounded(bar_full, full_ph[0], wd, kSiteWeighSFull);
+        if (two) got = got && wait_bounded(bar_full + 8, full_ph[1], wd, kSiteWeighSFull);
         got = __all_sync(0xffffffffu, got);
         if (!got) { ok = false; break; }
+        full_ph[0] ^= 1u;
+        if (two) full_ph[1] ^= 1u;
         tc_fence_after_sync();
-        const float4* const l4 = reinterpret_cast<const float4*>(lse);
-        if (now == 128 && !__any_sync(0xffffffffu, lo > 0)) {
-          uint32_t sr[128];
-          tmem_ld32x128_wait(tS, sr);
-          tc_fence_before_sync();
-          mbar_arrive(bar_s_free0 + 8 * buf);  // S^T is in registers: the buffer may be filled again
+        if (now > 16) {
+          // 32 columns of both tiles at a time. `masked`: a warp asks which of a tile's
+          // columns its keys are seen from, and only where some are and some are not it
+          // asks each. (Where the second tile has no position its columns are anything:
+          // not written.)
+          auto chunk = [&](int c0, auto masked) {
+            uint32_t sr[64];
+            tmem_ld32x32_two_wait(tS + c0, tS + 128 + c0, sr);
+            if (c0 + 32 >= now) {
+              tc_fence_before_sync();
+              mbar_arrive(bar_free);  // S^T is in registers: the buffers may be filled again
+            }
+            auto add = [&](int t, int lo, float(&acc)[4], auto each) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float4 l = l4[i];
-            float x0, x1, x2, x3;
-            ffma2(x0, x1, __uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1]), c, l.x, l.y);
-            ffma2(x2, x3, __uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3]), c, l.z, l.w);
-            fadd2_acc(acc[4 * (i & 1)], acc[4 * (i & 1) + 1], ex2_approx(x0), ex2_approx(x1));
-            fadd2_acc(acc[4 * (i & 1) + 2], acc[4 * (i & 1) + 3], ex2_approx(x2), ex2_approx(x3));
+              for (int i = 0; i < 8; ++i) {
+                const float4 l = l4[c0 / 4 + i];
+                const uint32_t* const x = sr + 32 * t + 4 * i;
+                float w[4];
+                ffma2(w[0], w[1], __uint_as_float(x[0]), __uint_as_float(x[1]), c, l.x, l.y);
+                ffma2(w[2], w[3], __uint_as_float(x[2]), __uint_as_float(x[3]), c, l.z, l.w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  w[j] = ex2_approx(w[j]);
+                  if constexpr (each.value) {
+                    const int col = c0 + 4 * i + j;
+                    if (col < lo || col >= now) w[j] = 0.f;
+                  }
+                }
+                fadd2_acc(acc[0], acc[1], w[0], w[1]);
+                fadd2_acc(acc[2], acc[3], w[2], w[3]);
+              }
+            };
+            if constexpr (!masked.value) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {  // both tiles with one read of the factors
+                const float4 l = l4[c0 / 4 + i];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  float(&acc)[4] = t == 0 ? acc0 : acc1;
+                  const uint32_t* const x = sr + 32 * t + 4 * i;
+                  float x0, x1, x2, x3;
+                  ffma2(x0, x1, __uint_as_float(x[0]), __uint_as_float(x[1]), c, l.x, l.y);
+                  ffma2(x2, x3, __uint_as_float(x[2]), __uint_as_float(x[3]), c, l.z, l.w);
+                  fadd2_acc(acc[0], acc[1], ex2_approx(x0), ex2_approx(x1));
+                  fadd2_acc(acc[2], acc[3], ex2_approx(x2), ex2_approx(x3));
+                }
+              }
+            } else {
+              const bool whole = c0 + 32 <= now;
+              if (whole && __all_sync(0xffffffffu, lo0 <= c0)) add(0, lo0, acc0, std::false_type{});
+              else if (__any_sync(0xffffffffu, lo0 < c0 + 32)) add(0, lo0, acc0, std::true_type{});
+              if (whole && __all_sync(0xffffffffu, lo1 <= c0)) add(1, lo1, acc1, std::false_type{});
+              else if (__any_sync(0xffffffffu, lo1 < c0 + 32)) add(1, lo1, acc1, std::true_type{});
+            }
+          };
+          if (now == 128 && !__any_sync(0xffffffffu, lo1 > 0)) {
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 32) chunk(c0, std::false_type{});
+          } else {
+#pragma unroll 1
+            for (int c0 = 0; c0 < now; c0 += 32) chunk(c0, std::true_type{});
           }
         } else {
           // eight columns at a time: single tokens' blocks have few
-#pragma unroll 1
-          for (int c0 = 0; c0 < now; c0 += 8) {
+          auto some = [&](uint32_t from, int c0, int lo, float (&acc)[4]) {
             uint32_t sr[8];
-            tmem_ld32x8_wait(tS + c0, sr);
+            tmem_ld32x8_wait(from + c0, sr);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float4 l = l4[c0 / 4 + i];
@@ -596,28 +690,57 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 4; ++j) {
                 const int col = c0 + 4 * i + j;
                 const float w = ex2_approx(fmaf(__uint_as_float(sr[4 * i + j]), c, x[j]));
-                acc[4 * i + j] += col >= lo && col < now ? w : 0.f;
+                acc[j] += col >= lo && col < now ? w : 0.f;
               }
             }
+          };
+#pragma unroll 1
+          for (int c0 = 0; c0 < now; c0 += 8) {
+            some(tS, c0, lo0, acc0);
+            if (two) some(tS + 128, c0, lo1, acc1);
           }
           tc_fence_before_sync();
-          mbar_arrive(bar_s_free0 + 8 * buf);
+          mbar_arrive(bar_free);
         }
       }
       if (!ok) break;
-      float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+      laid_b = u.b;  // (asked only where one block is all)
+      laid_head = u.head;
+      float sum0 = (acc0[0] + acc0[1]) + (acc0[2] + acc0[3]), sum1 = (acc1[0] + acc1[1]) + (acc1[2] + acc1[3]);
+      if (steps > 1) {  // the other warpgroup had steps too
+        if (!finishes) {
+          bool got = wait_bounded(bar_taken0 + 8 * wg, taken_ph, wd, kSiteWeighTaken);
+          got = __all_sync(0xffffffffu, got);
+          if (!got) break;
+          taken_ph ^= 1u;
+          part[wg * 128] = make_float2(sum0, sum1);
+          mbar_arrive(bar_part0 + 8 * wg);
+          continue;
+        }
+        const uint32_t other = wg ^ 1u;
+        bool got = wait_bounded(bar_part0 + 8 * other, part_ph, wd, kSiteWeighPart);
+        got = __all_sync(0xffffffffu, got);
+        if (!got) break;
+        part_ph ^= 1u;
+        const float2 theirs = part[other * 128];
+        sum0 += theirs.x;
+        sum1 += theirs.y;
+        mbar_arrive(bar_taken0 + 8 * other);
+      }
       if (!owner) {
-        // not the unit's first blocks: the sum to their holder
-        __stcg(p.ws_sums + (static_cast<size_t>(blockIdx.x) * 2 + t) * kKeys + key_lane, sum);
+        // not the unit's first blocks: the sums to their holder
+        float* const ws = p.ws_sums + static_cast<size_t>(blockIdx.x) * kUnitKeys + key_lane;
+        __stcg(ws, sum0);
+        __stcg(ws + kKeys, sum1);
         __threadfence();
-        mbar_arrive(bar_part0 + 8 * t);
+        mbar_arrive(bar_flag);
         if (key_lane < 32) {
-          bool done = wait_bounded(bar_part0 + 8 * t, part_ph, wd, kSiteWeighPart);
+          bool done = wait_bounded(bar_flag, flag_ph, wd, kSiteWeighPart);
           done = __all_sync(0xffffffffu, done);
           if (!done) break;
-          if (lane == 0) store_release(p.ws_flags + static_cast<size_t>(blockIdx.x) * 2 + t, p.epoch);
+          if (lane == 0) store_release(p.ws_flags + blockIdx.x, p.epoch);
         }
-        part_ph ^= 1u;
+        flag_ph ^= 1u;
         continue;
       }
       if (u.end < u.blocks) {  // others hold the rest: this is the share's last segment
@@ -626,24 +749,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (last + 1 < start->shares && weigh_share_begin(*start, last + 1) < rest_end) ++last;
         bool fine = true;
         for (int cb = blockIdx.x + 1 + lane; cb <= last && fine; cb += 32)
-          fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSiteWeighFlag);
+          fine = wait_flag(p.ws_flags + cb, p.epoch, wd, kSiteWeighFlag);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
         __syncwarp();  // what one lane acquired is visible to all
-        for (int cb = blockIdx.x + 1; cb <= last; ++cb)
-          sum += __ldcg(p.ws_sums + (static_cast<size_t>(cb) * 2 + t) * kKeys + key_lane);
+        for (int cb = blockIdx.x + 1; cb <= last; ++cb) {
+          const float* ws = p.ws_sums + static_cast<size_t>(cb) * kUnitKeys + key_lane;
+          sum0 += __ldcg(ws);
+          sum1 += __ldcg(ws + kKeys);
+        }
         // every thread has seen the flags: taken back, so that a replay of a captured
         // launch, which carries the same tag, does not find them
-        mbar_arrive(bar_part0 + 8 * t);
+        mbar_arrive(bar_flag);
         if (key_lane < 32) {
-          bool seen = wait_bounded(bar_part0 + 8 * t, part_ph, wd, kSiteWeighPart);
+          bool seen = wait_bounded(bar_flag, flag_ph, wd, kSiteWeighPart);
           seen = __all_sync(0xffffffffu, seen);
           if (!seen) break;
-          for (int cb = blockIdx.x + 1 + lane; cb <= last; cb += 32) p.ws_flags[static_cast<size_t>(cb) * 2 + t] = 0ull;
+          for (int cb = blockIdx.x + 1 + lane; cb <= last; cb += 32) p.ws_flags[cb] = 0ull;
         }
-        part_ph ^= 1u;
+        flag_ph ^= 1u;
       }
-      if (to >= 0) p.out[to] = old + sum;
+      auto place = [&](int page, int k) {
+        return ((static_cast<long long>(page) * p.heads + u.head) << p.page_shift) + (k & ((1 << p.page_shift) - 1));
+      };
+      const bool there0 = page_ok(p, page0), there1 = page_ok(p, page1);
+      const long long to0 = place(page0, key), to1 = place(page1, key + kKeys);
+      const float old0 = there0 && p.in ? p.in[to0] : 0.f, old1 = there1 && p.in ? p.in[to1] : 0.f;
+      if (there0) p.out[to0] = old0 + sum0;
+      if (there1) p.out[to1] = old1 + sum1;
     }
   }
 
