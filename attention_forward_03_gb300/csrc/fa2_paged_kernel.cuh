@@ -154,12 +154,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto has_page = [&](int j) { return lane * p.page_rows < kKeys && position(j) < w.keys; };
       auto entry = [&](int j) { return j < w.kv_end && has_page(j) ? paged_entry(p, w.b, position(j)) : -1; };
       auto load_tile = [&](const CUtensorMap* map, int j, int page, uint32_t is_v) -> bool {
-        bool free = lane != 0 || wait_bounded(bar_empty(slot), ring_ph ^ 1u, wd, kSiteLoadRingEmpty, true, kNapNs);
-        free = __all_sync(0xffffffffu, free);
-        if (!free) return false;
         const uint32_t full = bar_full(slot, is_v);
         const uint32_t dst = sRing + static_cast<uint32_t>(slot * L::kTileBytes + lane * p.page_rows * 128);
-        const bool mine = has_page(j), there = mine && page_ok(p, page);
+        const bool mine = has_page(j), there = mine && page_ok(p, page), load = mine && (there || is_v);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * page_bytes;
+        const int at = position(j) & in_page, from = there ? page : p.pages;
+        // every lane waits: each may go on by itself then (a box may land before lane 0
+        // has announced it: the phase still lacks that arrival)
+        const bool free = wait_bounded(bar_empty(slot), ring_ph ^ 1u, wd, kSiteLoadRingEmpty, true, kNapNs);
+        if (!__all_sync(0xffffffffu, free)) return false;
         if (mine && !there && !is_v) {  // no such page: its scores are NaN
           for (int pn = 0; pn < L::kPanels; ++pn)
             for (int r = 0; r < p.page_rows * 8; ++r)
@@ -167,15 +170,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                            0x7fff7fffu, 0x7fff7fffu);
           fence_proxy_async_shared();
         }
-        const bool load = mine && (there || is_v);
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, load));
+        __syncwarp();
         if (!(p.test_withhold && issued == 0)) {  // test hook: the first tile never arrives
-          if (lane == 0) mbar_arrive_expect_tx(full, boxes * page_bytes);
-          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
           if (load)
             for (int pn = 0; pn < L::kPanels; ++pn)
-              tma_load_4d_hint(dst + static_cast<uint32_t>(pn * kPanelBytes), map, full, pn * 64,
-                               position(j) & in_page, w.head, there ? page : p.pages, keep);
+              tma_load_4d_hint(dst + static_cast<uint32_t>(pn * kPanelBytes), map, full, pn * 64, at, w.head, from, keep);
         }
         types = (types & ~(1u << slot)) | (is_v << slot);
         if (is_v) vbits ^= 1u << slot; else kbits ^= 1u << slot;
@@ -533,20 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         base2 = nbase;
       }
       const float inv = l > 0.f ? __frcp_rn(l_o) : 0.f;
-#pragma unroll 1
-      for (int cc = 0; cc < D; cc += 32) {
-        uint32_t o[32];
-        tmem_ld32x32_wait(tO + cc, o);
-        float of[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]) * a_own;
-        for (int cb = first_c; cb <= last_c; ++cb) {
-          const size_t slot = static_cast<size_t>(cb) * 2 + t;
-          const float bc = __ldcg(p.ws_stats + slot * 3 * 128 + rr), a = bc == -CUDART_INF_F ? 0.f : ex2_approx(bc - nbase);
-          const float* po = p.ws_o + slot * D * 128;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) of[i] = fmaf(a, __ldcg(po + (cc + i) * 128 + rr), of[i]);
-        }
+      // 32 columns of the finished rows into the staged tile
+      auto stage = [&](int cc, const float (&of)[32]) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t pk[4];
@@ -555,6 +543,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c8 = cc / 8 + q;
           st_shared_v4(p_row + static_cast<uint32_t>((c8 >> 3) * kPanelBytes) + ((static_cast<uint32_t>(c8 & 7) ^ p_xor) << 4),
                        pk[0], pk[1], pk[2], pk[3]);
+        }
+      };
+      if (last_c < first_c) {
+#pragma unroll
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o[32];
+          tmem_ld32x32_wait(tO + cc, o);
+          float of[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]);
+          stage(cc, of);
+        }
+      } else {
+        // Partial results, 32 columns of one at a time, the next ones under way meanwhile
+        // (each waited for by itself: 8 us for one partial result at D = 128).
+        float part[32];
+        auto fetch = [&](int cc, int cb) {
+          const float* po = p.ws_o + ((static_cast<size_t>(cb) * 2 + t) * D + cc) * 128 + rr;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[i] = __ldcg(po + i * 128);
+        };
+        fetch(0, first_c);
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 32) {
+          uint32_t o[32];
+          tmem_ld32x32_wait(tO + cc, o);
+          float of[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]) * a_own;
+#pragma unroll 1
+          for (int cb = first_c; cb <= last_c; ++cb) {
+            const float bc = __ldcg(p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128 + rr);
+            const float a = bc == -CUDART_INF_F ? 0.f : ex2_approx(bc - nbase);
+            float now[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) now[i] = part[i];
+            if (cb < last_c) fetch(cc, cb + 1);
+            else if (cc + 32 < D) fetch(cc + 32, first_c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) of[i] = fmaf(a, now[i], of[i]);
+          }
+          stage(cc, of);
         }
       }
       // O_t is read out; the next segment's first P.V may overwrite it once this
@@ -565,13 +595,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           live ? (static_cast<long long>(w.t0 + token) * p.heads + w.head) * p.group + row_head : -1ll;
       __syncwarp();
       constexpr int kChunks = D / 8;
-#pragma unroll 4
+      uint4 chunk[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int at = i * 32 + lane, r = at / kChunks, ch = at - r * kChunks;
+        chunk[i] = *reinterpret_cast<const uint4*>(smem + L::kPOffset + t * L::kPBytes + (ch >> 3) * kPanelBytes +
+                                                   (wr * 32 + r) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+      }
+#pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int at = i * 32 + lane, r = at / kChunks, ch = at - r * kChunks;
         const long long to = __shfl_sync(0xffffffffu, out_row, r);
-        const uint8_t* from = smem + L::kPOffset + t * L::kPBytes + (ch >> 3) * kPanelBytes + (wr * 32 + r) * 128 +
-                              (((ch & 7) ^ (r & 7)) << 4);
-        if (to >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + to * D)[ch] = *reinterpret_cast<const uint4*>(from);
+        if (to >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + to * D)[ch] = chunk[i];
       }
       __syncwarp();  // read before the next segment's P is written there
       if (live) p.lse[out_row] = l != 0.f ? (base2 + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;  // NaN stays

@@ -3,6 +3,8 @@
 // units whose number of K/V tiles depends on the sequence and, under the causal
 // mask, on the unit's last token.
 #pragma once
+#include <climits>
+
 #include "fa2_paged.cuh"
 
 namespace fa2 {
@@ -31,6 +33,27 @@ __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned 
     m = a;
     a = t;
   }
+}
+
+// The same with m = 128. Steps of a power of two below it (those of 1, 2, 4, ..
+// query heads to a key head) need no division: every CTA takes this sum several
+// times before its first load.
+__device__ __forceinline__ long long floor_sum128(unsigned n, unsigned a, unsigned b) {
+  if ((a & 127u) == 0) {
+    // whole parts alone
+    return static_cast<long long>(n) * (n - 1) / 2 * (a >> 7) + static_cast<long long>(n) * (b >> 7);
+  }
+  if (a < 128u && (a & (a - 1u)) == 0) {
+    // floor((a i + b) / 128) = floor((i + b / a) / k), k = 128 / a: sums of floor(i / k) from 0
+    const int shift = 7 - (31 - __clz(a));  // log2 k
+    auto upto = [&](unsigned x) {
+      const long long t = x >> shift;
+      return (t * (t - 1) / 2 << shift) + t * (x - (static_cast<unsigned>(t) << shift));
+    };
+    const unsigned from = b >> (7 - shift);
+    return upto(from + n) - upto(from);
+  }
+  return floor_sum(n, 128u, a, b);
 }
 
 struct PagedUnits {  // of one sequence
@@ -76,81 +99,102 @@ __device__ __forceinline__ long long steps_before(const PagedTileParams& p, cons
     tiles += none;
     full -= none;
     if (full > 0)
-      tiles += floor_sum(static_cast<unsigned>(full), kKeys, static_cast<unsigned>(per),
-                         static_cast<unsigned>(c + (none + 1) * per + kKeys - 1));
+      tiles += floor_sum128(static_cast<unsigned>(full), static_cast<unsigned>(per),
+                            static_cast<unsigned>(c + (none + 1) * per + kKeys - 1));
   }
   return tiles + static_cast<long long>(m) * kPagedUnitCost;
 }
 
+// a / b for b > 0; in 32 bits where that is enough (most calls; a 64-bit division
+// is a routine of its own, fetched by every CTA).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b));
+}
+
 // Where this CTA's share begins, found once per CTA.
 struct PagedStart {
-  long long total;  // steps of the whole call
-  int shares;       // CTAs with a share
+  long long total;       // steps of the whole call
+  long long begin, end;  // this CTA's share of them
+  int shares;            // CTAs with a share
   int b, head, unit;
   int from;         // steps of that unit before the share
 };
 
 __device__ __forceinline__ long long paged_share_begin(const PagedStart& st, int c) {
-  return c >= st.shares ? st.total : st.total * c / st.shares;
+  return c >= st.shares ? st.total : quotient(st.total * c, st.shares);
+}
+
+// Which batch entry holds step `want`, by one whole warp: `steps(b)` are the
+// steps of entry b; *before: those of the entries before it, *mine: its own.
+// `first`: steps(lane), which the caller has taken already.
+template <typename F>
+__device__ __forceinline__ int find_entry(int B, long long want, long long first, F&& steps, long long* before,
+                                          long long* mine) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const long long here = b0 == 0 ? first : (b0 + lane < B ? steps(b0 + lane) : 0);
+    long long upto = here;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, sum + upto > want);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      *before = sum + __shfl_sync(0xffffffffu, upto - here, l);
+      *mine = __shfl_sync(0xffffffffu, here, l);
+      return b0 + l;
+    }
+    sum += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  *before = *mine = 0;
+  return 0;  // only should the tables have changed meanwhile
 }
 
 // By one whole warp.
 __device__ __forceinline__ PagedStart paged_start(const PagedTileParams& p) {
   PagedStart st = {};
   const int lane = threadIdx.x & 31;
-  long long sum = 0;
-  for (int b = lane; b < p.B; b += 32) {
+  auto steps = [&](int b) {
     const PagedUnits u = paged_units(p, b);
-    if (u.units) sum += p.heads * steps_before(p, u, u.units);
-  }
+    return u.units ? p.heads * steps_before(p, u, u.units) : 0ll;
+  };
+  const long long first = lane < p.B ? steps(lane) : 0;
+  long long sum = first;
+  for (int b = lane + 32; b < p.B; b += 32) sum += steps(b);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   st.total = sum;
   st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), sum));
   if (static_cast<int>(blockIdx.x) >= st.shares) return st;
-  const long long want = paged_share_begin(st, blockIdx.x);
-  long long before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    long long mine = 0;
-    if (b < p.B) {
-      const PagedUnits u = paged_units(p, b);
-      if (u.units) mine = p.heads * steps_before(p, u, u.units);
-    }
-    long long upto = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      st.b = b0 + l;
-      before += __shfl_sync(0xffffffffu, upto - mine, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
+  st.begin = paged_share_begin(st, blockIdx.x);
+  st.end = paged_share_begin(st, blockIdx.x + 1);
+  long long before, mine;
+  st.b = find_entry(p.B, st.begin, first, steps, &before, &mine);
   const PagedUnits u = paged_units(p, st.b);
-  if (u.units == 0) {  // only should the tables have changed meanwhile
-    st.shares = 0;
+  if (u.units == 0 || mine == 0) {  // only should the tables have changed meanwhile
+    st.end = st.begin;
     return st;
   }
-  const long long per_head = steps_before(p, u, u.units);
-  long long r = want - before;
-  st.head = static_cast<int>(min(r / per_head, p.heads - 1ll));
+  const long long per_head = quotient(mine, p.heads);
+  long long r = st.begin - before;
+  st.head = static_cast<int>(min(quotient(r, per_head), p.heads - 1ll));
   r -= st.head * per_head;
   // the last unit that starts at or before step r, 32 candidates at a time
   int lo = 0, hi = u.units;
+  long long at = 0;  // steps before unit lo
   while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, m = lo + (lane + 1) * step;
-    const bool ok = m < hi && steps_before(p, u, m) <= r;
-    lo += __popc(__ballot_sync(0xffffffffu, ok)) * step;
-    hi = min(hi, lo + step);
+    const int by = (hi - lo + 31) / 32, m = lo + (lane + 1) * by;
+    const long long s = m < hi ? steps_before(p, u, m) : LLONG_MAX;
+    const int n = __popc(__ballot_sync(0xffffffffu, s <= r));
+    if (n > 0) at = __shfl_sync(0xffffffffu, s, n - 1);
+    lo += n * by;
+    hi = min(hi, lo + by);
   }
   st.unit = lo;
-  st.from = static_cast<int>(r - steps_before(p, u, lo));
+  st.from = static_cast<int>(r - at);
   return st;
 }
 
@@ -175,8 +219,8 @@ __device__ __forceinline__ PagedCursor paged_first(const PagedTileParams& p, con
   c.head = st.head;
   c.unit = st.unit;
   c.from = st.from;
-  c.step = paged_share_begin(st, blockIdx.x);
-  c.end = paged_share_begin(st, blockIdx.x + 1);
+  c.step = st.begin;
+  c.end = st.end;
   c.u = paged_units(p, st.b);
   return c;
 }

@@ -138,68 +138,51 @@ struct WeighStart {
 };
 
 __device__ __forceinline__ long long weigh_share_begin(const WeighStart& st, int c) {
-  return c >= st.shares ? st.total : st.total * c / st.shares;
+  return c >= st.shares ? st.total : quotient(st.total * c, st.shares);
 }
 
 // By one whole warp.
 __device__ __forceinline__ WeighStart weigh_start(const PagedWeighParams& p) {
   WeighStart st = {};
   const int lane = threadIdx.x & 31;
-  long long sum = 0;
-  for (int b = lane; b < p.B; b += 32) {
+  auto steps = [&](int b) {
     const WeighSeq w = weigh_seq(p, b);
-    sum += p.heads * weigh_before(p, w, w.units);
-  }
+    return p.heads * weigh_before(p, w, w.units);
+  };
+  const long long first = lane < p.B ? steps(lane) : 0;
+  long long sum = first;
+  for (int b = lane + 32; b < p.B; b += 32) sum += steps(b);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   st.total = sum;
   st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), sum));
   if (static_cast<int>(blockIdx.x) >= st.shares) return st;
-  const long long want = weigh_share_begin(st, blockIdx.x);
-  st.begin = want;
+  st.begin = weigh_share_begin(st, blockIdx.x);
   st.end = weigh_share_begin(st, blockIdx.x + 1);
-  long long before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    long long mine = 0;
-    if (b < p.B) {
-      const WeighSeq w = weigh_seq(p, b);
-      mine = p.heads * weigh_before(p, w, w.units);
-    }
-    long long upto = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      st.b = b0 + l;
-      before += __shfl_sync(0xffffffffu, upto - mine, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
+  long long before, mine;
+  st.b = find_entry(p.B, st.begin, first, steps, &before, &mine);
   const WeighSeq w = weigh_seq(p, st.b);
-  if (w.units == 0) {  // only should the tables have changed meanwhile
+  if (w.units == 0 || mine == 0) {  // only should the tables have changed meanwhile
     st.end = st.begin;
     return st;
   }
-  const long long per_head = weigh_before(p, w, w.units);
-  long long r = want - before;
-  st.head = static_cast<int>(min(r / per_head, p.heads - 1ll));
+  const long long per_head = quotient(mine, p.heads);
+  long long r = st.begin - before;
+  st.head = static_cast<int>(min(quotient(r, per_head), p.heads - 1ll));
   r -= st.head * per_head;
   // the last unit that begins at or before step r, 32 candidates at a time
   int lo = 0, hi = w.units;
+  long long at = 0;  // steps before unit lo
   while (hi - lo > 1) {
     const int by = (hi - lo + 31) / 32, m = lo + (lane + 1) * by;
-    const bool ok = m < hi && weigh_before(p, w, m) <= r;
-    lo += __popc(__ballot_sync(0xffffffffu, ok)) * by;
+    const long long s = m < hi ? weigh_before(p, w, m) : LLONG_MAX;
+    const int n = __popc(__ballot_sync(0xffffffffu, s <= r));
+    if (n > 0) at = __shfl_sync(0xffffffffu, s, n - 1);
+    lo += n * by;
     hi = min(hi, lo + by);
   }
   st.unit = lo;
-  st.from = static_cast<int>(r - weigh_before(p, w, lo));
+  st.from = static_cast<int>(r - at);
   return st;
 }
 
