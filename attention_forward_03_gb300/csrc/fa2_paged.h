@@ -63,6 +63,7 @@ cudaError_t launch_paged_rows(int D, bool bf16, const CUtensorMap& k, const CUte
 struct PagedTileParams : PagedAttnParams {
   int sub_tokens;   // tokens of a sub-tile: 128 / group
   int page_rows;    // positions of a page in one K/V tile: min(page size, 128)
+  int wide;         // head dimension above 64
 };
 template <int D, bool kBf16>
 cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,

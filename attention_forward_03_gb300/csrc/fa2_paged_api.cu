@@ -308,6 +308,7 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   CUtensorMap mq, mk, mv;
   p.sub_tokens = kRows / group;
   p.page_rows = std::min(page_size, kKeys);
+  p.wide = D > 64;
   if (!encode_query_map(&mq, Q, p.q_token, p.q_head, T, Hq, D, dtype, group, p.sub_tokens) ||
       !encode_cache_map(&mk, k_cache, ks, z, p.page_rows) || !encode_cache_map(&mv, v_cache, vs, z, p.page_rows))
     return record_cuda_error(cudaErrorInvalidValue);

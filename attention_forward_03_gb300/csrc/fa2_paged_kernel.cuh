@@ -20,7 +20,10 @@
 //             counts them in closed form.
 //   output    through the warp's own rows of the P buffer (its own buffer where
 //             P lives in tensor memory), so that a row's 256 bytes go out
-//             together; rows of a next sequence may follow, so no box is stored.
+//             together, 16-byte chunks by neighbouring lanes; rows of a next
+//             sequence may follow, so no box of rows is stored. (Boxes of a
+//             warp's 32 rows, where they are whole tokens of the sequence, made
+//             no difference: 222 and 220 us for four prompts of 4096.)
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -65,6 +68,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa2_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const PagedTileParams p) {
   using L = PagedLayout<D>;
+  // issuers by instruction type (one thread for every S, one for every P.V) or by
+  // sub-tile: as in fa2_kernel.cuh
+  constexpr bool kTypeSplit = L::kPanels == 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -93,11 +99,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 32) {
     mbar_init(bar_q_full, 1);
-    mbar_init(bar_q_empty, 1);
+    mbar_init(bar_q_empty, kTypeSplit ? 1 : 2);
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(bar_full(s, 0u), 1);
       mbar_init(bar_full(s, 1u), 1);
-      mbar_init(bar_empty(s), 1);
+      mbar_init(bar_empty(s), kTypeSplit ? 1 : 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s_full0 + 8 * t, 1);
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp < kMmaWarp + kIssuers) {
-      // ------------------------------------- MMA issuers: 0 every S, 1 every P.V
+      // ------------------------------------------------------ MMA issuers
       if (lane == 0) {
         const int me = warp - kMmaWarp;
         constexpr uint32_t idesc_s = make_idesc_f16(kBf16, kKeys, false);
@@ -266,62 +272,118 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto k_index = [](int j, int b) { return j == b ? 0 : 2 * (j - b) - 1; };
         auto v_index = [](int j, int b, int e) { return j == e - 1 ? 2 * (j - b) + 1 : 2 * (j - b) + 2; };
-        uint32_t bits = 0u;  // parity of the next use of each slot's full barrier of this issuer's type
+        uint32_t bits[2] = {0u, 0u};  // [type]: parity of the next use of each slot's full barrier
         auto take = [&](uint32_t idx, uint32_t is_v) -> int {
           const int s = static_cast<int>(idx % L::kStages);
-          const uint32_t par = (bits >> s) & 1u;
-          bits ^= 1u << s;
+          const uint32_t par = (bits[is_v] >> s) & 1u;
+          bits[is_v] ^= 1u << s;
           return wait_bounded(bar_full(s, is_v), par, wd, kSiteMmaRingFull, true, kNapNs) ? s : -1;
         };
+        // The unit's last tile may be short: its rows behind the keys up to the last
+        // product's 16 are zeroed, the products beyond left out.
+        auto clean_v = [&](const PagedSegment& u, int j, int slot) -> int {
+          const int valid = u.keys - j * kKeys;
+          cross_zero_rows(sRing + static_cast<uint32_t>(slot * L::kTileBytes), L::kPanels, valid);
+          return cross_key_steps(valid);
+        };
+        auto full_end = [](const PagedSegment& u, int e) { return e == u.nkv && u.keys < e * kKeys ? e - 1 : e; };
         uint32_t base_idx = 0;  // global load index of the current segment's first tile
         bool ok = true;
         PagedCursor cur = paged_first(p, *start);
         PagedSegment w;
-        if (me == 0) {
-          uint32_t q_round = 0, s_free_ph[2] = {0u, 0u};
-          bool s_out[2] = {false, false};  // an S issued whose TMEM the softmax has not released yet
+        if constexpr (kTypeSplit) {
+          if (me == 0) {
+            uint32_t q_round = 0, s_free_ph[2] = {0u, 0u};
+            bool s_out[2] = {false, false};  // an S issued whose TMEM the softmax has not released yet
+            while (ok && paged_next(cur, w, p)) {
+              const int b = w.kv_begin, e = w.kv_end;
+              const int n_sub = live_subtiles(w);
+              if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) break;
+              ++q_round;
+              for (int j = b; j < e && ok; ++j) {
+                const int slot_k = take(base_idx + k_index(j, b), 0u);
+                if (slot_k < 0) { ok = false; break; }
+                for (int t = 0; t < n_sub; ++t) {
+                  if (s_out[t]) {
+                    if (!wait_bounded(bar_s_free0 + 8 * t, s_free_ph[t], wd, kSiteMmaSFree, true, kNapNs)) { ok = false; break; }
+                    s_free_ph[t] ^= 1u;
+                  }
+                  tc_fence_after_sync();
+                  issue_s(t, slot_k);
+                  mma_commit(bar_s_full0 + 8 * t);
+                  s_out[t] = true;
+                }
+                if (!ok) break;
+                mma_commit(bar_empty(slot_k));
+                if (j == e - 1) mma_commit(bar_q_empty);
+              }
+              base_idx += 2u * static_cast<uint32_t>(e - b);
+            }
+          } else {
+            uint32_t p_full_ph[2] = {0u, 0u};
+            while (ok && paged_next(cur, w, p)) {
+              const int b = w.kv_begin, e = w.kv_end;
+              const int n_sub = live_subtiles(w);
+              auto tile = [&](int j, auto tail) {
+                const int slot_v = take(base_idx + v_index(j, b, e), 1u);
+                if (slot_v < 0) { ok = false; return; }
+                int steps = kKeys / 16;
+                if constexpr (tail.value) steps = clean_v(w, j, slot_v);
+                for (int t = 0; t < n_sub; ++t) {
+                  if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
+                  p_full_ph[t] ^= 1u;
+                  tc_fence_after_sync();
+                  issue_pv(t, slot_v, j > b, tail, steps);
+                  mma_commit(bar_p_free0 + 8 * t);
+                  if (j == e - 1) mma_commit(bar_o_full0 + 8 * t);
+                }
+                mma_commit(bar_empty(slot_v));
+              };
+              const int e_full = full_end(w, e);
+              for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
+              if (e_full < e && ok) tile(e_full, std::true_type{});
+              base_idx += 2u * static_cast<uint32_t>(e - b);
+            }
+          }
+        } else {
+          // One issuer per sub-tile t = me: S_t one tile ahead of P.V_t, each S as soon as
+          // its K tile has landed and the softmax has loaded the sub-tile's S before, each
+          // P.V as soon as its V tile has landed and the softmax has published P_t. A
+          // sub-tile without tokens: nothing but the slots' release.
+          const int t = me;
+          uint32_t q_round = 0, s_free_ph = 0, p_full_ph = 0;
+          bool s_out = false;
           while (ok && paged_next(cur, w, p)) {
             const int b = w.kv_begin, e = w.kv_end;
-            const int n_sub = live_subtiles(w);
+            const bool live = t < live_subtiles(w);
             if (!wait_bounded(bar_q_full, q_round & 1u, wd, kSiteMmaQFull, true, kNapNs)) break;
             ++q_round;
-            for (int j = b; j < e && ok; ++j) {
+            auto next_s = [&](int j) -> bool {
               const int slot_k = take(base_idx + k_index(j, b), 0u);
-              if (slot_k < 0) { ok = false; break; }
-              for (int t = 0; t < n_sub; ++t) {
-                if (s_out[t]) {
-                  if (!wait_bounded(bar_s_free0 + 8 * t, s_free_ph[t], wd, kSiteMmaSFree, true, kNapNs)) { ok = false; break; }
-                  s_free_ph[t] ^= 1u;
+              if (slot_k < 0) return false;
+              if (live) {
+                if (s_out) {
+                  if (!wait_bounded(bar_s_free0 + 8 * t, s_free_ph, wd, kSiteMmaSFree, true, kNapNs)) return false;
+                  s_free_ph ^= 1u;
                 }
                 tc_fence_after_sync();
                 issue_s(t, slot_k);
                 mma_commit(bar_s_full0 + 8 * t);
-                s_out[t] = true;
+                s_out = true;
               }
-              if (!ok) break;
               mma_commit(bar_empty(slot_k));
-              if (j == e - 1) mma_commit(bar_q_empty);
-            }
-            base_idx += 2u * static_cast<uint32_t>(e - b);
-          }
-        } else {
-          uint32_t p_full_ph[2] = {0u, 0u};
-          while (ok && paged_next(cur, w, p)) {
-            const int b = w.kv_begin, e = w.kv_end;
-            const int n_sub = live_subtiles(w);
+              if (j + 1 == e) mma_commit(bar_q_empty);
+              return true;
+            };
             auto tile = [&](int j, auto tail) {
+              if (j + 1 < e && !next_s(j + 1)) { ok = false; return; }
               const int slot_v = take(base_idx + v_index(j, b, e), 1u);
               if (slot_v < 0) { ok = false; return; }
-              int steps = kKeys / 16;
-              if constexpr (tail.value) {
-                // rows behind the keys up to the last product's 16: zeros
-                const int valid = w.keys - j * kKeys;
-                steps = cross_key_steps(valid);
-                cross_zero_rows(sRing + static_cast<uint32_t>(slot_v * L::kTileBytes), L::kPanels, valid);
-              }
-              for (int t = 0; t < n_sub; ++t) {
-                if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph[t], wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
-                p_full_ph[t] ^= 1u;
+              if (live) {
+                int steps = kKeys / 16;
+                if constexpr (tail.value) steps = clean_v(w, j, slot_v);
+                if (!wait_bounded(bar_p_full0 + 8 * t, p_full_ph, wd, kSiteMmaPFull, true, kNapNs)) { ok = false; return; }
+                p_full_ph ^= 1u;
                 tc_fence_after_sync();
                 issue_pv(t, slot_v, j > b, tail, steps);
                 mma_commit(bar_p_free0 + 8 * t);
@@ -329,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               mma_commit(bar_empty(slot_v));
             };
-            // the unit's last tile may be short
-            const int e_full = e == w.nkv && w.keys < e * kKeys ? e - 1 : e;
+            if (!next_s(b)) break;
+            const int e_full = full_end(w, e);
             for (int j = b; j < e_full && ok; ++j) tile(j, std::false_type{});
             if (e_full < e && ok) tile(e_full, std::true_type{});
             base_idx += 2u * static_cast<uint32_t>(e - b);
@@ -370,7 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t >= live_subtiles(w)) continue;
       const int token = w.token + t * p.sub_tokens + row_token;
       const bool live = row_token < p.sub_tokens && token < w.n;
-      int limit = 0;  // this row's keys: [0, limit)
+      // this row's keys: [0, limit). A row without a token is anything and not written: it is
+      // not masked, so that it does not send its warp through the masks of every tile.
+      int limit = INT_MAX;
       if (live) limit = p.causal ? min(max(w.length - w.n + token + 1, 0), w.length) : w.length;
       float m_raw = -CUDART_INF_F;  // running max of the raw scores seen so far
       float base2 = -CUDART_INF_F;  // exponent base (log2 units) that l and O are relative to
@@ -407,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the base moves only when the max has passed it by 2^kRescaleLog2 (or on the first key)
         const float cand = m_raw * c;
         float alpha = 1.f;
-        if (m_raw != -CUDART_INF_F && (base2 == -CUDART_INF_F || cand - base2 > kRescaleLog2)) {
+        if (live && m_raw != -CUDART_INF_F && (base2 == -CUDART_INF_F || cand - base2 > kRescaleLog2)) {
           alpha = ex2_approx(base2 - cand);
           base2 = cand;
         }
@@ -501,7 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float a_own = 1.f, nbase = base2;
       int first_c = blockIdx.x + 1, last_c = blockIdx.x;  // partial holders [first_c, last_c]
       if (w.kv_end < w.nkv) {
-        while (last_c + 1 < start->shares && paged_share_begin(*start, last_c + 1) < w.unit_end) ++last_c;
+        if (start->parts) last_c += start->parts - 1 - start->part;
+        else
+          while (last_c + 1 < start->shares && paged_share_begin(*start, last_c + 1) < w.unit_end) ++last_c;
         bool fine = true;
         for (int cb = first_c + (rr & 31); cb <= last_c && fine; cb += 32)
           fine = wait_flag(p.ws_flags + static_cast<size_t>(cb) * 2 + t, p.epoch, wd, kSitePartialFlag);
@@ -518,17 +584,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int cb = first_c + rr; cb <= last_c; cb += 32) p.ws_flags[static_cast<size_t>(cb) * 2 + t] = 0ull;
         }
         part_phase ^= 1u;
-        for (int cb = first_c; cb <= last_c; ++cb)
-          nbase = fmaxf(nbase, __ldcg(p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128 + rr));
-        // 0 for a partial that saw no key (and for one of two: no difference of infinities)
-        a_own = base2 == -CUDART_INF_F ? 0.f : ex2_approx(base2 - nbase);
-        l *= a_own;
-        l_o *= a_own;
-        for (int cb = first_c; cb <= last_c; ++cb) {
-          const float* ps = p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128;
-          const float bc = __ldcg(ps + rr), a = bc == -CUDART_INF_F ? 0.f : ex2_approx(bc - nbase);
-          l += a * __ldcg(ps + 128 + rr);
-          l_o += a * __ldcg(ps + 256 + rr);
+        // their statistics, eight holders' loads under way at once (one holder after
+        // another: 25 us for 18 of them); 0 for a partial that saw no key
+#pragma unroll 1
+        for (int c0 = first_c; c0 <= last_c; c0 += 8) {
+          float bs[8], ls[8], los[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* ps = p.ws_stats + (static_cast<size_t>(min(c0 + i, last_c)) * 2 + t) * 3 * 128 + rr;
+            bs[i] = __ldcg(ps);
+            ls[i] = __ldcg(ps + 128);
+            los[i] = __ldcg(ps + 256);
+          }
+          float top = nbase;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, bs[i]);
+          const float scale = nbase == -CUDART_INF_F ? 0.f : ex2_approx(nbase - top);
+          a_own *= base2 == -CUDART_INF_F ? 0.f : scale;
+          l *= scale;
+          l_o *= scale;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = bs[i] == -CUDART_INF_F ? 0.f : ex2_approx(bs[i] - top);
+            if (c0 + i <= last_c) {
+              l = fmaf(a, ls[i], l);
+              l_o = fmaf(a, los[i], l_o);
+            }
+          }
+          nbase = top;
         }
         base2 = nbase;
       }
@@ -546,21 +629,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (last_c < first_c) {
+        if constexpr (D == 128) {
+          uint32_t o[128];
+          tmem_ld32x128_wait(tO, o);
 #pragma unroll
-        for (int cc = 0; cc < D; cc += 32) {
-          uint32_t o[32];
-          tmem_ld32x32_wait(tO + cc, o);
-          float of[32];
+          for (int cc = 0; cc < D; cc += 32) stage(cc, *reinterpret_cast<const float(*)[32]>(o + cc));
+        } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]);
-          stage(cc, of);
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32x32_wait(tO + cc, o);
+            stage(cc, *reinterpret_cast<const float(*)[32]>(o));
+          }
         }
       } else {
         // Partial results, 32 columns of one at a time, the next ones under way meanwhile
         // (each waited for by itself: 8 us for one partial result at D = 128).
-        float part[32];
+        float part[32], part_base;
         auto fetch = [&](int cc, int cb) {
           const float* po = p.ws_o + ((static_cast<size_t>(cb) * 2 + t) * D + cc) * 128 + rr;
+          part_base = __ldcg(p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128 + rr);
 #pragma unroll
           for (int i = 0; i < 32; ++i) part[i] = __ldcg(po + i * 128);
         };
@@ -574,13 +662,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) of[i] = __uint_as_float(o[i]) * a_own;
 #pragma unroll 1
           for (int cb = first_c; cb <= last_c; ++cb) {
-            const float bc = __ldcg(p.ws_stats + (static_cast<size_t>(cb) * 2 + t) * 3 * 128 + rr);
-            const float a = bc == -CUDART_INF_F ? 0.f : ex2_approx(bc - nbase);
+            const float a = part_base == -CUDART_INF_F ? 0.f : ex2_approx(part_base - nbase);
             float now[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) now[i] = part[i];
-            if (cb < last_c) fetch(cc, cb + 1);
-            else if (cc + 32 < D) fetch(cc + 32, first_c);
+            const bool more = cb < last_c;
+            if (more || cc + 32 < D) fetch(more ? cc : cc + 32, more ? cb + 1 : first_c);
 #pragma unroll
             for (int i = 0; i < 32; ++i) of[i] = fmaf(a, now[i], of[i]);
           }
@@ -590,23 +677,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O_t is read out; the next segment's first P.V may overwrite it once this
       // warpgroup publishes that segment's first P (ordered by bar_p).
       tc_fence_before_sync();
-      // the warp's rows, whole rows at a time: 16-byte chunks of a row by neighbouring lanes
       const long long out_row =
           live ? (static_cast<long long>(w.t0 + token) * p.heads + w.head) * p.group + row_head : -1ll;
+      // whole rows at a time: 16-byte chunks of a row by neighbouring lanes
       __syncwarp();
       constexpr int kChunks = D / 8;
-      uint4 chunk[kChunks];
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int at = i * 32 + lane, r = at / kChunks, ch = at - r * kChunks;
-        chunk[i] = *reinterpret_cast<const uint4*>(smem + L::kPOffset + t * L::kPBytes + (ch >> 3) * kPanelBytes +
-                                                   (wr * 32 + r) * 128 + (((ch & 7) ^ (r & 7)) << 4));
-      }
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < kChunks; ++i) {
         const int at = i * 32 + lane, r = at / kChunks, ch = at - r * kChunks;
         const long long to = __shfl_sync(0xffffffffu, out_row, r);
-        if (to >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + to * D)[ch] = chunk[i];
+        const uint8_t* from = smem + L::kPOffset + t * L::kPBytes + (ch >> 3) * kPanelBytes + (wr * 32 + r) * 128 +
+                              (((ch & 7) ^ (r & 7)) << 4);
+        if (to >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + to * D)[ch] = *reinterpret_cast<const uint4*>(from);
       }
       __syncwarp();  // read before the next segment's P is written there
       if (live) p.lse[out_row] = l != 0.f ? (base2 + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;  // NaN stays

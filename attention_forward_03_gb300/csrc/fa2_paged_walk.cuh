@@ -116,6 +116,7 @@ struct PagedStart {
   long long total;       // steps of the whole call
   long long begin, end;  // this CTA's share of them
   int shares;            // CTAs with a share
+  int parts, part;       // where every unit is `parts` CTAs': which part this one's is (0: equal shares)
   int b, head, unit;
   int from;         // steps of that unit before the share
 };
@@ -153,22 +154,79 @@ __device__ __forceinline__ int find_entry(int B, long long want, long long first
   return 0;  // only should the tables have changed meanwhile
 }
 
+// Whether and how to cut units when there are fewer than CTAs, all of about
+// `most` tiles: into how many parts each, or 0 for equal shares over all CTAs. In
+// tiles: a cut costs the way through memory, every part that the unit's first
+// holder adds to its own another, and shares that do not end where units do
+// make a CTA work on parts of two. The warp's lanes take a number of parts each.
+__device__ __forceinline__ int cut_parts(const PagedTileParams& p, long long tiles, int units, int most) {
+  const int lane = threadIdx.x & 31;
+  const float cut = 8.f, cut_equal = 5.f, join = p.wide ? 1.6f : 1.f;
+  const int parts = lane + 1;
+  float cost = 3e38f;
+  if (parts * units <= static_cast<int>(gridDim.x) && parts <= most)
+    cost = static_cast<float>((most + parts - 1) / parts) + (parts > 1 ? cut + join * static_cast<float>(parts - 1) : 0.f);
+  float best = cost;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, off));
+  const float shares = static_cast<float>(gridDim.x);
+  const float equal = static_cast<float>(tiles) / shares + cut_equal + join * ceilf(shares / static_cast<float>(units));
+  const int n = __ffs(__ballot_sync(0xffffffffu, cost == best));  // the fewest parts
+  return best < 3e38f && best <= equal ? n : 0;
+}
+
 // By one whole warp.
 __device__ __forceinline__ PagedStart paged_start(const PagedTileParams& p) {
   PagedStart st = {};
   const int lane = threadIdx.x & 31;
+  int units = 0, most = 0;  // of all sequences; the most tiles that a unit has
   auto steps = [&](int b) {
     const PagedUnits u = paged_units(p, b);
-    return u.units ? p.heads * steps_before(p, u, u.units) : 0ll;
+    if (!u.units) return 0ll;
+    units += u.units;
+    most = max(most, key_tiles(u.s.length));
+    return p.heads * steps_before(p, u, u.units);
   };
   const long long first = lane < p.B ? steps(lane) : 0;
+  const int first_units = units;
   long long sum = first;
   for (int b = lane + 32; b < p.B; b += 32) sum += steps(b);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  for (int off = 16; off > 0; off >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    units += __shfl_xor_sync(0xffffffffu, units, off);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+  }
   st.total = sum;
   st.shares = static_cast<int>(min(static_cast<long long>(gridDim.x), sum));
   if (static_cast<int>(blockIdx.x) >= st.shares) return st;
+  const long long all = static_cast<long long>(units) * p.heads, tiles = sum - all * kPagedUnitCost;
+  // fewer units than CTAs, and all about as long as the longest
+  if (all < gridDim.x && 10 * tiles >= 9 * all * most) st.parts = cut_parts(p, tiles, static_cast<int>(all), most);
+  if (st.parts) {
+    // this CTA's unit, counted over the sequences
+    const int index = blockIdx.x / st.parts;
+    st.part = blockIdx.x - index * st.parts;
+    st.shares = static_cast<int>(all) * st.parts;
+    if (static_cast<int>(blockIdx.x) >= st.shares) return st;
+    long long before, mine;
+    st.b = find_entry(p.B, index, static_cast<long long>(first_units) * p.heads,
+                      [&](int b) { return static_cast<long long>(paged_units(p, b).units) * p.heads; }, &before, &mine);
+    const PagedUnits u = paged_units(p, st.b);
+    if (u.units == 0 || mine == 0) return st;  // only should the tables have changed meanwhile
+    const int r = index - static_cast<int>(before);
+    st.head = min(r / u.units, p.heads - 1);
+    st.unit = min(r - st.head * u.units, u.units - 1);
+    // No more parts than tiles, so that every part after the first with a tile has one.
+    // Steps are counted from the unit's first.
+    const int its = key_tiles(unit_keys(p, u.s, st.unit)), per_unit = its + kPagedUnitCost;
+    st.parts = min(st.parts, its);
+    if (st.part >= st.parts) return st;
+    st.from = per_unit * st.part / st.parts;
+    st.begin = st.from;
+    st.end = per_unit * (st.part + 1) / st.parts;
+    return st;
+  }
   st.begin = paged_share_begin(st, blockIdx.x);
   st.end = paged_share_begin(st, blockIdx.x + 1);
   long long before, mine;
