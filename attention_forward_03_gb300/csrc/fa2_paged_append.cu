@@ -10,20 +10,23 @@
 namespace fa2 {
 namespace {
 
-// Sequence that token t belongs to, or -1; `s` is it. The starts ascend, so
-// the last one at or before t is searched for.
+// Sequence that token t belongs to, or -1; `s` is it. By one whole warp: the
+// starts ascend, and the last one at or before t is searched for among 32
+// candidates at a time.
 __device__ __forceinline__ int seq_of_token(const PagedBatch& p, int t, PagedSeq& s) {
   int b;
   if (!p.starts) {
     b = t / p.each;
   } else {
-    int lo = 0, hi = p.B;  // the first start past t lies in (lo, hi]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.starts + mid) > t) hi = mid;
-      else lo = mid + 1;
+    const int lane = threadIdx.x & 31;
+    int lo = -1, hi = p.B;  // starts[lo] <= t < starts[hi]
+    while (hi - lo > 1) {
+      const int by = (hi - lo + 31) / 32, m = lo + (lane + 1) * by;
+      const bool before = m < hi && __ldg(p.starts + m) <= t;
+      lo += __popc(__ballot_sync(0xffffffffu, before)) * by;
+      hi = min(hi, lo + by);
     }
-    b = lo - 1;
+    b = lo;
   }
   if (b < 0 || b >= p.B) return -1;
   s = paged_seq(p, b);
@@ -31,31 +34,51 @@ __device__ __forceinline__ int seq_of_token(const PagedBatch& p, int t, PagedSeq
 }
 
 // ------------------------------------------------------------------ append
-// Bound by bytes (each read and written once); a thread moves 16 of them.
+// Bound by bytes, each read and written once. A warp takes a token: 16 bytes of
+// its keys' and values' rows per lane and step, up to eight of them under way
+// while the token's sequence and page are looked up.
+constexpr int kMoveThreads = 256;
+constexpr int kUnder = 8;  // 16-byte pieces under way per lane
+
 template <int D>
-__global__ void __launch_bounds__(256) fa2_paged_append_kernel(const PagedAppendParams p) {
+__global__ void __launch_bounds__(kMoveThreads) fa2_paged_append_kernel(const PagedAppendParams p) {
   constexpr int kVecs = D / 8;  // 16-byte pieces of a row
-  const int per_token = p.heads * 2 * kVecs;
-  const long long items = static_cast<long long>(p.T) * per_token;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < items; i += stride) {
-    const int t = static_cast<int>(i / per_token);
-    const int r = static_cast<int>(i - static_cast<long long>(t) * per_token);
-    const int vec = r % kVecs, kv = (r / kVecs) & 1, head = r / (2 * kVecs);
-    PagedSeq s;
-    const int b = seq_of_token(p, t, s);
-    if (b < 0) continue;
-    const int pos = s.length - s.n + (t - s.t0);
-    if (pos < 0) continue;  // more tokens than positions
-    const int page = paged_entry(p, b, pos);
-    if (!page_ok(p, page)) continue;
-    const int slot = pos & ((1 << p.page_shift) - 1);
-    const uint16_t* from = kv ? static_cast<const uint16_t*>(p.v) + t * p.v_token + head * p.v_head
-                              : static_cast<const uint16_t*>(p.k) + t * p.k_token + head * p.k_head;
-    const PagedStrides& cs = kv ? p.vs : p.ks;
-    uint16_t* to = static_cast<uint16_t*>(kv ? p.vc : p.kc) + page * cs.page + head * cs.head + slot * cs.slot;
-    reinterpret_cast<uint4*>(to)[vec] = __ldg(reinterpret_cast<const uint4*>(from) + vec);
-    if (p.weights && kv == 0 && vec == 0)
+  const int lane = threadIdx.x & 31;
+  const int items = p.heads * 2 * kVecs;  // of a token: [head][K, V][piece]
+  const int warps = gridDim.x * (kMoveThreads / 32);
+  for (int t = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); t < p.T; t += warps) {
+    const uint16_t* const k = static_cast<const uint16_t*>(p.k) + t * p.k_token;
+    const uint16_t* const v = static_cast<const uint16_t*>(p.v) + t * p.v_token;
+    int page = -1, slot = 0;
+    for (int i0 = 0; i0 < items; i0 += 32 * kUnder) {
+      uint4 piece[kUnder];
+#pragma unroll
+      for (int j = 0; j < kUnder; ++j) {
+        const int i = i0 + 32 * j + lane, head = i / (2 * kVecs), r = i - head * 2 * kVecs;
+        if (i < items)
+          piece[j] = __ldg(reinterpret_cast<const uint4*>(r < kVecs ? k + head * p.k_head : v + head * p.v_head) +
+                           (r < kVecs ? r : r - kVecs));
+      }
+      if (i0 == 0) {
+        PagedSeq s;
+        const int b = seq_of_token(p, t, s);
+        const int pos = b < 0 ? -1 : s.length - s.n + (t - s.t0);
+        if (pos >= 0) page = paged_entry(p, b, pos);  // (of more tokens than positions the first ones have none)
+        slot = pos & ((1 << p.page_shift) - 1);
+      }
+      if (!page_ok(p, page)) break;
+#pragma unroll
+      for (int j = 0; j < kUnder; ++j) {
+        const int i = i0 + 32 * j + lane, head = i / (2 * kVecs), r = i - head * 2 * kVecs;
+        if (i >= items) continue;
+        const bool is_k = r < kVecs;
+        const PagedStrides& c = is_k ? p.ks : p.vs;
+        uint16_t* const to = static_cast<uint16_t*>(is_k ? p.kc : p.vc) + page * c.page + head * c.head + slot * c.slot;
+        reinterpret_cast<uint4*>(to)[is_k ? r : r - kVecs] = piece[j];
+      }
+    }
+    if (!p.weights || !page_ok(p, page)) continue;
+    for (int head = lane; head < p.heads; head += 32)
       p.weights[((static_cast<long long>(page) * p.heads + head) << p.page_shift) + slot] = 0.f;
   }
 }
@@ -101,8 +124,24 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
     return ordered_bits(__ldg(p.weights + ((static_cast<long long>(page) * p.heads + head) << p.page_shift) +
                               (i & ((1 << p.page_shift) - 1))));
   };
-  if (in_smem)
-    for (int i = threadIdx.x; i < old; i += kSelectThreads) bits[i] = read(i);
+  if (in_smem) {
+    // the pages, then the weights of eight positions at once (one after another: 1.5 us
+    // of latency for every 1024 positions)
+    for (int i0 = threadIdx.x; i0 < old; i0 += 8 * kSelectThreads) {
+      int page[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) page[j] = i0 + j * kSelectThreads < old ? paged_entry(p, b, i0 + j * kSelectThreads) : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (page_ok(p, page[j]))
+          w[j] = __ldg(p.weights + ((static_cast<long long>(page[j]) * p.heads + head) << p.page_shift) +
+                       ((i0 + j * kSelectThreads) & ((1 << p.page_shift) - 1)));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * kSelectThreads < old) bits[i0 + j * kSelectThreads] = page_ok(p, page[j]) ? ordered_bits(w[j]) : 0u;
+    }
+  }
   auto key = [&](int i) { return in_smem ? bits[i] : read(i); };
   if (threadIdx.x == 0) {
     s_prefix = 0;
@@ -196,53 +235,89 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
 }
 
 // Keys, values and weights of the kept positions to their new pages: bound by
-// bytes, 16 of them per thread and step.
+// bytes. A warp takes runs of up to 32 rows: a lane looks up a row each, then
+// 16 bytes per lane and step, eight of them under way.
 template <int D>
-__global__ void __launch_bounds__(256) fa2_paged_move_kernel(const PagedEvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads) fa2_paged_move_kernel(const PagedEvictParams p) {
   constexpr int kVecs = D / 8;
-  const int per_row = 2 * kVecs;
-  const long long rows = static_cast<long long>(p.B) * p.heads * p.keep;
-  const long long items = rows * per_row;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  constexpr int kRowsAtOnce = 32 / (2 * kVecs) > 0 ? 32 / (2 * kVecs) : 1;  // rows (K and V) of a step
+  constexpr int kRun = kRowsAtOnce * kUnder;                                  // rows of a run: 8, 16 or 32
+  static_assert(kRun <= 32 && 2 * kVecs <= 32, "a lane per row and piece");
+  cudaGridDependencySynchronize();  // what the selection wrote
+  const int lane = threadIdx.x & 31;
+  const int runs = (p.keep + kRun - 1) / kRun;  // of a key head of a sequence
+  const long long all = static_cast<long long>(p.B) * p.heads * runs;
+  const long long warps = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
   const int in_page = (1 << p.page_shift) - 1;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < items; i += stride) {
-    const long long row = i / per_row;
-    const int r = static_cast<int>(i - row * per_row), vec = r % kVecs, kv = r / kVecs;
-    const int src = __ldg(p.kept + row);
-    if (src < 0) continue;
-    const int bh = static_cast<int>(row / p.keep), j = static_cast<int>(row - static_cast<long long>(bh) * p.keep);
+  // this lane's piece of a step: row, cache, 16 bytes
+  const int row_of = lane / (2 * kVecs), r = lane - row_of * 2 * kVecs;
+  const bool is_k = r < kVecs, works = row_of < kRowsAtOnce;
+  const int vec = is_k ? r : r - kVecs;
+  const PagedStrides& c = is_k ? p.ks : p.vs;
+  for (long long run = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); run < all; run += warps) {
+    const int bh = static_cast<int>(run / runs), j0 = static_cast<int>(run - static_cast<long long>(bh) * runs) * kRun;
     const int b = bh / p.heads, head = bh - b * p.heads;
-    const int from = paged_entry(p, b, src), to = __ldg(p.new_table + b * p.new_stride + (j >> p.page_shift));
-    if (!page_ok(p, to)) continue;
-    const bool there = page_ok(p, from);
-    const PagedStrides& cs = kv ? p.vs : p.ks;
-    uint16_t* const c = static_cast<uint16_t*>(kv ? p.vc : p.kc) + head * cs.head;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (there) u = reinterpret_cast<const uint4*>(c + from * cs.page + (src & in_page) * cs.slot)[vec];
-    reinterpret_cast<uint4*>(c + to * cs.page + (j & in_page) * cs.slot)[vec] = u;
-    if (r == 0) {
-      const float w = there ? p.weights[((static_cast<long long>(from) * p.heads + head) << p.page_shift) + (src & in_page)] : 0.f;
-      p.weights[((static_cast<long long>(to) * p.heads + head) << p.page_shift) + (j & in_page)] = w;
+    // lane l: row j0 + l; `from`: its old page or -1, `to`: its new one or -1
+    int src = -1, from = -1, to = -1;
+    if (lane < kRun && j0 + lane < p.keep) src = p.kept[static_cast<long long>(bh) * p.keep + j0 + lane];
+    if (src >= 0) {
+      from = paged_entry(p, b, src);
+      to = __ldg(p.new_table + b * p.new_stride + ((j0 + lane) >> p.page_shift));
+      if (!page_ok(p, from)) from = -1;
+      if (!page_ok(p, to)) to = -1;
     }
+    if (__all_sync(0xffffffffu, src < 0)) continue;
+    uint16_t* const cache = static_cast<uint16_t*>(is_k ? p.kc : p.vc) + head * c.head;
+    uint4 piece[kUnder];
+#pragma unroll
+    for (int i = 0; i < kUnder; ++i) {
+      const int row = i * kRowsAtOnce + (works ? row_of : 0);
+      const int f = __shfl_sync(0xffffffffu, from, row), s = __shfl_sync(0xffffffffu, src, row);
+      piece[i] = make_uint4(0u, 0u, 0u, 0u);  // of a position whose page is none
+      if (works && f >= 0) piece[i] = reinterpret_cast<const uint4*>(cache + f * c.page + (s & in_page) * c.slot)[vec];
+    }
+    float w = 0.f;
+    if (from >= 0) w = p.weights[((static_cast<long long>(from) * p.heads + head) << p.page_shift) + (src & in_page)];
+#pragma unroll
+    for (int i = 0; i < kUnder; ++i) {
+      const int row = i * kRowsAtOnce + (works ? row_of : 0);
+      const int t = __shfl_sync(0xffffffffu, to, row);
+      if (works && t >= 0) reinterpret_cast<uint4*>(cache + t * c.page + ((j0 + row) & in_page) * c.slot)[vec] = piece[i];
+    }
+    if (to >= 0) p.weights[((static_cast<long long>(to) * p.heads + head) << p.page_shift) + ((j0 + lane) & in_page)] = w;
   }
 }
 
+// At most 8 blocks per SM; `dependent`: the kernel may be set up while the one before it still runs.
 template <typename P, typename F>
-cudaError_t launch_flat(F kern, const P& p, long long items, int sms, cudaStream_t s) {
-  const int grid = static_cast<int>(std::min<long long>((items + 255) / 256, 8ll * sms));
-  kern<<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_moves(F kern, const P& p, long long warps, int sms, bool dependent, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((warps * 32 + kMoveThreads - 1) / kMoveThreads, 8ll * sms)));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int D>
+cudaError_t launch_move(const PagedEvictParams& p, int sms, cudaStream_t s) {
+  constexpr int rows = std::max(1, 32 / (2 * (D / 8))) * kUnder;
+  const long long warps = static_cast<long long>(p.B) * p.heads * ((p.keep + rows - 1) / rows);
+  return warps == 0 ? cudaSuccess : launch_moves(fa2_paged_move_kernel<D>, p, warps, sms, true, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(int D, const PagedAppendParams& p, int sms, cudaStream_t s) {
-  const long long items = static_cast<long long>(p.T) * p.heads * 2 * (D / 8);
   switch (D) {
-    case 32: return launch_flat(fa2_paged_append_kernel<32>, p, items, sms, s);
-    case 64: return launch_flat(fa2_paged_append_kernel<64>, p, items, sms, s);
-    case 96: return launch_flat(fa2_paged_append_kernel<96>, p, items, sms, s);
-    default: return launch_flat(fa2_paged_append_kernel<128>, p, items, sms, s);
+    case 32: return launch_moves(fa2_paged_append_kernel<32>, p, p.T, sms, false, s);
+    case 64: return launch_moves(fa2_paged_append_kernel<64>, p, p.T, sms, false, s);
+    case 96: return launch_moves(fa2_paged_append_kernel<96>, p, p.T, sms, false, s);
+    default: return launch_moves(fa2_paged_append_kernel<128>, p, p.T, sms, false, s);
   }
 }
 
@@ -257,13 +332,11 @@ cudaError_t launch_paged_evict(int D, const PagedEvictParams& p, int sms, cudaSt
   fa2_paged_select_kernel<<<p.B * p.heads, kSelectThreads, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long items = static_cast<long long>(p.B) * p.heads * p.keep * 2 * (D / 8);
-  if (items == 0) return cudaSuccess;
   switch (D) {
-    case 32: return launch_flat(fa2_paged_move_kernel<32>, p, items, sms, s);
-    case 64: return launch_flat(fa2_paged_move_kernel<64>, p, items, sms, s);
-    case 96: return launch_flat(fa2_paged_move_kernel<96>, p, items, sms, s);
-    default: return launch_flat(fa2_paged_move_kernel<128>, p, items, sms, s);
+    case 32: return launch_move<32>(p, sms, s);
+    case 64: return launch_move<64>(p, sms, s);
+    case 96: return launch_move<96>(p, sms, s);
+    default: return launch_move<128>(p, sms, s);
   }
 }
 
