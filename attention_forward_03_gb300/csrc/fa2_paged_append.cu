@@ -86,11 +86,14 @@ __global__ void __launch_bounds__(kMoveThreads) fa2_paged_append_kernel(const Pa
 // ------------------------------------------------------------------- evict
 // Which positions stay: of those before the last `recent` the `need` of the
 // greatest weight, found by a radix selection over the weights' bits as
-// unsigned integers in the same order, then all that are above the threshold
-// and the first of those at it, written in order.
+// unsigned integers in the same order (11, 11 and 10 bits at a time), then all
+// that are above the threshold and the first of those at it, written in order.
+// One block for each key head of a sequence. What bounds it is latency: the
+// rounds over the positions and the three scans of the counts.
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectKeys = 49152;  // bits of so many positions are kept in shared memory
+constexpr int kBins = 2048;         // of a digit
 
 // NaN above +inf; zeros of both signs equal.
 __device__ __forceinline__ uint32_t ordered_bits(float w) {
@@ -101,7 +104,8 @@ __device__ __forceinline__ uint32_t ordered_bits(float w) {
 
 __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(const PagedEvictParams p) {
   extern __shared__ uint32_t bits[];
-  __shared__ int hist[256];
+  __shared__ int hist[kBins];
+  __shared__ int warp_sum[kSelectWarps];
   __shared__ int warp_above[kSelectWarps], warp_equal[kSelectWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -148,46 +152,51 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
     s_need = p.keep - p.recent;
   }
   __syncthreads();
-  // The threshold, 8 bits at a time from the top: the prefix that the need-th
+  // The threshold, a digit at a time from the top: the prefix that the need-th
   // greatest has, and how many are needed among those with it.
-  const int rounds = (old + kSelectThreads - 1) / kSelectThreads;
   if (s_need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    const int rounds = (old + kSelectThreads - 1) / kSelectThreads;
+    for (int digits = 0; digits < 3; ++digits) {
+      const int shift = digits == 0 ? 21 : digits == 1 ? 10 : 0, width = digits == 2 ? 10 : 11;
+      hist[threadIdx.x] = hist[threadIdx.x + kSelectThreads] = 0;
       __syncthreads();
       const uint32_t prefix = s_prefix;
+#pragma unroll 4
       for (int r = 0; r < rounds; ++r) {
         const int i = r * kSelectThreads + threadIdx.x;
         const uint32_t u = i < old ? key(i) : 0u;
-        const bool in = i < old && (shift == 24 || (u >> (shift + 8)) == prefix);
+        const bool in = i < old && (digits == 0 || (u >> (shift + width)) == prefix);
+        const int digit = (u >> shift) & ((1 << width) - 1);
+        // equal weights meet in one count: a warp of them adds once
         const unsigned who = __ballot_sync(0xffffffffu, in);
         if (in) {
-          const int digit = (u >> shift) & 255;
-          const unsigned same = __match_any_sync(who, digit);
-          if (__ffs(same) - 1 == lane) atomicAdd(&hist[digit], __popc(same));
+          int same;
+          __match_all_sync(who, digit, &same);
+          if (!same) atomicAdd(&hist[digit], 1);
+          else if (__ffs(who) - 1 == lane) atomicAdd(&hist[digit], __popc(who));
         }
       }
       __syncthreads();
-      if (warp == 0) {
-        // lane l holds digits 255 - 8 l .. 248 - 8 l; how many lie above
-        int sum = 0;
+      // thread i: digits 2047 - 2 i and 2046 - 2 i; how many lie above
+      const int bin = kBins - 1 - 2 * static_cast<int>(threadIdx.x);
+      const int high = hist[bin], sum = high + hist[bin - 1];
+      int upto = sum;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) sum += hist[255 - 8 * lane - d];
-        int upto = sum;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+      }
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      int warps_before = lane < warp ? warp_sum[lane] : 0;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, off);
-          if (lane >= off) upto += v;
-        }
-        const int need = s_need;
-        __syncwarp();
-        int above = upto - sum;
-        if (above < need && need <= upto) {
-          int d = 255 - 8 * lane;
-          while (above + hist[d] < need && (d & 7)) above += hist[d--];  // at most its 8 digits
-          s_prefix = (prefix << 8) | static_cast<uint32_t>(d);
-          s_need = need - above;
-        }
+      for (int off = 16; off > 0; off >>= 1) warps_before += __shfl_xor_sync(0xffffffffu, warps_before, off);
+      const int need = s_need, above = warps_before + upto - sum;
+      __syncthreads();  // everyone has read the need
+      if (above < need && need <= above + sum) {
+        const bool first = above + high >= need;
+        s_prefix = (prefix << width) | static_cast<uint32_t>(first ? bin : bin - 1);
+        s_need = need - above - (first ? 0 : high);
       }
       __syncthreads();
     }
@@ -200,6 +209,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
   const int from = min(old, warp * run), to = min(old, from + run);
   int above = 0, equal = 0;
   if (any)
+#pragma unroll 4
     for (int i0 = from; i0 < to; i0 += 32) {
       const int i = i0 + lane;
       const uint32_t u = i < to ? key(i) : 0u;
@@ -213,9 +223,14 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
   __syncthreads();
   if (any) {
     int at = 0, eq = 0;
-    for (int w = 0; w < warp; ++w) {
-      at += warp_above[w];
-      eq += warp_equal[w];
+    if (lane < warp) {
+      at = warp_above[lane];
+      eq = warp_equal[lane];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      at += __shfl_xor_sync(0xffffffffu, at, off);
+      eq += __shfl_xor_sync(0xffffffffu, eq, off);
     }
     at += min(eq, equal_kept);
     for (int i0 = from; i0 < to; i0 += 32) {
