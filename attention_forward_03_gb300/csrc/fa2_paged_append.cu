@@ -103,12 +103,13 @@ __device__ __forceinline__ uint32_t ordered_bits(float w) {
 }
 
 __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(const PagedEvictParams p) {
-  extern __shared__ uint32_t bits[];
+  extern __shared__ __align__(16) uint32_t bits[];
   __shared__ int hist[kBins];
   __shared__ int warp_sum[kSelectWarps];
   __shared__ int warp_above[kSelectWarps], warp_equal[kSelectWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
+  cudaTriggerProgrammaticLaunchCompletion();  // the moving kernel may take the SMs that are free
   const int b = blockIdx.x / p.heads, head = blockIdx.x - b * p.heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int length = min(max(__ldg(p.lengths + b), 0), p.capacity);
@@ -146,7 +147,11 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
         if (i0 + j * kSelectThreads < old) bits[i0 + j * kSelectThreads] = page_ok(p, page[j]) ? ordered_bits(w[j]) : 0u;
     }
   }
-  auto key = [&](int i) { return in_smem ? bits[i] : read(i); };
+  // four positions' keys from i, a multiple of 4, on
+  auto keys4 = [&](int i) {
+    if (in_smem) return *reinterpret_cast<const uint4*>(bits + i);  // (past `old`: anything)
+    return make_uint4(read(i), i + 1 < old ? read(i + 1) : 0u, i + 2 < old ? read(i + 2) : 0u, i + 3 < old ? read(i + 3) : 0u);
+  };
   if (threadIdx.x == 0) {
     s_prefix = 0;
     s_need = p.keep - p.recent;
@@ -155,17 +160,13 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
   // The threshold, a digit at a time from the top: the prefix that the need-th
   // greatest has, and how many are needed among those with it.
   if (s_need > 0) {
-    const int rounds = (old + kSelectThreads - 1) / kSelectThreads;
     for (int digits = 0; digits < 3; ++digits) {
       const int shift = digits == 0 ? 21 : digits == 1 ? 10 : 0, width = digits == 2 ? 10 : 11;
       hist[threadIdx.x] = hist[threadIdx.x + kSelectThreads] = 0;
       __syncthreads();
       const uint32_t prefix = s_prefix;
-#pragma unroll 4
-      for (int r = 0; r < rounds; ++r) {
-        const int i = r * kSelectThreads + threadIdx.x;
-        const uint32_t u = i < old ? key(i) : 0u;
-        const bool in = i < old && (digits == 0 || (u >> (shift + width)) == prefix);
+      auto count = [&](uint32_t u, bool there) {
+        const bool in = there && (digits == 0 || (u >> (shift + width)) == prefix);
         const int digit = (u >> shift) & ((1 << width) - 1);
         // equal weights meet in one count: a warp of them adds once
         const unsigned who = __ballot_sync(0xffffffffu, in);
@@ -175,6 +176,15 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
           if (!same) atomicAdd(&hist[digit], 1);
           else if (__ffs(who) - 1 == lane) atomicAdd(&hist[digit], __popc(who));
         }
+      };
+      for (int i0 = 0; i0 < old; i0 += 4 * kSelectThreads) {
+        const int i = i0 + 4 * static_cast<int>(threadIdx.x);
+        if (i0 + 128 * warp >= old) break;  // none of the warp's
+        const uint4 u = i < old ? keys4(i) : make_uint4(0u, 0u, 0u, 0u);
+        count(u.x, i < old);
+        count(u.y, i + 1 < old);
+        count(u.z, i + 2 < old);
+        count(u.w, i + 3 < old);
       }
       __syncthreads();
       // thread i: digits 2047 - 2 i and 2046 - 2 i; how many lie above
@@ -204,46 +214,67 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
   const uint32_t threshold = s_prefix;
   const int equal_kept = s_need;  // of the positions at the threshold
   const bool any = p.keep > p.recent;
-  // each warp a run of positions: how many above and at the threshold, then written in order
-  const int run = ((old + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+  // Each warp a run of positions, eight neighbouring ones to a lane and step: how
+  // many lie above and at the threshold (in two halves of one number), then the
+  // places of those that stay.
+  constexpr int kStep = 8 * 32;
+  const int run = ((old + kSelectWarps - 1) / kSelectWarps + kStep - 1) / kStep * kStep;
   const int from = min(old, warp * run), to = min(old, from + run);
+  auto keys8 = [&](int i, uint32_t (&u)[8]) {
+    const uint4 a = i < to ? keys4(i) : make_uint4(0u, 0u, 0u, 0u), b = i + 4 < to ? keys4(i + 4) : make_uint4(0u, 0u, 0u, 0u);
+    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
+    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+  };
+  // (above, at) of a lane's eight, 16 bits each: a step of a warp has 256 at most
+  auto counts = [&](const uint32_t (&u)[8], int i) {
+    unsigned n = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k < to) n += (u[k] > threshold ? 1u : 0u) + (u[k] == threshold ? 0x10000u : 0u);
+    return n;
+  };
   int above = 0, equal = 0;
   if (any)
-#pragma unroll 4
-    for (int i0 = from; i0 < to; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t u = i < to ? key(i) : 0u;
-      above += __popc(__ballot_sync(0xffffffffu, i < to && u > threshold));
-      equal += __popc(__ballot_sync(0xffffffffu, i < to && u == threshold));
+    for (int i0 = from; i0 < to; i0 += kStep) {
+      uint32_t u[8];
+      keys8(i0 + 8 * lane, u);
+      const unsigned n = __reduce_add_sync(0xffffffffu, counts(u, i0 + 8 * lane));
+      above += n & 0xffffu;
+      equal += n >> 16;
     }
   if (lane == 0) {
     warp_above[warp] = above;
     warp_equal[warp] = equal;
   }
   __syncthreads();
-  if (any) {
-    int at = 0, eq = 0;
-    if (lane < warp) {
-      at = warp_above[lane];
-      eq = warp_equal[lane];
-    }
+  if (any && from < to) {
+    int at = __reduce_add_sync(0xffffffffu, lane < warp ? warp_above[lane] : 0);
+    int eq = __reduce_add_sync(0xffffffffu, lane < warp ? warp_equal[lane] : 0);
+    // `at`: above the threshold so far; `eq`: at it, of which the first equal_kept stay
+    for (int i0 = from; i0 < to; i0 += kStep) {
+      const int i = i0 + 8 * lane;
+      uint32_t u[8];
+      keys8(i, u);
+      const unsigned mine = counts(u, i);
+      unsigned upto = mine;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      at += __shfl_xor_sync(0xffffffffu, at, off);
-      eq += __shfl_xor_sync(0xffffffffu, eq, off);
-    }
-    at += min(eq, equal_kept);
-    for (int i0 = from; i0 < to; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t u = i < to ? key(i) : 0u;
-      const bool gt = i < to && u > threshold, is = i < to && u == threshold;
-      const unsigned below = (1u << lane) - 1u;
-      const unsigned eqs = __ballot_sync(0xffffffffu, is);
-      const bool stays = gt || (is && eq + __popc(eqs & below) < equal_kept);
-      const unsigned all = __ballot_sync(0xffffffffu, stays);
-      if (stays && at + __popc(all & below) < p.keep - p.recent) kept[at + __popc(all & below)] = i;
-      at += __popc(all);
-      eq += __popc(eqs);
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+      }
+      const unsigned all = __shfl_sync(0xffffffffu, upto, 31);
+      int lane_at = at + static_cast<int>((upto - mine) & 0xffffu), lane_eq = eq + static_cast<int>((upto - mine) >> 16);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i + k >= to) continue;
+        const bool gt = u[k] > threshold, is = u[k] == threshold;
+        const int place = lane_at + min(lane_eq, equal_kept);
+        if ((gt || (is && lane_eq < equal_kept)) && place < p.keep - p.recent) kept[place] = i + k;
+        lane_at += gt;
+        lane_eq += is;
+      }
+      at += all & 0xffffu;
+      eq += all >> 16;
     }
   }
   for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) kept[p.keep - p.recent + i] = old + i;
