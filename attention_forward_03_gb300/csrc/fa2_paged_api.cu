@@ -283,9 +283,22 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   // more on the tensor cores (unless a token alone has more rows than a
   // sub-tile); each kernel passes over the other's. Only the device knows the
   // sequences' tokens, so both are launched unless the sizes rule one out.
-  const int64_t most = static_cast<int64_t>(query_starts ? std::min(T, max_query_length) : p.each) * group;
-  const int64_t least = static_cast<int64_t>(query_starts ? 1 : p.each) * group;
-  const bool tiles = most > kPagedRows && group <= kRows, rows_too = !tiles || least <= kPagedRows;
+  //
+  // The rows kernel takes them all (in blocks of 16 rows) where there are at
+  // most 48 blocks: its CTAs share the keys of few units better (us, rows kernel
+  // / tensor cores, 4 query heads to a key head: 8 key heads of 64 over 4000
+  // positions, 32 rows 12.0 / 20.1, 96 rows 17.6 / 20.1, 128 rows 20.7 / 20.1; of
+  // 128, 64 rows 19.9 / 23.9, 128 rows 26.1 / 23.9; 64 key heads of 64, 32 rows
+  // over 100 positions 7.0 / 9.2, over 4000 31.2 / 26.2).
+  const int longest = query_starts ? std::min(T, max_query_length) : p.each;
+  const int64_t most = static_cast<int64_t>(longest) * group;
+  const int64_t blocks = std::min(static_cast<int64_t>(B) * ((most + kPagedRows - 1) / kPagedRows),
+                                  static_cast<int64_t>(T) * group / kPagedRows + B) * Hkv;
+  const bool tiles = most > kPagedRows && group <= kRows && blocks > 48;
+  // A sequence of so few tokens would leave the others more than `longest` each.
+  const int few = kPagedRows / group;
+  const bool none_short = group > kPagedRows || (longest > few && static_cast<int64_t>(B) * longest - T < longest - few);
+  const bool rows_too = !tiles || !none_short;
   p.test_withhold = take_test_withhold();
   char* const ws = static_cast<char*>(workspace);
   const bool bf = dtype == FA2_BF16;

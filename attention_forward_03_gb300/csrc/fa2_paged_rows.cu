@@ -32,8 +32,7 @@
 
 #include <climits>
 
-#include "fa2_cross.cuh"
-#include "fa2_paged.cuh"
+#include "fa2_paged_walk.cuh"
 #include "mma_sync.cuh"
 
 namespace fa2 {
@@ -59,15 +58,14 @@ struct RowsLayout {
   static constexpr int kMerge = kRowWarps * kStages * kPieceBytes;
   static constexpr int kStats = kMerge + 4 * kBufFloats * 4;            // [warps][3][16]
   static constexpr int kBars = kStats + kRowWarps * 3 * kPagedRows * 4;   // [warps][stages]
-  static constexpr int kStart = kBars + kRowWarps * kStages * 8;
-  static constexpr int kAbort = kStart + static_cast<int>(sizeof(CrossStart));
+  static constexpr int kAbort = kBars + kRowWarps * kStages * 8;
   static constexpr int kNoPage = kAbort + 16;                           // [warps][stages] int: the piece has no page
   static constexpr int kSmemBytes = kNoPage + kRowWarps * kStages * 4 + 1024;  // + slack for 1 KB alignment
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   // what joining the partial results of up to kPagedRowsMaxCtas CTAs takes fits the ring
   static_assert((kPagedRows * D + 3 * kPagedRows + (kPagedRowsMaxCtas + 3) * kPagedRows) * 4 + 2 * kPagedRows * D * 4 + 16 * kRowThreads <= kMerge,
                 "joining in the ring");
-  static_assert(kStart % alignof(CrossStart) == 0 && kBars % 8 == 0, "alignment");
+  static_assert(kBars % 8 == 0, "alignment");
 };
 
 __device__ __forceinline__ int row_tiles(int n_keys) { return max(1, (n_keys + kPagedRowsKeys - 1) / kPagedRowsKeys); }
@@ -242,7 +240,6 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   uint8_t* const smem = smem_raw + (smem_base - raw);
   float* const merge = reinterpret_cast<float*>(smem + L::kMerge);
   float* const stats = reinterpret_cast<float*>(smem + L::kStats);
-  CrossStart* const start = reinterpret_cast<CrossStart*>(smem + L::kStart);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_base + static_cast<uint32_t>(warp * L::kStages * L::kPieceBytes);
@@ -250,35 +247,40 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   volatile int* const no_page = reinterpret_cast<volatile int*>(smem + L::kNoPage) + warp * L::kStages;
 
   // every warp finds the share and sets up its own ring
-  const CrossStart st = cross_find_start(p.B, false, [&](int b) {
-    const PagedSeq s = paged_seq(p, b);
-    return static_cast<long long>(p.heads) * TileCursor::row_blocks(p, s) * (row_tiles(s.length) + kRowsUnitCost);
-  });
+  auto steps = [&](int b) {
+    const PagedSeq q = paged_seq(p, b);
+    return static_cast<long long>(p.heads) * TileCursor::row_blocks(p, q) * (row_tiles(q.length) + kRowsUnitCost);
+  };
+  const long long first = lane < p.B ? steps(lane) : 0;
+  long long total = first;
+  for (int b = lane + 32; b < p.B; b += 32) total += steps(b);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  const int shares = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  if (static_cast<int>(blockIdx.x) >= shares) return;
+  auto share_begin = [&](int c) { return c >= shares ? total : quotient(total * c, shares); };
+  const long long s0 = share_begin(blockIdx.x), s1 = share_begin(blockIdx.x + 1);
+  long long before, mine;
   if (lane == 0) {
     for (int i = 0; i < L::kStages; ++i) mbar_init(bars + 8 * i, 1);
     mbar_init_fence();
-    if (warp == 0) {
-      *start = st;
-      *abort_flag = 0;
-    }
+    if (warp == 0) *abort_flag = 0;
   }
-  const long long s0 = cross_share_begin(st, blockIdx.x), s1 = cross_share_begin(st, blockIdx.x + 1);
-  if (s0 >= s1) return;
   TileCursor cur;  // the tile being computed
-  cur.b = st.b;
+  cur.b = find_entry(p.B, s0, first, steps, &before, &mine);
   cur.enter(p);
   if (cur.blocks == 0) return;  // only should the tables have changed meanwhile
   {
-    const long long r = s0 - st.b_start;
-    const int unit = static_cast<int>(r / (cur.tiles + kRowsUnitCost));
-    const long long at = r - static_cast<long long>(unit) * (cur.tiles + kRowsUnitCost);
+    const long long r = s0 - before;
+    const int unit = static_cast<int>(quotient(r, cur.tiles + kRowsUnitCost));
+    const int at = static_cast<int>(r - static_cast<long long>(unit) * (cur.tiles + kRowsUnitCost));
     cur.head = unit / cur.blocks;
     cur.block = unit - cur.head * cur.blocks;
-    cur.tile = static_cast<int>(max(at - kRowsUnitCost, 0ll));
+    cur.tile = max(at - kRowsUnitCost, 0);
     cur.step = s0 - at + kRowsUnitCost + cur.tile;
     cur.enter_block(p);
   }
-  if (cur.step >= s1) return;  // no share, or one without a tile
+  if (cur.step >= s1) return;  // a share without a tile
   const long long first_step = cur.step;
   // whether this warp's piece of a tile has a key
   auto has_keys = [&](const TileCursor& t) { return t.tile * kPagedRowsKeys + warp * kPiece < t.keys; };
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     int last = blockIdx.x;
     if (from_start && !unit_end) {
       const long long end = done.step + done.tiles - done.tile;  // one past the unit's last tile
-      while (last + 1 < st.shares && cross_share_begin(st, last + 1) < end) ++last;
+      while (last + 1 < shares && share_begin(last + 1) < end) ++last;
     }
     ok = !__syncthreads_or(!ok);
     if (!ok) break;

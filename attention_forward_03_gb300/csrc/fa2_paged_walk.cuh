@@ -117,6 +117,7 @@ struct PagedStart {
   long long begin, end;  // this CTA's share of them
   int shares;            // CTAs with a share
   int parts, part;       // where every unit is `parts` CTAs': which part this one's is (0: equal shares)
+  bool whole;            // equal shares of units that are not cut: those that begin in the share
   int b, head, unit;
   int from;         // steps of that unit before the share
 };
@@ -202,7 +203,14 @@ __device__ __forceinline__ PagedStart paged_start(const PagedTileParams& p) {
   if (static_cast<int>(blockIdx.x) >= st.shares) return st;
   const long long all = static_cast<long long>(units) * p.heads, tiles = sum - all * kPagedUnitCost;
   // fewer units than CTAs, and all about as long as the longest
-  if (all < gridDim.x && 10 * tiles >= 9 * all * most) st.parts = cut_parts(p, tiles, static_cast<int>(all), most);
+  const bool alike = 10 * tiles >= 9 * all * most;
+  if (all < gridDim.x && alike) st.parts = cut_parts(p, tiles, static_cast<int>(all), most);
+  // Short units are not cut where the CTA with the most of them has less to do than a
+  // cut and a join take (in tiles: 5 and 1.6).
+  if (!st.parts) {
+    const float mean = static_cast<float>(sum) / static_cast<float>(all), each = static_cast<float>(all) / static_cast<float>(gridDim.x);
+    st.whole = (alike ? (ceilf(each) - each) * mean : static_cast<float>(most + kPagedUnitCost)) <= 6.6f;
+  }
   if (st.parts) {
     // this CTA's unit, counted over the sequences
     const int index = blockIdx.x / st.parts;
@@ -268,6 +276,7 @@ struct PagedSegment {
 struct PagedCursor {
   PagedUnits u;
   int b, head, unit, from;
+  bool whole;
   long long step, end;
 };
 
@@ -277,6 +286,7 @@ __device__ __forceinline__ PagedCursor paged_first(const PagedTileParams& p, con
   c.head = st.head;
   c.unit = st.unit;
   c.from = st.from;
+  c.whole = st.whole;
   c.step = st.begin;
   c.end = st.end;
   c.u = paged_units(p, st.b);
@@ -297,7 +307,8 @@ __device__ __forceinline__ bool paged_next(PagedCursor& c, PagedSegment& s, cons
     s.keys = unit_keys(p, c.u.s, c.unit);
     s.nkv = key_tiles(s.keys);
     const int per_unit = s.nkv + kPagedUnitCost, from = min(c.from, per_unit);
-    const int to = static_cast<int>(min(static_cast<long long>(per_unit), from + (c.end - c.step)));
+    const int to = c.whole ? per_unit : static_cast<int>(min(static_cast<long long>(per_unit), from + (c.end - c.step)));
+    const bool mine = !c.whole || from == 0;  // else it began in an earlier share, whose it is
     s.unit_end = c.step - from + per_unit;
     s.kv_begin = max(from - kPagedUnitCost, 0);
     s.kv_end = max(to - kPagedUnitCost, 0);
@@ -316,7 +327,7 @@ __device__ __forceinline__ bool paged_next(PagedCursor& c, PagedSegment& s, cons
         } while (c.u.units == 0);
       }
     }
-    if (s.kv_end > s.kv_begin) return true;
+    if (mine && s.kv_end > s.kv_begin) return true;
   }
   return false;
 }
