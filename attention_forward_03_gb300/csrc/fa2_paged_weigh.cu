@@ -479,11 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
             }
             const uint32_t wg = step & 1u, use = step++ >> 1;  // whose step, and which of its
+            // The warpgroup's step before has been read. (Waited for in every step, also of units
+            // without this tile: a barrier's phase is known by its parity alone, so no
+            // waiter may fall two phases behind or run ahead.)
+            ok = wait_bounded(bar_s_free0 + 8 * wg, (use & 1u) ^ 1u, wd, kSiteWeighSFree, true, kNapNs);
+            if (!ok) break;
             if (live) {
               const uint32_t buf = 2 * wg + t;
-              // the warpgroup's step before has been read
-              ok = wait_bounded(bar_s_free0 + 8 * wg, (use & 1u) ^ 1u, wd, kSiteWeighSFree, true, kNapNs);
-              if (!ok) break;
               tc_fence_after_sync();
               const uint32_t qa = desc_lo_sw128(sQ, 16) + ((static_cast<uint32_t>(qs) * q_slot) >> 4);
               const uint32_t dt = tmem + buf * 128;

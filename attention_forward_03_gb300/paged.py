@@ -47,24 +47,27 @@ def fa2_paged_key_weights_workspace_bytes() -> int:
     return n.value
 
 
+# The checks of a small call cost more than its kernel (measured on one of 4
+# sequences: 20 us, of which the library's own share is 5), so each tensor is
+# asked for each of its properties once.
 def _check_cache(name, c, dt, dev, shape=None):
     """(shape, page, head and slot strides) of a cache, which has the dtype and device of the call."""
     s = c.shape
-    if len(s) != 4 or (shape is not None and s != shape):
+    if (s != shape if shape is not None else len(s) != 4):
         raise ValueError(f"{name} must be [pages, Hkv, page size, D]" + ("" if shape is None else " like k_cache"))
-    if c.dtype != dt or c.get_device() != dev:
+    if c.dtype is not dt or c.get_device() != dev:
         raise ValueError(f"{name} must have the dtype and device of the other tensors")
-    sp, sh, ss, sd = c.stride()
-    if sd != 1 and s[3] > 1:
+    strides = c.stride()
+    if strides[3] != 1 and s[3] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return s, (sp, sh, ss)
+    return s, strides[:3]
 
 
 def _check_tokens(name, t, T, heads, D, dt, dev):
     """(token, head) strides of a [T, heads, D] view."""
     if t.shape != (T, heads, D):
         raise ValueError(f"{name} must have the shape {[T, heads, D]}")
-    if t.dtype != dt or t.get_device() != dev:
+    if t.dtype is not dt or t.get_device() != dev:
         raise ValueError(f"{name} must have the dtype and device of the other tensors")
     st, sh, sd = t.stride()
     if sd != 1:
@@ -75,24 +78,27 @@ def _check_tokens(name, t, T, heads, D, dt, dev):
 def _check_table(name, table, dev, B=None):
     """(rows, entries per row, row stride) of a page table."""
     import torch
-    if table.dim() != 2 or table.dtype != torch.int32 or table.get_device() != dev or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"{name} must be an int32 [B, pages] tensor on the caches' device, its rows contiguous")
-    rows, width = table.shape
+    shape = table.shape
+    if len(shape) != 2 or table.dtype is not torch.int32 or table.get_device() != dev:
+        raise ValueError(f"{name} must be an int32 [B, pages] tensor on the caches' device")
+    rows, width = shape
+    row, column = table.stride()
+    if column != 1 and width > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
     if B is not None and rows != B:
         raise ValueError(f"{name} must have {B} rows")
-    return rows, width, table.stride(0)
+    return rows, width, row
 
 
 def _check_ints(name, t, n, dev):
     import torch
-    if t.shape != (n,) or t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != dev:
+    if t.shape != (n,) or t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on the caches' device")
     return t.data_ptr()
 
 
 def _check_batch(table, key_lengths, query_starts, T, dev):
-    """(B, max_pages, table stride, pointers of the lengths and starts)."""
+    """(B, max_pages, table stride, pointers of the table, lengths and starts)."""
     B, width, row = _check_table("block_table", table, dev)
     lengths = _check_ints("key_lengths", key_lengths, B, dev)
     starts = None
@@ -100,7 +106,7 @@ def _check_batch(table, key_lengths, query_starts, T, dev):
         starts = _check_ints("query_starts", query_starts, B + 1, dev)
     elif T and (B == 0 or T % B):
         raise ValueError(f"without query_starts the {T} tokens must be a multiple of the {B} sequences")
-    return B, width, row, lengths, starts
+    return B, width, row, table.data_ptr(), lengths, starts
 
 
 def _check_pool(name, t, shape, dev):
@@ -153,12 +159,12 @@ def paged_cache_append(k, v, k_cache, v_cache, block_table, key_lengths, query_s
     T = k.shape[0]
     kt = _check_tokens("k", k, T, Hkv, D, dt, dev)
     vt = _check_tokens("v", v, T, Hkv, D, dt, dev)
-    B, width, row, lengths, starts = _check_batch(block_table, key_lengths, query_starts, T, dev)
+    B, width, row, table, lengths, starts = _check_batch(block_table, key_lengths, query_starts, T, dev)
     w = None if weights is None else _check_pool("weights", weights, shape, dev)
     handle = stream_handle(dev, stream, (k, v, k_cache, v_cache, block_table, key_lengths, query_starts, weights))
     with device_guard(dev):
         code = library().fa2_paged_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), w,
-                                          block_table.data_ptr(), lengths, starts, _STRIDES11(*kt, *vt, *ks, *vs, row),
+                                          table, lengths, starts, _STRIDES11(*kt, *vt, *ks, *vs, row),
                                           T, B, Hkv, D, pages, page, width, dtc, handle)
     if code != FA2_OK:
         _check(code, "fa2_paged_append")
@@ -198,7 +204,7 @@ def paged_attention_forward(q, k_cache, v_cache, block_table, key_lengths, query
     pages, Hkv, page, _ = shape
     _group(Hq, Hkv)
     qs = _check_tokens("q", q, T, Hq, shape[3], dt, dev)
-    B, width, row, lengths, starts = _check_batch(block_table, key_lengths, query_starts, T, dev)
+    B, width, row, table, lengths, starts = _check_batch(block_table, key_lengths, query_starts, T, dev)
     if out is not None:
         _like("out", out, q.shape, dt, dev)
     if lse is not None:
@@ -220,7 +226,7 @@ def paged_attention_forward(q, k_cache, v_cache, block_table, key_lengths, query
         else:
             _check_workspace(workspace, need, dev)
         code = library().fa2_paged_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
-                                       lse.data_ptr(), block_table.data_ptr(), lengths, starts,
+                                       lse.data_ptr(), table, lengths, starts,
                                        _STRIDES9(*qs, *ks, *vs, row), T, B, Hq, Hkv, D, pages, page, width,
                                        T if max_query_length is None else max_query_length, scale,
                                        1 if is_causal else 0, dtc, workspace.data_ptr(), workspace.nbytes, handle)
@@ -259,7 +265,7 @@ def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=No
     _group(Hq, Hkv)
     qs = _check_tokens("q", q, T, Hq, shape[3], dt, dev)
     _like("lse", lse, (T, Hq), torch.float32, dev)
-    B, width, row, lengths, starts = _check_batch(block_table, key_lengths, query_starts, T, dev)
+    B, width, row, table, lengths, starts = _check_batch(block_table, key_lengths, query_starts, T, dev)
     w = None if weights is None else _check_pool("weights", weights, shape, dev)
     if out is None:
         out = weights
@@ -285,7 +291,7 @@ def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=No
         else:
             _check_workspace(workspace, need, dev)
         code = library().fa2_paged_key_weights(q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), w, out.data_ptr(),
-                                               block_table.data_ptr(), lengths, starts, _STRIDES6(*qs, *ks, row), T, B,
+                                               table, lengths, starts, _STRIDES6(*qs, *ks, row), T, B,
                                                Hq, Hkv, D, pages, page, width,
                                                T if max_query_length is None else max_query_length, scale,
                                                1 if is_causal else 0, dtc, workspace.data_ptr(), workspace.nbytes,
