@@ -269,8 +269,8 @@ struct WeighLayout {
   static constexpr int kLseOffset = kWide > kNarrow ? kWide : kNarrow;  // [8 warps][128] floats
   static constexpr int kPartOffset = kLseOffset + 8 * 128 * 4;          // [2 warpgroups][128] pairs of floats
   static constexpr int kBarOffset = kPartOffset + 2 * 128 * 8;
-  // k_full, k_empty [tile][K], q_full, q_empty [Q], s_full [warpgroup][tile], s_free, part, taken, flag [warpgroup], drain[2]
-  static constexpr int kNumBars = 4 * kMostK + 2 * kMostQ + 14;
+  // k_full, k_empty [tile][K], q_full, q_empty [Q], s_full, s_free [warpgroup][tile], part, taken, flag [warpgroup], drain[2]
+  static constexpr int kNumBars = 4 * kMostK + 2 * kMostQ + 16;
   static constexpr int kMiscOffset = kBarOffset + kNumBars * 8;
   static constexpr int kStartOffset = kMiscOffset + 16;
   static constexpr int kSmemBytes = kStartOffset + static_cast<int>(sizeof(WeighStart)) + 1024;
@@ -299,11 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_q_full = [&](int s) { return bars + 8u * (4 * L::kMostK + s); };
   auto bar_q_empty = [&](int s) { return bars + 8u * (4 * L::kMostK + L::kMostQ + s); };
   const uint32_t rest = bars + 8u * (4 * L::kMostK + 2 * L::kMostQ);
-  const uint32_t bar_s_full0 = rest;                               // [warpgroup][tile]
-  // [warpgroup]: its buffers have been read; its sums of a unit are in shared memory; those
-  // have been read; steps of joining a cut unit
-  const uint32_t bar_s_free0 = rest + 32, bar_part0 = rest + 48, bar_taken0 = rest + 64, bar_flag0 = rest + 80;
-  const uint32_t bar_drain0 = rest + 96;                           // [issuer]
+  const uint32_t bar_s_full0 = rest, bar_s_free0 = rest + 32;      // [warpgroup][tile]
+  // [warpgroup]: its sums of a unit are in shared memory; those have been read; steps of
+  // joining a cut unit
+  const uint32_t bar_part0 = rest + 64, bar_taken0 = rest + 80, bar_flag0 = rest + 96;
+  const uint32_t bar_drain0 = rest + 112;                          // [issuer]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOffset);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOffset + 4);
   WeighStart* const start = reinterpret_cast<WeighStart*>(smem + L::kStartOffset);
@@ -323,9 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_q_full(s), 1);
       mbar_init(bar_q_empty(s), 2);  // both issuers pass every block
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar_s_full0 + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar_s_full0 + 8 * i, 1);
       mbar_init(bar_s_free0 + 8 * i, 128);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar_part0 + 8 * i, 128);
       mbar_init(bar_taken0 + 8 * i, 128);
       mbar_init(bar_flag0 + 8 * i, 128);
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kHi = desc_hi_sw128(1024);
         int ks = 0, qs = -1;  // qs: the block's slot; -1 none yet
         uint32_t k_ph = 0, q_ph = 1;
-        uint32_t step = 0;
+        uint32_t step = 0, free_bits = 3u;  // [warpgroup]: parity of its next s_free phase; nothing to wait for at first
         bool held = false;  // a block that stays
         WeighCursor cur = weigh_cursor(p, *start);
         WeighSegment u;
@@ -478,14 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = wait_bounded(bar_q_full(qs), q_ph, wd, kSiteWeighQFull, true, kNapNs);
               if (!ok) break;
             }
-            const uint32_t wg = step & 1u, use = step++ >> 1;  // whose step, and which of its
-            // The warpgroup's step before has been read. (Waited for in every step, also of units
-            // without this tile: a barrier's phase is known by its parity alone, so no
-            // waiter may fall two phases behind or run ahead.)
-            ok = wait_bounded(bar_s_free0 + 8 * wg, (use & 1u) ^ 1u, wd, kSiteWeighSFree, true, kNapNs);
-            if (!ok) break;
+            const uint32_t wg = step++ & 1u;  // whose step
             if (live) {
+              // The warpgroup's step before with this tile has been read. (Tiles have barriers
+              // of their own: a barrier's phase is known by its parity alone, so whoever waits
+              // must wait for every phase, and not all units have the second tile.)
               const uint32_t buf = 2 * wg + t;
+              ok = wait_bounded(bar_s_free0 + 8 * buf, (free_bits >> wg) & 1u, wd, kSiteWeighSFree, true, kNapNs);
+              if (!ok) break;
+              free_bits ^= 1u << wg;
               tc_fence_after_sync();
               const uint32_t qa = desc_lo_sw128(sQ, 16) + ((static_cast<uint32_t>(qs) * q_slot) >> 4);
               const uint32_t dt = tmem + buf * 128;
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t wg = warp >> 2;
     const int key_lane = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 256;
-    const uint32_t bar_full = bar_s_full0 + 16 * wg, bar_free = bar_s_free0 + 8 * wg, bar_flag = bar_flag0 + 8 * wg;
+    const uint32_t bar_full = bar_s_full0 + 16 * wg, bar_free = bar_s_free0 + 16 * wg, bar_flag = bar_flag0 + 8 * wg;
     float* const lse = reinterpret_cast<float*>(smem + L::kLseOffset) + warp * 128;
     const float4* const l4 = reinterpret_cast<const float4*>(lse);
     float2* const part = reinterpret_cast<float2*>(smem + L::kPartOffset) + key_lane;  // [warpgroup][128]
@@ -600,6 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         full_ph[0] ^= 1u;
         if (two) full_ph[1] ^= 1u;
         tc_fence_after_sync();
+        auto give_back = [&]() {
+          mbar_arrive(bar_free);
+          if (two) mbar_arrive(bar_free + 8);
+        };
         if (now > 16) {
           // 32 columns of both tiles at a time. `masked`: a warp asks which of a tile's
           // columns its keys are seen from, and only where some are and some are not it
@@ -610,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32x32_two_wait(tS + c0, tS + 128 + c0, sr);
             if (c0 + 32 >= now) {
               tc_fence_before_sync();
-              mbar_arrive(bar_free);  // S^T is in registers: the buffers may be filled again
+              give_back();  // S^T is in registers: the buffers may be filled again
             }
             auto add = [&](int t, int lo, float(&acc)[4], auto each) {
 #pragma unroll
@@ -685,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (two) some(tS + 128, c0, lo1, acc1);
           }
           tc_fence_before_sync();
-          mbar_arrive(bar_free);
+          give_back();
         }
       }
       if (!ok) break;

@@ -333,3 +333,17 @@ def test_no_tokens_and_no_sequences():
     assert fa2.paged_attention_forward(q, b.kc, b.vc, *none)[0].shape == (0, 4, 64)
     n, kept = fa2.paged_cache_evict(b.kc, b.vc, b.weights, *none, b.table[:0], 4)
     assert n.shape == (0,) and kept.shape == (0, 2, 4)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_key_weights_where_many_units_lack_their_second_tile(D):
+    # lengths around 128 and 256, in runs: warpgroups and loads of the one tile go on without those of the other
+    lengths = [90] * 40 + [200] * 9 + [128] * 25 + [256, 257, 129, 1] * 20 + [300] * 30 + [60] * 60
+    for counts in ([1] * len(lengths), [1 + (i % 4) * 29 for i in range(len(lengths))]):
+        counts = [min(n, length) for n, length in zip(counts, lengths)]
+        b = Batch(lengths, counts, 4, D, 16, BF16, seed=21)
+        q = b.tokens(8)
+        lse = torch.full((b.T, 8), 5.0, device="cuda")
+        for most in (None, max(counts)):
+            w = ops().paged_key_weights(q, lse, b.kc, *b.batch, max_query_length=most)
+            check_key_weights(w, q, lse, b.kc, None, b.batch, D ** -0.5)
