@@ -84,6 +84,56 @@ __global__ void __launch_bounds__(kMoveThreads) fa2_paged_append_kernel(const Pa
 }
 
 // ------------------------------------------------------------------- evict
+// Keys, values and weights of the kept positions to their new pages: bound by
+// bytes. A warp takes runs of up to 32 rows: a lane looks up a row each, then
+// 16 bytes per lane and step, eight of them under way.
+template <int D>
+struct Moves {
+  static constexpr int kVecs = D / 8;
+  static constexpr int kRowsAtOnce = 32 / (2 * kVecs) > 0 ? 32 / (2 * kVecs) : 1;  // rows (K and V) of a step
+  static constexpr int kRun = kRowsAtOnce * kUnder;                                  // rows of a run: 8, 16 or 32
+  static_assert(kRun <= 32 && 2 * kVecs <= 32, "a lane per row and piece");
+
+  // By one warp: kept rows j0, j0 + 1, .. of key head bh (counted over the sequences).
+  static __device__ __forceinline__ void run(const PagedEvictParams& p, int bh, int j0) {
+    const int lane = threadIdx.x & 31, in_page = (1 << p.page_shift) - 1;
+    const int b = bh / p.heads, head = bh - b * p.heads;
+    // this lane's piece of a step: row, cache, 16 bytes
+    const int row_of = lane / (2 * kVecs), r = lane - row_of * 2 * kVecs;
+    const bool is_k = r < kVecs, works = row_of < kRowsAtOnce;
+    const int vec = is_k ? r : r - kVecs;
+    const PagedStrides& c = is_k ? p.ks : p.vs;
+    // lane l: row j0 + l; `from`: its old page or -1, `to`: its new one or -1
+    int src = -1, from = -1, to = -1;
+    if (lane < kRun && j0 + lane < p.keep) src = p.kept[static_cast<long long>(bh) * p.keep + j0 + lane];
+    if (src >= 0) {
+      from = paged_entry(p, b, src);
+      to = __ldg(p.new_table + b * p.new_stride + ((j0 + lane) >> p.page_shift));
+      if (!page_ok(p, from)) from = -1;
+      if (!page_ok(p, to)) to = -1;
+    }
+    if (__all_sync(0xffffffffu, src < 0)) return;
+    uint16_t* const cache = static_cast<uint16_t*>(is_k ? p.kc : p.vc) + head * c.head;
+    uint4 piece[kUnder];
+#pragma unroll
+    for (int i = 0; i < kUnder; ++i) {
+      const int row = i * kRowsAtOnce + (works ? row_of : 0);
+      const int f = __shfl_sync(0xffffffffu, from, row), s = __shfl_sync(0xffffffffu, src, row);
+      piece[i] = make_uint4(0u, 0u, 0u, 0u);  // of a position whose page is none
+      if (works && f >= 0) piece[i] = reinterpret_cast<const uint4*>(cache + f * c.page + (s & in_page) * c.slot)[vec];
+    }
+    float w = 0.f;
+    if (from >= 0) w = p.weights[((static_cast<long long>(from) * p.heads + head) << p.page_shift) + (src & in_page)];
+#pragma unroll
+    for (int i = 0; i < kUnder; ++i) {
+      const int row = i * kRowsAtOnce + (works ? row_of : 0);
+      const int t = __shfl_sync(0xffffffffu, to, row);
+      if (works && t >= 0) reinterpret_cast<uint4*>(cache + t * c.page + ((j0 + row) & in_page) * c.slot)[vec] = piece[i];
+    }
+    if (to >= 0) p.weights[((static_cast<long long>(to) * p.heads + head) << p.page_shift) + ((j0 + lane) & in_page)] = w;
+  }
+};
+
 // Which positions stay: of those before the last `recent` the `need` of the
 // greatest weight, found by a radix selection over the weights' bits as
 // unsigned integers in the same order (11, 11 and 10 bits at a time), then all
@@ -102,6 +152,8 @@ __device__ __forceinline__ uint32_t ordered_bits(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// `kMoves`: the block moves its key head's rows itself afterwards.
+template <int D, bool kMoves>
 __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(const PagedEvictParams p) {
   extern __shared__ __align__(16) uint32_t bits[];
   __shared__ int hist[kBins];
@@ -109,7 +161,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
   __shared__ int warp_above[kSelectWarps], warp_equal[kSelectWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  cudaTriggerProgrammaticLaunchCompletion();  // the moving kernel may take the SMs that are free
+  if constexpr (!kMoves) cudaTriggerProgrammaticLaunchCompletion();  // the moving kernel may take the SMs that are free
   const int b = blockIdx.x / p.heads, head = blockIdx.x - b * p.heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int length = min(max(__ldg(p.lengths + b), 0), p.capacity);
@@ -117,8 +169,15 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
   int* const kept = p.kept + static_cast<long long>(blockIdx.x) * p.keep;
   if (head == 0 && threadIdx.x == 0) p.new_lengths[b] = m;
   for (int i = m + threadIdx.x; i < p.keep; i += kSelectThreads) kept[i] = -1;
+  auto move = [&]() {
+    if constexpr (kMoves) {
+      __syncthreads();  // the kept positions are all written
+      for (int j0 = warp * Moves<D>::kRun; j0 < m; j0 += kSelectWarps * Moves<D>::kRun) Moves<D>::run(p, blockIdx.x, j0);
+    }
+  };
   if (length <= p.keep) {
     for (int i = threadIdx.x; i < m; i += kSelectThreads) kept[i] = i;
+    move();
     return;
   }
   const int old = length - p.recent;  // positive: recent <= keep < length
@@ -278,59 +337,20 @@ __global__ void __launch_bounds__(kSelectThreads, 1) fa2_paged_select_kernel(con
     }
   }
   for (int i = threadIdx.x; i < p.recent; i += kSelectThreads) kept[p.keep - p.recent + i] = old + i;
+  move();
 }
 
-// Keys, values and weights of the kept positions to their new pages: bound by
-// bytes. A warp takes runs of up to 32 rows: a lane looks up a row each, then
-// 16 bytes per lane and step, eight of them under way.
+// The moves of all key heads by as many warps as there are SMs for.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) fa2_paged_move_kernel(const PagedEvictParams p) {
-  constexpr int kVecs = D / 8;
-  constexpr int kRowsAtOnce = 32 / (2 * kVecs) > 0 ? 32 / (2 * kVecs) : 1;  // rows (K and V) of a step
-  constexpr int kRun = kRowsAtOnce * kUnder;                                  // rows of a run: 8, 16 or 32
-  static_assert(kRun <= 32 && 2 * kVecs <= 32, "a lane per row and piece");
   cudaGridDependencySynchronize();  // what the selection wrote
-  const int lane = threadIdx.x & 31;
+  constexpr int kRun = Moves<D>::kRun;
   const int runs = (p.keep + kRun - 1) / kRun;  // of a key head of a sequence
   const long long all = static_cast<long long>(p.B) * p.heads * runs;
   const long long warps = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
-  const int in_page = (1 << p.page_shift) - 1;
-  // this lane's piece of a step: row, cache, 16 bytes
-  const int row_of = lane / (2 * kVecs), r = lane - row_of * 2 * kVecs;
-  const bool is_k = r < kVecs, works = row_of < kRowsAtOnce;
-  const int vec = is_k ? r : r - kVecs;
-  const PagedStrides& c = is_k ? p.ks : p.vs;
   for (long long run = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); run < all; run += warps) {
-    const int bh = static_cast<int>(run / runs), j0 = static_cast<int>(run - static_cast<long long>(bh) * runs) * kRun;
-    const int b = bh / p.heads, head = bh - b * p.heads;
-    // lane l: row j0 + l; `from`: its old page or -1, `to`: its new one or -1
-    int src = -1, from = -1, to = -1;
-    if (lane < kRun && j0 + lane < p.keep) src = p.kept[static_cast<long long>(bh) * p.keep + j0 + lane];
-    if (src >= 0) {
-      from = paged_entry(p, b, src);
-      to = __ldg(p.new_table + b * p.new_stride + ((j0 + lane) >> p.page_shift));
-      if (!page_ok(p, from)) from = -1;
-      if (!page_ok(p, to)) to = -1;
-    }
-    if (__all_sync(0xffffffffu, src < 0)) continue;
-    uint16_t* const cache = static_cast<uint16_t*>(is_k ? p.kc : p.vc) + head * c.head;
-    uint4 piece[kUnder];
-#pragma unroll
-    for (int i = 0; i < kUnder; ++i) {
-      const int row = i * kRowsAtOnce + (works ? row_of : 0);
-      const int f = __shfl_sync(0xffffffffu, from, row), s = __shfl_sync(0xffffffffu, src, row);
-      piece[i] = make_uint4(0u, 0u, 0u, 0u);  // of a position whose page is none
-      if (works && f >= 0) piece[i] = reinterpret_cast<const uint4*>(cache + f * c.page + (s & in_page) * c.slot)[vec];
-    }
-    float w = 0.f;
-    if (from >= 0) w = p.weights[((static_cast<long long>(from) * p.heads + head) << p.page_shift) + (src & in_page)];
-#pragma unroll
-    for (int i = 0; i < kUnder; ++i) {
-      const int row = i * kRowsAtOnce + (works ? row_of : 0);
-      const int t = __shfl_sync(0xffffffffu, to, row);
-      if (works && t >= 0) reinterpret_cast<uint4*>(cache + t * c.page + ((j0 + row) & in_page) * c.slot)[vec] = piece[i];
-    }
-    if (to >= 0) p.weights[((static_cast<long long>(to) * p.heads + head) << p.page_shift) + ((j0 + lane) & in_page)] = w;
+    const int bh = static_cast<int>(run / runs);
+    Moves<D>::run(p, bh, static_cast<int>(run - static_cast<long long>(bh) * runs) * kRun);
   }
 }
 
@@ -349,11 +369,33 @@ cudaError_t launch_moves(F kern, const P& p, long long warps, int sms, bool depe
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Up to so many bytes of a key head the block that chose its rows moves them
+// too, without a second kernel. Of 2500 positions, D = 64 and 8 key heads (us,
+// one block / second kernel): 32 KB 10.6 / 11.3, 64 KB 11.2 / 11.5, 128 KB 13.3 /
+// 11.6; 256 key heads: 20.0 / 21.9, 21.6 / 21.9, 26.2 / 26.2; and the host
+// launches once.
+constexpr long long kOwnMoveBytes = 64 << 10;
+
+template <int D, bool kMoves>
+cudaError_t launch_select(const PagedEvictParams& p, cudaStream_t s) {
+  constexpr int kMost = kSelectKeys * 4;
+  auto kern = fa2_paged_select_kernel<D, kMoves>;
+  static PerDeviceOnce prepared;
+  const cudaError_t e = once_per_device(
+      prepared, [&]() { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost); });
+  if (e != cudaSuccess) return e;
+  kern<<<p.B * p.heads, kSelectThreads, std::min(p.capacity, kSelectKeys) * 4, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D>
-cudaError_t launch_move(const PagedEvictParams& p, int sms, cudaStream_t s) {
-  constexpr int rows = std::max(1, 32 / (2 * (D / 8))) * kUnder;
-  const long long warps = static_cast<long long>(p.B) * p.heads * ((p.keep + rows - 1) / rows);
-  return warps == 0 ? cudaSuccess : launch_moves(fa2_paged_move_kernel<D>, p, warps, sms, true, s);
+cudaError_t launch_evict(const PagedEvictParams& p, int sms, cudaStream_t s) {
+  if (static_cast<long long>(p.keep) * D * 4 <= kOwnMoveBytes) return launch_select<D, true>(p, s);
+  const cudaError_t e = launch_select<32, false>(p, s);  // the same for every head dimension
+  if (e != cudaSuccess) return e;
+  constexpr int rows = Moves<D>::kRun;
+  return launch_moves(fa2_paged_move_kernel<D>, p, static_cast<long long>(p.B) * p.heads * ((p.keep + rows - 1) / rows), sms,
+                      true, s);
 }
 
 }  // namespace
@@ -368,21 +410,11 @@ cudaError_t launch_paged_append(int D, const PagedAppendParams& p, int sms, cuda
 }
 
 cudaError_t launch_paged_evict(int D, const PagedEvictParams& p, int sms, cudaStream_t s) {
-  constexpr int kMost = kSelectKeys * 4;
-  static PerDeviceOnce prepared;
-  cudaError_t e = once_per_device(prepared, [&]() {
-    return cudaFuncSetAttribute(fa2_paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  });
-  if (e != cudaSuccess) return e;
-  const int smem = std::min(p.capacity, kSelectKeys) * 4;
-  fa2_paged_select_kernel<<<p.B * p.heads, kSelectThreads, smem, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   switch (D) {
-    case 32: return launch_move<32>(p, sms, s);
-    case 64: return launch_move<64>(p, sms, s);
-    case 96: return launch_move<96>(p, sms, s);
-    default: return launch_move<128>(p, sms, s);
+    case 32: return launch_evict<32>(p, sms, s);
+    case 64: return launch_evict<64>(p, sms, s);
+    case 96: return launch_evict<96>(p, sms, s);
+    default: return launch_evict<128>(p, sms, s);
   }
 }
 
