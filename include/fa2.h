@@ -702,10 +702,11 @@ FA2_API int fa2_set_watchdog_ns(unsigned long long ns);
  * fa2_test_withhold_next_load — test hook for the watchdog. When enable is
  * nonzero, the next launch of this library (process-wide, one launch only:
  * a forward kernel, the main kernel of fa2_bwd or fa2_cross_bwd, or a kernel
- * of fa2_cross_fwd, fa2_paged_fwd or fa2_paged_key_weights that waits for tiles) withholds its first K/V
- * tile: the waits for that tile run out after the watchdog time, the kernel
- * records the wait site in the watchdog word, winds down without leaving
- * work in flight, and its outputs (O/LSE, or dQ/dK/dV) are left unspecified.
+ * of fa2_cross_fwd, fa2_paged_fwd or fa2_paged_key_weights that waits for
+ * tiles) withholds its first K/V tile: the waits for that tile run out after
+ * the watchdog time, the kernel records the wait site in the watchdog word,
+ * winds down without leaving work in flight, and its outputs (O/LSE, or
+ * dQ/dK/dV) are left unspecified.
  * No GPU fault, trap or hang is involved. Returns FA2_OK.
  */
 FA2_API int fa2_test_withhold_next_load(int enable);
