@@ -25,13 +25,13 @@
 //             warp's 32 rows, where they are whole tokens of the sequence, made
 //             no difference: 222 and 220 us for four prompts of 4096.)
 //
-// Measured: four prompts of 4096, 32 query heads on 8 key heads of 128, 220 us
+// Measured: four prompts of 4096, 16 query heads on 4 key heads of 128, 220 us
 // (1,250 TFLOP/s, 64 % of the measured peak; floor 140): a tile step takes about
 // 1.3 us, bound by shared memory (K, V and P are read from it) with a ring of
 // three tiles, and the power cap lowers the clock. 512 tokens over 8192
-// positions, same heads: 58 us (floor 34), with about 5 for the start (search of
-// the share, first instructions and loads) and a join of cut units at the end. At
-// D = 64 the exponentials bound it. Issuers by type where D > 64 and by sub-tile
+// positions, 32 query heads on 8 key heads: 58 us (floor 34), with about 5 for the
+// start (search of the share, first instructions and loads) and a join of cut
+// units at the end. At D = 64 the exponentials bound it. Issuers by type where D > 64 and by sub-tile
 // below, as in fa2_kernel.cuh; at D = 64 that, rows without a token unmasked and
 // the rules for cutting took a mixed batch from 88 to 66 us together.
 #pragma once

@@ -28,8 +28,8 @@
 // Measured: single tokens of 64 sequences of up to 4096 positions, 8 key heads of
 // 128 with 4 query heads each, 91 to 97 us, 6.0 TB/s (88 % of the measured copy;
 // floor 80.5): equal shares end between 64 and 92 us, some SMs' loads are served
-// slower. 4 sequences of 1500 positions, 12 heads of 64: 9.7 us, latency (start,
-// two to five tiles, join). Whole units instead of cut ones, where each SM would
+// slower. 4 sequences of up to 1000 positions, 12 heads of 64: 9.7 us, latency
+// (start, two or three tiles, join). Whole units instead of cut ones, where each SM would
 // have one: 12.5 against 10.6 us and 12.1 against 9.0.
 //
 // Positions that a row does not see have their scores set to -inf; V behind the

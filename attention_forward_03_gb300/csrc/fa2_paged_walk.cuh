@@ -209,12 +209,18 @@ __device__ __forceinline__ PagedStart paged_start(const PagedTileParams& p) {
   // fewer units than CTAs, and all about as long as the longest
   const bool alike = 10 * tiles >= 9 * all * most;
   if (all < gridDim.x && alike) st.parts = cut_parts(p, tiles, static_cast<int>(all), most);
-  // Short units are not cut where the CTA with the most of them has less to do than a
-  // cut and a join take (in tiles: 5 and 1.6). 51 sequences of 213 tokens: cut 32.6
-  // us, whole 24.8.
+  // Units are not cut where what the CTA with the most of them has to do beyond an
+  // equal share (of units of very different lengths: one of the longest) costs less
+  // than the cuts: in tiles, a cut and a join, and about one more for every unit of a
+  // share. Fitted to 160 to 800 units (us whole / cut at 1.3 and at 5.3 units to a
+  // CTA). D = 128, all of 8 tiles: 40.2 / 39.1 and 113 / 123, of 16: 65.6 / 56.9 and
+  // 196 / 186, of up to 8: 29.9 / 28.9 and 83 / 97, of up to 16: 44.8 / 41.4 and 130 /
+  // 130. D = 64: 30.4 / 27.3 and 81 / 85, 49.4 / 41.3 and 139 / 131, 25.2 / 22.7 and
+  // 64 / 68, 34.5 / 29.3 and 98 / 93.
   if (!st.parts) {
     const float mean = static_cast<float>(sum) / static_cast<float>(all), each = static_cast<float>(all) / static_cast<float>(gridDim.x);
-    st.whole = (alike ? (ceilf(each) - each) * mean : static_cast<float>(most + kPagedUnitCost)) <= 6.6f;
+    st.whole = alike ? (ceilf(each) - each) * mean <= each + (p.wide ? 6.f : 5.f)
+                     : static_cast<float>(most + kPagedUnitCost) <= each + (p.wide ? 12.f : 7.f);
   }
   if (st.parts) {
     // this CTA's unit, counted over the sequences
