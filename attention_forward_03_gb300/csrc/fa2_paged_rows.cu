@@ -17,8 +17,9 @@
 // page (page sizes are multiples of 16), for all rows and works on its own. It
 // has a ring of 16-position pieces of K and V that its first lane fills by TMA,
 // a barrier of its own for each, and no other warp to wait for until the unit's
-// end. The page number of the piece after next is under way while one is
-// requested. S comes from mma.m16n8k16 (rows x keys, Q in registers for the
+// end. The page numbers of its pieces of 32 tiles are read at once, one per lane
+// (one per piece, a piece ahead, and the loads waited for it: 95 us below, 89 so).
+// S comes from mma.m16n8k16 (rows x keys, Q in registers for the
 // whole unit), the weights stay in registers in the layout that the second
 // product's A operand has, O (rows x D) accumulates in fp32 registers. The
 // exponent base of a row lags its maximum by up to 2^8, as in the other
@@ -26,9 +27,9 @@
 // merged through shared memory.
 //
 // Measured: single tokens of 64 sequences of up to 4096 positions, 8 key heads of
-// 128 with 4 query heads each, 91 to 97 us, 6.0 TB/s (88 % of the measured copy;
-// floor 80.5): equal shares end between 64 and 92 us, some SMs' loads are served
-// slower. 4 sequences of up to 1000 positions, 12 heads of 64: 9.7 us, latency
+// 128 with 4 query heads each, 89 to 91 us, 6.1 TB/s (90 % of the measured copy; floor
+// 80.5), for pages of 16 as for those of 256: equal shares end up to a fifth
+// apart, some SMs' loads are served slower. 4 sequences of up to 1000 positions, 12 heads of 64: 9.7 us, latency
 // (start, two or three tiles, join). Whole units instead of cut ones, where each SM would
 // have one: 12.5 against 10.6 us and 12.1 against 9.0.
 //
@@ -291,17 +292,23 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   const long long first_step = cur.step;
   // whether this warp's piece of a tile has a key
   auto has_keys = [&](const TileCursor& t) { return t.tile * kPagedRowsKeys + warp * kPiece < t.keys; };
-  TileCursor ahead = cur;  // the tile whose piece is requested next, and its page
-  int page = 0;
+  TileCursor ahead = cur;  // the tile whose piece is requested next
+  // the pages of this warp's pieces of 32 tiles of a sequence, one per lane
+  int pages = 0, pages_b = -1, pages_tile = 0;
   int into = 0;       // its ring slot
   int under_way = 0;  // pieces requested and not yet used
   auto find_page = [&]() {
     while (ahead.step < s1 && !has_keys(ahead)) ahead.next(p);
-    if (ahead.step < s1) page = paged_entry(p, ahead.b, ahead.tile * kPagedRowsKeys + warp * kPiece);
+    if (ahead.step >= s1 || (ahead.b == pages_b && (ahead.tile & ~31) == pages_tile)) return;
+    pages_b = ahead.b;
+    pages_tile = ahead.tile & ~31;
+    const int at = (pages_tile + lane) * kPagedRowsKeys + warp * kPiece;
+    pages = at < ahead.s.length ? paged_entry(p, ahead.b, at) : -1;
   };
   const uint64_t once = l2_policy_evict_first();
   auto request = [&]() {
     if (ahead.step >= s1) return;
+    const int page = __shfl_sync(0xffffffffu, pages, ahead.tile & 31);
     if (lane == 0) {
       const bool ok = page_ok(p, page);
       no_page[into] = !ok;
