@@ -600,18 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (q + 2 < u.end) read_block(u, q + 2, token0, valid, row_lse);
         }
-        bool got = wait_bounded(bar_full, full_ph[0], wd, kSiteWeighSFull);
-        if (two) got = got && wait_bounded(bar_full + 8, full_ph[1], wd, kSiteWeighSFull);
-        got = __all_sync(0xffffffffu, got);
-        if (!got) { ok = false; break; }
-        full_ph[0] ^= 1u;
-        if (two) full_ph[1] ^= 1u;
-        tc_fence_after_sync();
-        auto give_back = [&]() {
-          mbar_arrive(bar_free);
-          if (two) mbar_arrive(bar_free + 8);
+        auto filled = [&](int t) {  // the step's S^T of tile t is there
+          bool got = wait_bounded(bar_full + 8 * t, full_ph[t], wd, kSiteWeighSFull);
+          got = __all_sync(0xffffffffu, got);
+          full_ph[t] ^= 1u;
+          tc_fence_after_sync();
+          return got;
         };
+        if (!filled(0)) { ok = false; break; }
         if (now > 16) {
+          if (two && !filled(1)) { ok = false; break; }
           // 32 columns of both tiles at a time. `masked`: a warp asks which of a tile's
           // columns its keys are seen from, and only where some are and some are not it
           // asks each. (Where the second tile has no position its columns are anything:
@@ -621,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32x32_two_wait(tS + c0, tS + 128 + c0, sr);
             if (c0 + 32 >= now) {
               tc_fence_before_sync();
-              give_back();  // S^T is in registers: the buffers may be filled again
+              mbar_arrive(bar_free);  // S^T is in registers: the buffers may be filled again
+              if (two) mbar_arrive(bar_free + 8);
             }
             auto add = [&](int t, int lo, float(&acc)[4], auto each) {
 #pragma unroll
@@ -674,29 +673,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c0 = 0; c0 < now; c0 += 32) chunk(c0, std::true_type{});
           }
         } else {
-          // eight columns at a time: single tokens' blocks have few
-          auto some = [&](uint32_t from, int c0, int lo, float (&acc)[4]) {
-            uint32_t sr[8];
-            tmem_ld32x8_wait(from + c0, sr);
+          // eight columns at a time: single tokens' blocks have few. One tile after the
+          // other, the second one's product under way meanwhile.
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float4 l = l4[c0 / 4 + i];
-              const float x[4] = {l.x, l.y, l.z, l.w};
+          for (int t = 0; t < 2; ++t) {
+            if (t == 1) {
+              if (!two) break;
+              if (!filled(1)) { ok = false; break; }
+            }
+            const int lo = t == 0 ? lo0 : lo1;
+            float(&acc)[4] = t == 0 ? acc0 : acc1;
+#pragma unroll 1
+            for (int c0 = 0; c0 < now; c0 += 8) {
+              uint32_t sr[8];
+              tmem_ld32x8_wait(tS + 128 * t + c0, sr);
+              if (c0 + 8 >= now) {
+                tc_fence_before_sync();
+                mbar_arrive(bar_free + 8 * t);
+              }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int col = c0 + 4 * i + j;
-                const float w = ex2_approx(fmaf(__uint_as_float(sr[4 * i + j]), c, x[j]));
-                acc[j] += col >= lo && col < now ? w : 0.f;
+              for (int i = 0; i < 2; ++i) {
+                const float4 l = l4[c0 / 4 + i];
+                const float x[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int col = c0 + 4 * i + j;
+                  const float w = ex2_approx(fmaf(__uint_as_float(sr[4 * i + j]), c, x[j]));
+                  acc[j] += col >= lo && col < now ? w : 0.f;
+                }
               }
             }
-          };
-#pragma unroll 1
-          for (int c0 = 0; c0 < now; c0 += 8) {
-            some(tS, c0, lo0, acc0);
-            if (two) some(tS + 128, c0, lo1, acc1);
           }
-          tc_fence_before_sync();
-          give_back();
+          if (!ok) break;
         }
       }
       if (!ok) break;
