@@ -64,7 +64,11 @@ struct PagedTileParams : PagedAttnParams {
   int sub_tokens;   // tokens of a sub-tile: 128 / group
   int page_rows;    // positions of a page in one K/V tile: min(page size, 128)
   int wide;         // head dimension above 64
+  unsigned long long* ws_spread;  // [2][grid][kPagedMostParts]: which parts of its unit a CTA may read
 };
+// Parts that a unit is cut into at most.
+constexpr int kPagedMostParts = 32;
+constexpr size_t paged_spread_bytes(int grid) { return static_cast<size_t>(grid) * 2 * kPagedMostParts * 8; }
 template <int D, bool kBf16>
 cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                const PagedTileParams& p, int grid, cudaStream_t stream);

@@ -159,9 +159,11 @@ size_t tokens_reach(int T, long long token, int heads, long long head, int D) {
   return static_cast<size_t>((T - 1) * token * (T > 1) + (heads - 1) * head * (heads > 1) + D) * 2;
 }
 
-// The rows kernel's partial results, then the tiles kernel's.
+// The rows kernel's partial results, then the tiles kernel's, then its flags for units that all of their CTAs join.
 size_t rows_workspace(int sms, int D) { return paged_rows_workspace_bytes(std::min(sms, kPagedRowsMaxCtas), D); }
-size_t fwd_workspace_bytes(int sms, int D) { return rows_workspace(sms, D) + stream_k_workspace_bytes(sms, D); }
+size_t fwd_workspace_bytes(int sms, int D) {
+  return rows_workspace(sms, D) + stream_k_workspace_bytes(sms, D) + paged_spread_bytes(sms);
+}
 
 using TilesFn = cudaError_t (*)(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const PagedTileParams&, int,
                                 cudaStream_t);
@@ -300,7 +302,7 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   const int64_t most = static_cast<int64_t>(longest) * group;
   const int64_t blocks = std::min(static_cast<int64_t>(B) * ((most + kPagedRows - 1) / kPagedRows),
                                   static_cast<int64_t>(T) * group / kPagedRows + B) * Hkv;
-  const bool tiles = most > kPagedRows && group <= kRows && blocks > 48;
+  const bool tiles = most > kPagedRows && group <= kRows && blocks > (D > 64 ? 16 : 24);
   // A sequence of so few tokens would leave the others more than `longest` each.
   const int few = kPagedRows / group;
   const bool none_short = group > kPagedRows || (longest > few && static_cast<int64_t>(B) * longest - T < longest - few);
@@ -338,6 +340,7 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   p.ws_stats = p.ws_o + slots * D * 128;
   p.ws_flags = reinterpret_cast<unsigned long long*>(
       ws + rows_workspace(sms, D) + (slots * (static_cast<size_t>(D) * 128 + 3 * 128) * sizeof(float) + 255) / 256 * 256);
+  p.ws_spread = reinterpret_cast<unsigned long long*>(ws + rows_workspace(sms, D) + stream_k_workspace_bytes(sms, D));
   p.epoch = next_launch_epoch();
   return cuda_result(pick_tiles(D, bf)(mq, mk, mv, p, sms, s));
 }

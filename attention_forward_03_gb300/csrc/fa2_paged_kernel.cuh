@@ -436,6 +436,91 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_phase = 0, o_phase = 0, part_phase = 0;
     uint32_t p_count = 0;  // P tiles published so far
     bool ok = true;
+    // By a warpgroup of each of the `parts` CTAs that hold a unit: every parts-th 8 or 16
+    // rows of its sub-tile, from all partial results (the first holder alone, one partial
+    // result after another: 23 us for 19 of them). The rows' statistics are read at once,
+    // then 4 rows of a column per thread from several holders at a time.
+    auto join_rows = [&](const PagedSegment& u, int parts, auto per) {
+      constexpr int kPer = per.value;
+      auto meet = [&]() {  // of the warpgroup's threads
+        mbar_arrive(bar_part);
+        bool met = wait_bounded(bar_part, part_phase, wd, kSitePartialFlag);
+        part_phase ^= 1u;
+        return __all_sync(0xffffffffu, met) != 0;
+      };
+      const int first = blockIdx.x - start->part;
+      unsigned long long* const flags = p.ws_spread + (static_cast<size_t>(t) * gridDim.x + blockIdx.x) * kPagedMostParts;
+      bool fine = lane >= parts || wait_flag(flags + lane, p.epoch, wd, kSitePartialFlag);
+      fine = __all_sync(0xffffffffu, fine);
+      if (!fine) return;
+      __syncwarp();  // what one lane acquired is visible to all
+      // seen by every thread of the warpgroup: taken back, so that a replay of a captured
+      // launch, which carries the same tag, does not find them
+      if (!meet()) return;
+      if (rr < parts) flags[rr] = 0ull;
+      // in the P buffer, which is free: [part][row] bases, l, l_o, weights, then base, l, l_o of the rows
+      constexpr int kAll = kPagedMostParts * kPer;
+      float* const sm = reinterpret_cast<float*>(smem + L::kPOffset + t * L::kPBytes);
+      float* const total = sm + 4 * kAll;
+      const int token0 = u.token + t * p.sub_tokens, rows = min(p.sub_tokens, u.n - token0) * p.group;
+      const float* const po = p.ws_o + (static_cast<size_t>(first) * 2 + t) * D * 128;
+      const float* const ps = p.ws_stats + (static_cast<size_t>(first) * 2 + t) * 3 * 128;
+      for (int row0 = kPer * start->part; row0 < rows; row0 += kPer * parts) {
+        const int row = rr % kPer;
+        for (int j = rr / kPer; j < parts; j += 128 / kPer) {
+          const float* const from = ps + static_cast<size_t>(j) * 2 * 3 * 128 + row0 + row;
+          const float a = __ldcg(from), b = __ldcg(from + 128), d = __ldcg(from + 256);
+          sm[j * kPer + row] = a;
+          sm[kAll + j * kPer + row] = b;
+          sm[2 * kAll + j * kPer + row] = d;
+        }
+        if (!meet()) return;
+        float top = -CUDART_INF_F;
+        for (int j = 0; j < parts; ++j) top = fmaxf(top, sm[j * kPer + row]);
+        auto weight = [&](int j) {
+          const float b = sm[j * kPer + row];
+          return b == -CUDART_INF_F ? 0.f : ex2_approx(b - top);
+        };
+        for (int j = rr / kPer; j < parts; j += 128 / kPer) sm[3 * kAll + j * kPer + row] = weight(j);
+        if (rr < kPer) {
+          float l = 0.f, l_o = 0.f;
+          for (int j = 0; j < parts; ++j) {
+            const float e = weight(j);
+            l = fmaf(e, sm[kAll + j * kPer + row], l);
+            l_o = fmaf(e, sm[2 * kAll + j * kPer + row], l_o);
+          }
+          total[row] = top;
+          total[kPer + row] = l;
+          total[2 * kPer + row] = l_o;
+        }
+        if (!meet()) return;
+        const int q = 4 * (rr % (kPer / 4));
+        for (int col = rr / (kPer / 4); col < D; col += 512 / kPer) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+          for (int j = 0; j < parts; ++j) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(po + (static_cast<size_t>(j) * 2 * D + col) * 128 + row0 + q));
+            const float4 e = *reinterpret_cast<const float4*>(sm + 3 * kAll + j * kPer + q);
+            acc[0] = fmaf(e.x, x.x, acc[0]);
+            acc[1] = fmaf(e.y, x.y, acc[1]);
+            acc[2] = fmaf(e.z, x.z, acc[2]);
+            acc[3] = fmaf(e.w, x.w, acc[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = row0 + q + i;
+            if (at >= rows) break;
+            const float l = total[kPer + q + i];
+            const float inv = l > 0.f ? __frcp_rn(total[2 * kPer + q + i]) : 0.f;
+            const int tok = at / p.group;
+            const long long to = (static_cast<long long>(u.t0 + token0 + tok) * p.heads + u.head) * p.group + (at - tok * p.group);
+            static_cast<uint16_t*>(p.o)[to * D + col] = static_cast<uint16_t>(pack2(acc[i] * inv, 0.f, kBf16) & 0xffffu);
+            if (col == 0) p.lse[to] = l != 0.f ? (total[q + i] + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;
+          }
+        }
+        if (row0 + kPer * parts < rows && !meet()) return;  // read before the next rows' are written there
+      }
+    };
     PagedCursor cur = paged_first(p, *start);
     PagedSegment w;
     while (ok && paged_next(cur, w, p)) {
@@ -544,8 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!got) break;
       o_phase ^= 1u;
       tc_fence_after_sync();
-      if (w.kv_begin > 0) {
-        // Not the unit's first tiles: the unnormalised partial (O, base, l, l_o) to the owner.
+      const int spread = start->parts >= kPagedSpreadParts ? start->parts : 0;
+      if (w.kv_begin > 0 || spread) {
+        // Not the unit's first tiles: the unnormalised partial (O, base, l, l_o) to the owner,
+        // or to all that the unit is cut between.
         const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + t;
         float* po = p.ws_o + slot * D * 128;
         float* ps = p.ws_stats + slot * 3 * 128;
@@ -565,10 +652,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool done = wait_bounded(bar_part, part_phase, wd, kSitePartialWrite);
           done = __all_sync(0xffffffffu, done);
           if (!done) break;
-          if (rr == 0) store_release(p.ws_flags + slot, p.epoch);
+          if (spread) {
+            if (lane < spread)
+              store_release(p.ws_spread + (static_cast<size_t>(t) * gridDim.x + blockIdx.x - start->part + lane) * kPagedMostParts + start->part,
+                            p.epoch);
+          } else if (rr == 0) {
+            store_release(p.ws_flags + slot, p.epoch);
+          }
         }
         part_phase ^= 1u;
         tc_fence_before_sync();
+        if (spread) {
+          if (spread >= 16) join_rows(w, spread, std::integral_constant<int, 8>{});
+          else join_rows(w, spread, std::integral_constant<int, 16>{});
+          break;  // the share's only segment
+        }
         continue;
       }
       // Owner (or whole unit): fold in the partials of the CTAs that took the rest of it, if any.

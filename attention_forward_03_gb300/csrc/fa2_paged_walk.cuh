@@ -156,6 +156,12 @@ __device__ __forceinline__ int find_entry(int B, long long want, long long first
   return 0;  // only should the tables have changed meanwhile
 }
 
+// A unit in so many parts or more is joined by all of its CTAs, 16 rows of a
+// sub-tile at a time (8 of 16 parts or more); below, by its first part's.
+constexpr int kPagedSpreadParts = 6;
+constexpr float kSpreadCut = 7.f, kSpreadSlice = 1.f;
+static_assert(kPagedMostParts == 32, "a number of parts per lane");
+
 // Whether and how to cut units when there are fewer than CTAs, all of about
 // `most` tiles: into how many parts each, or 0 for equal shares over all CTAs. In
 // tiles: a cut costs the way through memory, every part that the unit's first
@@ -169,8 +175,11 @@ __device__ __forceinline__ int cut_parts(const PagedTileParams& p, long long til
   const float cut = 8.f, cut_equal = 5.f, join = p.wide ? 1.6f : 1.f;
   const int parts = lane + 1;
   float cost = 3e38f;
-  if (parts * units <= static_cast<int>(gridDim.x) && parts <= most)
-    cost = static_cast<float>((most + parts - 1) / parts) + (parts > 1 ? cut + join * static_cast<float>(parts - 1) : 0.f);
+  if (parts * units <= static_cast<int>(gridDim.x) && parts <= most) {
+    cost = static_cast<float>((most + parts - 1) / parts);
+    if (parts >= kPagedSpreadParts) cost += parts >= 16 ? kSpreadCut : kSpreadCut + kSpreadSlice * static_cast<float>((8 + parts - 1) / parts);
+    else if (parts > 1) cost += cut + join * static_cast<float>(parts - 1);
+  }
   float best = cost;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, off));
@@ -236,14 +245,14 @@ __device__ __forceinline__ PagedStart paged_start(const PagedTileParams& p) {
     const int r = index - static_cast<int>(before);
     st.head = min(r / u.units, p.heads - 1);
     st.unit = min(r - st.head * u.units, u.units - 1);
-    // No more parts than tiles, so that every part after the first with a tile has one.
-    // Steps are counted from the unit's first.
-    const int its = key_tiles(unit_keys(p, u.s, st.unit)), per_unit = its + kPagedUnitCost;
+    // No more parts than tiles, so that every part has one. Steps are counted from the
+    // unit's first; those that stand for no tile are left out.
+    const int its = key_tiles(unit_keys(p, u.s, st.unit));
     st.parts = min(st.parts, its);
     if (st.part >= st.parts) return st;
-    st.from = per_unit * st.part / st.parts;
+    st.from = kPagedUnitCost + its * st.part / st.parts;
     st.begin = st.from;
-    st.end = per_unit * (st.part + 1) / st.parts;
+    st.end = kPagedUnitCost + its * (st.part + 1) / st.parts;
     return st;
   }
   st.begin = paged_share_begin(st, blockIdx.x);
