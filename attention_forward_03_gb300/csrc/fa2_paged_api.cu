@@ -292,12 +292,12 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   // sub-tile); each kernel passes over the other's. Only the device knows the
   // sequences' tokens, so both are launched unless the sizes rule one out.
   //
-  // The rows kernel takes them all (in blocks of 16 rows) where there are at
-  // most 48 blocks: its CTAs share the keys of few units better (us, rows kernel
-  // / tensor cores, 4 query heads to a key head: 8 key heads of 64 over 4000
-  // positions, 32 rows 12.0 / 20.1, 96 rows 17.6 / 20.1, 128 rows 20.7 / 20.1; of
-  // 128, 64 rows 19.9 / 23.9, 128 rows 26.1 / 23.9; 64 key heads of 64, 32 rows
-  // over 100 positions 7.0 / 9.2, over 4000 31.2 / 26.2).
+  // The rows kernel takes them all (in blocks of 16 rows) where there are few
+  // blocks (us, rows kernel / tensor cores, over 300, 1000, 4000 and 16,000
+  // positions; D = 128, 16 blocks: 11.2 / 10.2, 14.3 / 15.5, 15.3 / 18.4, 25.9 / 26.6;
+  // 32 blocks: 12.3 / 10.4, 14.4 / 15.5, 19.9 / 18.6, 39.6 / 26.7; D = 64, 24 blocks:
+  // 9.3 / 9.5, 10.8 / 14.6, 13.8 / 16.2, 25.6 / 22.4; 48 blocks: 10.0 / 9.4, 11.8 / 14.5,
+  // 17.2 / 16.2, 40.2 / 22.3). The host does not know the positions.
   const int longest = query_starts ? std::min(T, max_query_length) : p.each;
   const int64_t most = static_cast<int64_t>(longest) * group;
   const int64_t blocks = std::min(static_cast<int64_t>(B) * ((most + kPagedRows - 1) / kPagedRows),

@@ -31,9 +31,10 @@
 // three tiles, and the power cap lowers the clock. 512 tokens over 8192
 // positions, 32 query heads on 8 key heads: 58 us (floor 34), with about 5 for the
 // start (search of the share, first instructions and loads) and a join of cut
-// units at the end. At D = 64 the exponentials bound it. Issuers by type where D > 64 and by sub-tile
-// below, as in fa2_kernel.cuh; at D = 64 that, rows without a token unmasked and
-// the rules for cutting took a mixed batch from 88 to 66 us together.
+// units at the end; 64 tokens 26 us, a unit's 19 CTAs joining its rows. At D = 64
+// the exponentials bound it. Issuers by type where D > 64 and by sub-tile below, as
+// in fa2_kernel.cuh; at D = 64 that, rows without a token unmasked and the rules for
+// cutting took a mixed batch from 88 to 66 us together.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // By a warpgroup of each of the `parts` CTAs that hold a unit: every parts-th 8 or 16
     // rows of its sub-tile, from all partial results (the first holder alone, one partial
     // result after another: 23 us for 19 of them). The rows' statistics are read at once,
-    // then 4 rows of a column per thread from several holders at a time.
+    // then 4 rows of two columns per thread from eight holders at a time.
     auto join_rows = [&](const PagedSegment& u, int parts, auto per) {
       constexpr int kPer = per.value;
       auto meet = [&]() {  // of the warpgroup's threads
@@ -495,16 +496,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!meet()) return;
         const int q = 4 * (rr % (kPer / 4));
-        for (int col = rr / (kPer / 4); col < D; col += 512 / kPer) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-          for (int j = 0; j < parts; ++j) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(po + (static_cast<size_t>(j) * 2 * D + col) * 128 + row0 + q));
-            const float4 e = *reinterpret_cast<const float4*>(sm + 3 * kAll + j * kPer + q);
-            acc[0] = fmaf(e.x, x.x, acc[0]);
-            acc[1] = fmaf(e.y, x.y, acc[1]);
-            acc[2] = fmaf(e.z, x.z, acc[2]);
-            acc[3] = fmaf(e.w, x.w, acc[3]);
+        // two columns at a time, eight holders' loads of both under way
+        constexpr int kStep = 512 / kPer;
+        for (int col = rr / (kPer / 4); col < D; col += 2 * kStep) {
+          float acc[2][4] = {};
+          const bool two = col + kStep < D;
+          const float* const from = po + static_cast<size_t>(col) * 128 + row0 + q;
+#pragma unroll 1
+          for (int j0 = 0; j0 < parts; j0 += 8) {
+            float4 x[2][8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float* const at = from + static_cast<size_t>(j0 + k) * 2 * D * 128;
+              x[0][k] = x[1][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (j0 + k < parts) x[0][k] = __ldcg(reinterpret_cast<const float4*>(at));
+              if (j0 + k < parts && two) x[1][k] = __ldcg(reinterpret_cast<const float4*>(at + kStep * 128));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (j0 + k >= parts) break;
+              const float4 e = *reinterpret_cast<const float4*>(sm + 3 * kAll + (j0 + k) * kPer + q);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                acc[h][0] = fmaf(e.x, x[h][k].x, acc[h][0]);
+                acc[h][1] = fmaf(e.y, x[h][k].y, acc[h][1]);
+                acc[h][2] = fmaf(e.z, x[h][k].z, acc[h][2]);
+                acc[h][3] = fmaf(e.w, x[h][k].w, acc[h][3]);
+              }
+            }
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -514,7 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = l > 0.f ? __frcp_rn(total[2 * kPer + q + i]) : 0.f;
             const int tok = at / p.group;
             const long long to = (static_cast<long long>(u.t0 + token0 + tok) * p.heads + u.head) * p.group + (at - tok * p.group);
-            static_cast<uint16_t*>(p.o)[to * D + col] = static_cast<uint16_t>(pack2(acc[i] * inv, 0.f, kBf16) & 0xffffu);
+            uint16_t* const o = static_cast<uint16_t*>(p.o) + to * D + col;
+            *o = static_cast<uint16_t>(pack2(acc[0][i] * inv, 0.f, kBf16) & 0xffffu);
+            if (two) o[kStep] = static_cast<uint16_t>(pack2(acc[1][i] * inv, 0.f, kBf16) & 0xffffu);
             if (col == 0) p.lse[to] = l != 0.f ? (total[q + i] + __log2f(l)) * 0.69314718055994530942f : CUDART_INF_F;
           }
         }

@@ -27,11 +27,12 @@
 // merged through shared memory.
 //
 // Measured: single tokens of 64 sequences of up to 4096 positions, 8 key heads of
-// 128 with 4 query heads each, 89 to 91 us, 6.1 TB/s (90 % of the measured copy; floor
-// 80.5), for pages of 16 as for those of 256: equal shares end up to a fifth
-// apart, some SMs' loads are served slower. 4 sequences of up to 1000 positions, 12 heads of 64: 9.7 us, latency
-// (start, two or three tiles, join). Whole units instead of cut ones, where each SM would
-// have one: 12.5 against 10.6 us and 12.1 against 9.0.
+// 128 with 4 query heads each, 88 to 91 us, 6.1 TB/s (90 % of the measured copy;
+// floor 80.5), for pages of 16 as for those of 256: equal shares end up to a fifth
+// apart, some SMs' loads are served slower. 4 sequences of up to 1000 positions,
+// 12 heads of 64: 10 us, latency (start, two or three tiles, join). Whole units
+// instead of cut ones, where each SM would have one: 12.5 against 10.6 us and 12.1
+// against 9.0.
 //
 // Positions that a row does not see have their scores set to -inf; V behind the
 // sequence's positions is set to zero in registers, so what lies there is never

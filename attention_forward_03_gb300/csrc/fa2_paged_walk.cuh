@@ -159,7 +159,7 @@ __device__ __forceinline__ int find_entry(int B, long long want, long long first
 // A unit in so many parts or more is joined by all of its CTAs, 16 rows of a
 // sub-tile at a time (8 of 16 parts or more); below, by its first part's.
 constexpr int kPagedSpreadParts = 6;
-constexpr float kSpreadCut = 7.f, kSpreadSlice = 1.f;
+constexpr float kSpreadCut = 4.f, kSpreadPart = 0.3f;
 static_assert(kPagedMostParts == 32, "a number of parts per lane");
 
 // Whether and how to cut units when there are fewer than CTAs, all of about
@@ -167,9 +167,11 @@ static_assert(kPagedMostParts == 32, "a number of parts per lane");
 // tiles: a cut costs the way through memory, every part that the unit's first
 // holder adds to its own another, and shares that do not end where units do
 // make a CTA work on parts of two. The warp's lanes take a number of parts each.
-// Fitted to sweeps; 8 units of 8192 positions, D = 128, equal shares / whole
-// parts: 16 tokens 42.4 / 33.6 us, 64 tokens 50.0 / 40.8; 512 tokens (64 units)
-// 58.8 / 66, for which the rule takes equal shares.
+// Units that all of their CTAs join cost less, and each part 0.3. Fitted to sweeps
+// of 16 to 512 tokens of 2 and 8 key heads over 1000 to 32,000 positions; D = 128,
+// 8 key heads of 8192 positions: 16 tokens 42.4 us in equal shares, 33.6 joined by
+// the first part's CTA, 20 by all; 64 tokens 50.0, 40.8, 26; 512 tokens (64 units)
+// 58.8 in equal shares and 66 in two parts, for which the rule takes the former.
 __device__ __forceinline__ int cut_parts(const PagedTileParams& p, long long tiles, int units, int most) {
   const int lane = threadIdx.x & 31;
   const float cut = 8.f, cut_equal = 5.f, join = p.wide ? 1.6f : 1.f;
@@ -177,7 +179,8 @@ __device__ __forceinline__ int cut_parts(const PagedTileParams& p, long long til
   float cost = 3e38f;
   if (parts * units <= static_cast<int>(gridDim.x) && parts <= most) {
     cost = static_cast<float>((most + parts - 1) / parts);
-    if (parts >= kPagedSpreadParts) cost += parts >= 16 ? kSpreadCut : kSpreadCut + kSpreadSlice * static_cast<float>((8 + parts - 1) / parts);
+    if (parts >= kPagedSpreadParts)
+      cost += kSpreadCut + kSpreadPart * static_cast<float>(parts) + (parts < 16 ? static_cast<float>((8 + parts - 1) / parts) : 0.f);
     else if (parts > 1) cost += cut + join * static_cast<float>(parts - 1);
   }
   float best = cost;
