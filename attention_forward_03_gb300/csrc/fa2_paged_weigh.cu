@@ -564,6 +564,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key = u.unit * kUnitKeys + t * kKeys + key_lane;
       return key < u.s.length ? paged_entry(p, u.b, key) : -1;
     };
+    // Of the warpgroup's threads. All of its warps wait: a share can meet twice (a cut
+    // unit's tail, then the next unit's head), and the arrivals of a warp that went on
+    // would stand for those of one that has yet to store its sums.
+    auto meet = [&]() {
+      mbar_arrive(bar_flag);
+      const bool met = wait_bounded(bar_flag, flag_ph, wd, kSiteWeighPart);
+      flag_ph ^= 1u;
+      return __all_sync(0xffffffffu, met) != 0;
+    };
     WeighCursor cur = weigh_cursor(p, *start);
     WeighSegment u;
     bool ok = true;
@@ -739,14 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __stcg(ws, sum0);
         __stcg(ws + kKeys, sum1);
         __threadfence();
-        mbar_arrive(bar_flag);
-        if (key_lane < 32) {
-          bool done = wait_bounded(bar_flag, flag_ph, wd, kSiteWeighPart);
-          done = __all_sync(0xffffffffu, done);
-          if (!done) break;
-          if (lane == 0) store_release(p.ws_flags + blockIdx.x, p.epoch);
-        }
-        flag_ph ^= 1u;
+        if (!meet()) break;
+        if (key_lane == 0) store_release(p.ws_flags + blockIdx.x, p.epoch);
         continue;
       }
       if (u.end < u.blocks) {  // others hold the rest: this is the share's last segment
@@ -766,14 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every thread has seen the flags: taken back, so that a replay of a captured
         // launch, which carries the same tag, does not find them
-        mbar_arrive(bar_flag);
-        if (key_lane < 32) {
-          bool seen = wait_bounded(bar_flag, flag_ph, wd, kSiteWeighPart);
-          seen = __all_sync(0xffffffffu, seen);
-          if (!seen) break;
-          for (int cb = blockIdx.x + 1 + lane; cb <= last; cb += 32) p.ws_flags[cb] = 0ull;
-        }
-        flag_ph ^= 1u;
+        if (!meet()) break;
+        for (int cb = blockIdx.x + 1 + key_lane; cb <= last; cb += 128) p.ws_flags[cb] = 0ull;
       }
       auto place = [&](int page, int k) {
         return ((static_cast<long long>(page) * p.heads + u.head) << p.page_shift) + (k & ((1 << p.page_shift) - 1));
