@@ -453,6 +453,9 @@ extern "C" int fa2_paged_evict(void* k_cache, void* v_cache, float* weights, con
                         {weights, static_cast<size_t>(pages) * Hkv * page_size * 4}, {block_table, old_bytes},
                         {new_table, new_bytes}, {key_lengths, static_cast<size_t>(B) * 4}};
   if (any_overlap(outs, 2, ins, 6)) return FA2_ERR_INVALID_ARG;
+  // the caches (which may interleave) and the weights are written too
+  for (int i = 0; i < 3; ++i)
+    if (any_overlap(ins + i, 1, ins + std::max(i + 1, 2), 6 - std::max(i + 1, 2))) return FA2_ERR_INVALID_ARG;
   // pages are written while others are read
   if (keep > 0 && new_table == block_table) return FA2_ERR_INVALID_ARG;
   int sms = 0;

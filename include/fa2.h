@@ -670,6 +670,9 @@ FA2_API int fa2_paged_key_weights_workspace_bytes(size_t* bytes);
  *             the kept positions, ascending, and -1 behind them.
  * strides   : k_cache page, head, slot; v_cache page, head, slot; block_table
  *             row; new_table row (8).
+ * The caches (which may interleave) overlap neither the weights nor a table or
+ * the lengths, from a cache's first element to its last; nothing overlaps an
+ * output or the weights.
  * 0 <= recent <= keep <= new_max_pages * page_size. A position whose page
  * number is not one counts as the least weight and is copied as zeros.
  */
