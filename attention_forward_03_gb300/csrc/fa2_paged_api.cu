@@ -220,6 +220,7 @@ extern "C" int fa2_paged_append(const void* K, const void* V, void* k_cache, voi
                          {weights, static_cast<size_t>(pages) * Hkv * page_size * 4}};
   for (const Range& o : outs)  // the two caches may interleave
     if (any_overlap(&o, 1, ins, 5)) return FA2_ERR_INVALID_ARG;
+  if (any_overlap(outs + 2, 1, outs, 2)) return FA2_ERR_INVALID_ARG;
   int sms = 0;
   int* status = nullptr;
   rc = current_device_facts(&sms, &status);

@@ -566,6 +566,7 @@ FA2_API int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk
  *             they and the tables overlap neither cache.
  * weights   : device pointer, contiguous [pages, Hkv, page_size] fp32, or NULL:
  *             the written positions' weights (fa2_paged_key_weights) become 0.
+ *             They overlap nothing.
  * strides   : K token, head; V token, head; k_cache page, head, slot; v_cache
  *             page, head, slot; block_table row (11).
  * Tokens without a position and those whose page number is not one are not

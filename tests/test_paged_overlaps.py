@@ -17,3 +17,12 @@ EVICT = [
 @pytest.mark.parametrize("over", EVICT, ids=str)
 def test_evict(lib, over):  # noqa: F811
     assert call(lib, "evict", **over) == INVALID
+
+
+# the weights beside the caches that the same call writes
+APPEND = [dict(w=3 * A), dict(w=3 * A + 4096), dict(w=4 * A + 64), dict(w=4 * A - 64), dict(w=11 * A, kc=11 * A + 1024)]
+
+
+@pytest.mark.parametrize("over", APPEND, ids=str)
+def test_append(lib, over):  # noqa: F811
+    assert call(lib, "append", **over) == INVALID
