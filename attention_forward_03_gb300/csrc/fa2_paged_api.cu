@@ -431,6 +431,7 @@ extern "C" int fa2_paged_evict(void* k_cache, void* v_cache, float* weights, con
   if (rc != FA2_OK) return rc;
   if (keep < 0 || recent < 0 || recent > keep || new_max_pages < 0) return FA2_ERR_INVALID_ARG;
   if (static_cast<int64_t>(new_max_pages) * page_size < keep) return FA2_ERR_INVALID_ARG;
+  if (keep > (1 << 30)) return FA2_ERR_INVALID_ARG;  // as positions: an index plus a block's step stays inside 32 bits
   if (static_cast<int64_t>(B) * Hkv * std::max(keep, 1) > (1ll << 40)) return FA2_ERR_INVALID_ARG;
   if (B == 0) return FA2_OK;
   if (Hkv == 0 || pages == 0 || max_pages == 0) return FA2_ERR_INVALID_ARG;

@@ -674,8 +674,9 @@ FA2_API int fa2_paged_key_weights_workspace_bytes(size_t* bytes);
  * The caches (which may interleave) overlap neither the weights nor a table or
  * the lengths, from a cache's first element to its last; nothing overlaps an
  * output or the weights.
- * 0 <= recent <= keep <= new_max_pages * page_size. A position whose page
- * number is not one counts as the least weight and is copied as zeros.
+ * 0 <= recent <= keep <= new_max_pages * page_size, keep at most 2^30. A
+ * position whose page number is not one counts as the least weight and is
+ * copied as zeros.
  */
 FA2_API int fa2_paged_evict(void* k_cache, void* v_cache, float* weights, const int* block_table,
                             const int* key_lengths, const int* new_table, int* new_lengths, int* kept,
