@@ -80,8 +80,9 @@ int check_sizes(const Sizes& z) {
   if (z.dtype != FA2_F16 && z.dtype != FA2_BF16) return FA2_ERR_UNSUPPORTED;
   if (z.page_size < 16 || z.page_size > (1 << kMaxPageShift) || (z.page_size & (z.page_size - 1)))
     return FA2_ERR_UNSUPPORTED;
-  // 2^30: a position, token or row index plus a tile stays inside 32 bits
-  if (static_cast<int64_t>(z.max_pages) * z.page_size > (1 << 30) || z.T > (1 << 30)) return FA2_ERR_INVALID_ARG;
+  // 2^30: a position, token, row or sequence index plus a tile or a warp's step stays inside 32 bits
+  if (static_cast<int64_t>(z.max_pages) * z.page_size > (1 << 30) || z.T > (1 << 30) || z.B > (1 << 30))
+    return FA2_ERR_INVALID_ARG;
   if (static_cast<int64_t>(z.B) * z.Hkv > INT32_MAX) return FA2_ERR_INVALID_ARG;
   return FA2_OK;
 }
