@@ -83,7 +83,8 @@ int check_sizes(const Sizes& z) {
   // 2^30: a position, token, row or sequence index plus a tile or a warp's step stays inside 32 bits
   if (static_cast<int64_t>(z.max_pages) * z.page_size > (1 << 30) || z.T > (1 << 30) || z.B > (1 << 30))
     return FA2_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(z.B) * z.Hkv > INT32_MAX) return FA2_ERR_INVALID_ARG;
+  // 2^24: the rows of up to 128 tokens (a block of key weights) are counted in 32 bits over all heads
+  if (static_cast<int64_t>(z.B) * z.Hkv > INT32_MAX || z.Hkv > (1 << 24)) return FA2_ERR_INVALID_ARG;
   return FA2_OK;
 }
 

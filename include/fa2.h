@@ -551,7 +551,8 @@ FA2_API int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk
  *             tables': any), not negative, those of the caches and of Q
  *             positive and below 2^39; no view reaches further than 2^44 elements.
  * T, B, Hq, Hkv: sizes >= 0, Hq a multiple of Hkv.
- *             max_pages * page_size, T, B and T * Hq / Hkv are at most 2^30.
+ *             max_pages * page_size, T, B and T * Hq / Hkv are at most 2^30,
+ *             Hkv at most 2^24, B * Hkv below 2^31.
  * D         : 32, 64, 96 or 128.
  * scale, dtype, stream: as fa2_fwd.
  * The tables, lengths and starts do not change while a call runs; what they
