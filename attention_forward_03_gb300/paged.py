@@ -185,7 +185,8 @@ def paged_attention_forward(q, k_cache, v_cache, block_table, key_lengths, query
     that see its positions NaN.
     q: a view with any strides, the head dim contiguous.
     max_query_length: the most new tokens that a sequence has, where the caller
-    knows (the call chooses its kernels by it; a wrong one costs time only).
+    knows (the call chooses its kernels by it: a wrong one costs time, and O
+    and LSE may differ in their last bits).
     out, lse: caller-owned outputs. workspace: a uint8 CUDA tensor of at least
     fa2_paged_fwd_workspace_bytes(D) bytes (by default one is kept for each
     device, head dim, current stream and host thread; a captured call, and one

@@ -597,8 +597,9 @@ FA2_API int fa2_paged_append(const void* K, const void* V, void* k_cache, void* 
  * strides   : Q token, head; k_cache page, head, slot; v_cache page, head,
  *             slot; block_table row (9).
  * max_query_length: the most new tokens that a sequence has, or any larger
- *             number (T). Kernels are chosen by it; the results do not depend
- *             on its being right.
+ *             number (T). Kernels are chosen by it: the results are right to
+ *             the same bounds whatever it is (a wrong one costs time), but
+ *             only the same number gives the same bits again.
  * workspace : device memory of at least fa2_paged_fwd_workspace_bytes(D)
  *             bytes, 16-byte aligned; scratch, needs no initialisation, not
  *             shared by calls that run at the same time. A captured call can
