@@ -248,7 +248,9 @@ def paged_key_weights(q, lse, k_cache, block_table, key_lengths, query_starts=No
     size]; weights=None stands for zeros. out may be `weights` itself, and is
     where it is not given (without either, a new tensor of zeros). Every
     position of every sequence is written, nothing else is; two sequences share
-    no position. The sums have a fixed order.
+    no position. The sums have a fixed order. A row whose lse is NaN (it sees a
+    page number outside the cache, say) makes all that it sees NaN, and
+    paged_cache_evict keeps these first.
     max_query_length: as for paged_attention_forward. workspace: a uint8 CUDA
     tensor of at least fa2_paged_key_weights_workspace_bytes() bytes (kept by
     default, as paged_attention_forward's is).
@@ -312,8 +314,8 @@ def paged_cache_evict(k_cache, v_cache, weights, block_table, key_lengths, new_t
     keeps all. Their keys, values and weights are copied in order to the
     positions 0, 1, ... of the pages in new_table [B, pages] int32 (room for
     `keep` positions; none of them may be a page that a sequence still has
-    positions in). The old pages keep what they hold and may be given away
-    once the call has run.
+    positions in, nor occur twice). The old pages keep what they hold and may
+    be given away once the call has run.
     new_lengths: int32 [B], min(key_lengths, keep), the lengths for the calls
     that follow with new_table. kept: int32 [B, Hkv, keep], the positions that
     were kept, ascending, -1 behind them. A position whose page number is not

@@ -571,7 +571,7 @@ FA2_API int fa2_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk
  * strides   : K token, head; V token, head; k_cache page, head, slot; v_cache
  *             page, head, slot; block_table row (11).
  * Tokens without a position and those whose page number is not one are not
- * written. No two tokens have one position.
+ * written (none, where there are no pages). No two tokens have one position.
  */
 FA2_API int fa2_paged_append(const void* K, const void* V, void* k_cache, void* v_cache, float* weights,
                              const int* block_table, const int* key_lengths, const int* query_starts,
@@ -635,7 +635,10 @@ FA2_API int fa2_paged_fwd_workspace_bytes(int D, size_t* bytes);
  *             overlaps nothing. Every position of every sequence is written
  *             (also of one without new tokens), those whose page number is not
  *             one aside; no two sequences share one. Sums are fp32, in a fixed
- *             order.
+ *             order. A row whose LSE is NaN (it has a NaN score, or sees a
+ *             position whose page number is not one) makes the weights of all
+ *             the positions that it sees NaN, which fa2_paged_evict keeps
+ *             before any others.
  * strides   : Q token, head; k_cache page, head, slot; block_table row (6).
  * max_query_length: as for fa2_paged_fwd.
  * workspace : as for fa2_paged_fwd, at least
@@ -666,8 +669,9 @@ FA2_API int fa2_paged_key_weights_workspace_bytes(size_t* bytes);
  * new_table : device pointer, [B, new_max_pages] int32: the pages that the kept
  *             keys, values and weights are copied to, in order, from position 0
  *             on. None is a page that a sequence has positions in (pages are
- *             read and written at once), and it is another table than
- *             block_table. An entry outside [0, pages) is not written to.
+ *             read and written at once), nor the page of another entry; the
+ *             table is another than block_table. An entry outside [0, pages)
+ *             is not written to.
  * new_lengths: device pointer, [B] int32, overwritten with min(length, keep).
  * kept      : device pointer, contiguous [B, Hkv, keep] int32, overwritten with
  *             the kept positions, ascending, and -1 behind them.
@@ -676,6 +680,7 @@ FA2_API int fa2_paged_key_weights_workspace_bytes(size_t* bytes);
  * The caches (which may interleave) overlap neither the weights nor a table or
  * the lengths, from a cache's first element to its last; nothing overlaps an
  * output or the weights.
+ * Hkv, pages and max_pages are at least 1 where there is a sequence, and
  * 0 <= recent <= keep <= new_max_pages * page_size, keep at most 2^30. A
  * position whose page number is not one counts as the least weight and is
  * copied as zeros.
