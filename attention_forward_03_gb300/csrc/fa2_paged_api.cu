@@ -300,7 +300,7 @@ extern "C" int fa2_paged_fwd(const void* Q, const void* k_cache, const void* v_c
   // positions; D = 128, 16 blocks: 11.2 / 10.2, 14.3 / 15.5, 15.3 / 18.4, 25.9 / 26.6;
   // 32 blocks: 12.3 / 10.4, 14.4 / 15.5, 19.9 / 18.6, 39.6 / 26.7; D = 64, 24 blocks:
   // 9.3 / 9.5, 10.8 / 14.6, 13.8 / 16.2, 25.6 / 22.4; 48 blocks: 10.0 / 9.4, 11.8 / 14.5,
-  // 17.2 / 16.2, 40.2 / 22.3). The host does not know the positions.
+  // 17.2 / 16.2, 40.2 / 22.3). Of the positions the host knows the table's width alone.
   const int longest = query_starts ? std::min(T, max_query_length) : p.each;
   const int64_t most = static_cast<int64_t>(longest) * group;
   const int64_t blocks = std::min(static_cast<int64_t>(B) * ((most + kPagedRows - 1) / kPagedRows),

@@ -144,6 +144,9 @@ struct Moves {
 // One block for each key head of a sequence. What bounds it is latency: the
 // rounds over the positions and the three scans of the counts (64 heads of 8192
 // positions: 12 us; digits of 8 bits, each position counted by itself: 4 more).
+// Of more than kSelectKeys positions every pass reads the table and the weights
+// again (8 key heads of one sequence cut to 2048, with the move: of 49,152 positions
+// 49 us, of 65,536 126, of 131,072 239).
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectKeys = 49152;  // bits of so many positions are kept in shared memory

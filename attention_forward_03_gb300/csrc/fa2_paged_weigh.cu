@@ -32,10 +32,14 @@
 // overlapped with another's: 1.45 us a step; so 0.85).
 // Measured, 8 key heads of 128 with 4 query heads each: single tokens of 64
 // sequences of up to 4096 positions 51 us (floor 41.5, the bytes of K); 512
-// tokens over 8192 positions 37 us (floor 16.9), 5 of them the start, the rest
-// steps of 256 keys x 128 rows, two in 1.55 us: the exponentials take 0.54 of each,
-// the rows' factors out of shared memory 0.27 (0.54, and 41 us in all, with one tile
-// after the other, whose buffers are filled again earlier), the products 0.56.
+// tokens over 8192 positions 37 us (floor 16.9). Of these a CTA has no scores for
+// 7 (its share 3, the first instructions 1, the first loads and product 3), then
+// 26.5 steps of 256 keys x 128 rows, two in 1.55 to 1.7 us, 22 in all; 1 goes
+// where the unit changes, 2 into sums that are left to others or joined; and the
+// last CTA ends 2.5 after the mean (time stamps in every warpgroup). Of a step
+// the exponentials take 0.54, the rows' factors out of shared memory 0.27 (0.54, and
+// 41 us in all, with one tile after the other, whose buffers are filled again
+// earlier), the products 0.56.
 // A unit's sums of the warpgroup that did not take its last step go through
 // shared memory to the other, which writes.
 #include <cuda_runtime.h>
